@@ -454,6 +454,99 @@ moe_status_t moe_nvfp4_w4a4_forward(const moe_nvfp4_layer_t* layer, const uint16
                                     float act_gscale_x, float act_gscale_h, uint16_t* out, void* workspace,
                                     size_t workspace_bytes, const moe_forward_aux_t* aux, void* stream);
 
+/* ---------------------------------------------------------------- paged NVFP4 key/value cache
+ * The attention half of a decoder block in the same 4-bit format: keys and values as E2M1 elements,
+ * one E4M3FN scale per 16 elements along the head dimension and one fp32 dequant global scale each
+ * for keys and values -- 0.5625 bytes per element against 2 in bf16.
+ * Source: the NVFP4 KV cache ("packed FP4 + per-block FP8 scales", 0.5625 B per element) and the
+ * kernel that gathers and dequantizes its rows ("Qwen3.8-Flash-Next-NVFP4", the NVFP4 KV section).
+ *
+ * Pages hold page_size consecutive positions of one request; a request's positions [j*page_size,
+ * (j+1)*page_size) live in page block_table[r][j].  Slot = page * page_size + position % page_size.
+ *
+ * Page layout: pages is [num_pages][kv_heads][page_size / 32] units of 36*D bytes, D = head_dim, each
+ * 32 consecutive positions of one head, in the operand order of the matrix instructions.  With
+ * position p = 16b + n = 16h + 4q + i of the unit (b, h in 0..1; n in 0..15; q, i in 0..3), element
+ * d, and NS = D / 32:
+ *   bytes [0, 16D)     key codes:  s = d / 32, u = (d % 32) / 8, w = b*NS + s: byte
+ *                      1024*(w / 4) + 16*(16u + n) + 4*(w % 4) + (d % 8) / 2, even d in the low nibble
+ *   bytes [16D, 32D)   value codes: R = d / 32, m = (d % 32) / 2: byte
+ *                      1024*(R / 2) + 16*(16q + m) + 8*(R % 2) + 4h + i, even d in the low nibble
+ *   bytes [32D, 34D)   key scales of group g = d / 16 = 2s + z: byte (16z + n)*2*NS + b*NS + s
+ *   bytes [34D, 36D)   value scales of group g = 2R + z: byte ((2q + z)*NS + R)*8 + 4h + i
+ *
+ * Limits: D in {64, 128, 256}; page_size a multiple of 32, at most 65536; num_pages * page_size <
+ * 2^31; 1 <= kv_heads <= 1024; global scales within [2^-64, 2^64] (all intermediate fp32 values stay
+ * normal); scale bytes that the caller writes into pages itself must not be NaN (0x7F, 0xFF). */
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;   /* positions per page */
+  int32_t kv_heads;    /* Hkv */
+  int32_t head_dim;    /* D */
+  float k_gscale;      /* dequant global scales (host values) */
+  float v_gscale;
+  uint8_t* pages;      /* device */
+} moe_nvfp4_kv_cache_t;
+
+/* Bytes of the pages of a cache; 0 for sizes outside the limits (host). */
+size_t moe_nvfp4_kv_cache_bytes(int32_t num_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim);
+
+/* Block table entries, slots and offsets of one step, from the request lengths.
+ * kv_lens [R]: positions each request holds already; new_lens [R]: tokens it adds (0: idle; negative
+ * lengths count as 0).  Token t of the step belongs to request r when query_offsets[r] <= t <
+ * query_offsets[r+1] and has position kv_lens[r] + t - query_offsets[r].  Pages that a request opens
+ * are taken from free_pages [num_free] in order, request by request, and entered into
+ * block_table [R][table_width] (in place: entries of the pages it holds are read, all others are left).
+ * Writes query_offsets [R+1] (exclusive prefix sum of new_lens), seq_lens [R] (kv_lens + new_lens),
+ * positions [T] and slots [T] (T = num_tokens, the rows of the step's tensors; past the last token
+ * position 0 and slot -1) and pages_used [1] (free pages the step needs).
+ * Shortage and bad entries are reported, never written past: a token whose page lies beyond the free
+ * list (pages_used > num_free), beyond the table width, or outside [0, num_pages) gets slot -1
+ * (moe_nvfp4_kv_append skips it) and a block table entry it would have opened becomes -1; tokens
+ * beyond num_tokens get no row (query_offsets[R] > T).  Sums past 2^31 - 1 are stored as 2^31 - 1.
+ * Limits: 0 <= R <= 4096; table_width * R < 2^31; page_size a positive multiple of 32.  Outputs must not
+ * overlap inputs.  num_tokens = 0 still writes offsets, seq_lens and pages_used. */
+moe_status_t moe_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int32_t R, int32_t page_size,
+                         int32_t num_pages, const int32_t* free_pages, int32_t num_free, int32_t* block_table,
+                         int32_t table_width, int32_t num_tokens, int32_t* query_offsets, int32_t* seq_lens,
+                         int32_t* positions, int32_t* slots, int32_t* pages_used, void* stream);
+
+/* Quantizes T rows of keys and values [T][Hkv][D] bf16 into the cache at slots [T] (codes and scales by
+ * the rule of moe_nvfp4_quantize_act with k_gscale / v_gscale).  k_stride, v_stride: elements from one
+ * token's row to the next (at least Hkv*D, multiples of 8; heads are contiguous).  A slot outside
+ * [0, num_pages * page_size) is skipped.  Slots of one call must be distinct.  The cache holds finite
+ * values only: infinities saturate, a NaN is stored as the largest code of its group. */
+moe_status_t moe_nvfp4_kv_append(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* k, const uint16_t* v,
+                                 int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T, void* stream);
+
+/* Dequantizes the rows at slots [n] (any order, repeats allowed): k, v [n][Hkv][D] bf16 of
+ * e2m1 * e4m3 * global scale (one fp32 product, rounded to bf16).  A slot outside the cache gives a
+ * NaN row. */
+moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, const int32_t* slots, int32_t n,
+                                 uint16_t* k, uint16_t* v, void* stream);
+
+/* Attention of the step's query rows over the cache.  q [T][Hq][D] bf16 with q_stride elements from
+ * token to token (at least Hq*D, a multiple of 8); Hq a multiple of kv_heads, head h reads kv head
+ * h / (Hq / kv_heads).  Rows [query_offsets[r], query_offsets[r+1]) belong to request r, whose cache
+ * holds seq_lens[r] positions, the rows' own included (append first): row i of n has position
+ * seq_lens[r] - n + i and sees the positions j <= its own, and with window > 0 only j > position -
+ * window.  out [T][Hq][D] bf16 = softmax(scale * q.k) v over the positions seen; lse [T][Hq] fp32 (or
+ * NULL) the natural logarithm of the sum of exponentials.  A row that sees nothing gets zeros and
+ * lse = -inf.  Rows outside every request are left as they were.  A row that sees a position whose
+ * block table entry is outside [0, num_pages), or beyond the table, becomes NaN.
+ * Products are exact (q re-encoded as fp16 under a power of two per row, keys and values as fp16) and
+ * sums fp32; the probabilities are rounded to fp16 (11 bits) for the value product only.
+ * Deterministic; a row's result depends on the other requests of the call only through the order in
+ * which its partial sums are added.
+ * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; scale finite and positive; window >= 0.
+ * workspace: moe_nvfp4_kv_attention_workspace_size bytes, 16-byte aligned. */
+size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);
+moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q, int64_t q_stride,
+                                    int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens,
+                                    int32_t R, const int32_t* block_table, int32_t table_width, float scale,
+                                    int32_t window, uint16_t* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- measurement helper
  * Not a step of the layer: reads `bytes` bytes of device memory at `buf` once with a plain
  * streaming-read kernel (16-byte non-temporal loads, at most `workgroups` workgroups of 256 threads

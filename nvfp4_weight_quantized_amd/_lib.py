@@ -24,6 +24,7 @@ MOE_GEMM_DOWN = 1
 
 c_void_p = ctypes.c_void_p
 i32 = ctypes.c_int32
+i64 = ctypes.c_int64
 u32 = ctypes.c_uint32
 size_t = ctypes.c_size_t
 
@@ -51,6 +52,12 @@ class ForwardAux(ctypes.Structure):
     """moe_forward_aux_t"""
     _fields_ = [("logits", c_void_p), ("topk_ids", c_void_p), ("topk_w", c_void_p), ("expert_counts", c_void_p),
                 ("stage_events", ctypes.POINTER(c_void_p)), ("y_rows", c_void_p), ("flags", u32)]
+
+
+class KvCache(ctypes.Structure):
+    """moe_nvfp4_kv_cache_t"""
+    _fields_ = [("num_pages", i32), ("page_size", i32), ("kv_heads", i32), ("head_dim", i32),
+                ("k_gscale", ctypes.c_float), ("v_gscale", ctypes.c_float), ("pages", c_void_p)]
 
 
 MOE_FORWARD_FUSED_DECODE = 1
@@ -99,6 +106,15 @@ SIGNATURES = {
     "moe_nvfp4_h16_bound": (i32, [ctypes.POINTER(Experts), c_void_p, c_void_p]),
     "moe_nvfp4_forward_noalloc": (i32, [ctypes.POINTER(Layer), c_void_p, i32, c_void_p, ctypes.POINTER(ForwardAux),
                                         c_void_p]),
+    "moe_nvfp4_kv_cache_bytes": (size_t, [i32, i32, i32, i32]),
+    "moe_kv_plan": (i32, [c_void_p, c_void_p, i32, i32, i32, c_void_p, i32, c_void_p, i32, i32, c_void_p, c_void_p,
+                          c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_nvfp4_kv_append": (i32, [ctypes.POINTER(KvCache), c_void_p, c_void_p, i64, i64, c_void_p, i32, c_void_p]),
+    "moe_nvfp4_kv_gather": (i32, [ctypes.POINTER(KvCache), c_void_p, i32, c_void_p, c_void_p, c_void_p]),
+    "moe_nvfp4_kv_attention_workspace_size": (size_t, [i32, i32, i32, i32, i32]),
+    "moe_nvfp4_kv_attention": (i32, [ctypes.POINTER(KvCache), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32,
+                                     c_void_p, i32, ctypes.c_float, i32, c_void_p, c_void_p, c_void_p, size_t,
+                                     c_void_p]),
 }
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES

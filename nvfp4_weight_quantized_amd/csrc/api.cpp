@@ -10,17 +10,10 @@
 
 #include "common.h"
 
-namespace {
-
-using moe::GemmBank;
-using moe::GemmProblem;
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+namespace moe {
 
 // gfx950 check, cached per device (the value never changes for a device).
-int g_arch_ok[64];  // 0 unknown, 1 ok, 2 not gfx950
+static int g_arch_ok[64];  // 0 unknown, 1 ok, 2 not gfx950
 
 moe_status_t check_arch(const char* arch) {
   if (arch) return std::strncmp(arch, "gfx950", 6) == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
@@ -34,8 +27,18 @@ moe_status_t check_arch(const char* arch) {
   return ok ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
 }
 
-// The kernels move weights, activations and outputs with 16-byte vector accesses.
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+}  // namespace moe
+
+namespace {
+
+using moe::al16;
+using moe::check_arch;
+using moe::GemmBank;
+using moe::GemmProblem;
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 bool valid_bank(const moe_nvfp4_experts_t& b, int32_t H, int32_t expected_experts) {
   if (b.num_experts != expected_experts || b.hidden != H) return false;

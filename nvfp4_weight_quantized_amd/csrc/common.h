@@ -53,6 +53,12 @@ inline moe_status_t launch_status() {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
+// MOE_OK if `arch` (NULL: the current device's, cached) is gfx950.  Defined in api.cpp.
+moe_status_t check_arch(const char* arch);
+
+// The kernels move weights, activations and outputs with 16-byte vector accesses.
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // Permute -----------------------------------------------------------------------------------
 constexpr int kPermuteChunk = 2048;     // slots per workgroup of the multi-block path
 constexpr int kPermuteThreads = 512;    // 8 waves
@@ -268,5 +274,36 @@ moe_status_t launch_quantize_act_mx(const uint16_t* a, int64_t rows, int32_t col
 // may alias a.
 moe_status_t launch_quantize_act_nv(const uint16_t* a, int64_t rows, int32_t cols, float d, uint8_t* packed,
                                     uint8_t* scales, uint16_t* values, hipStream_t stream);
+
+// Paged NVFP4 key/value cache ------------------------------------------------------------------
+constexpr int kKvMaxRequests = 4096;
+constexpr int kKvUnit = 32;   // positions per unit of a page (36 * head_dim bytes)
+
+moe_status_t launch_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int32_t R, int32_t page_size,
+                            int32_t num_pages, const int32_t* free_pages, int32_t num_free, int32_t* block_table,
+                            int32_t table_width, int32_t num_tokens, int32_t* query_offsets, int32_t* seq_lens,
+                            int32_t* positions, int32_t* slots, int32_t* pages_used, hipStream_t stream);
+moe_status_t launch_kv_append(const moe_nvfp4_kv_cache_t& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                              int64_t v_stride, const int32_t* slots, int32_t T, hipStream_t stream);
+moe_status_t launch_kv_gather(const moe_nvfp4_kv_cache_t& c, const int32_t* slots, int32_t n, uint16_t* k,
+                              uint16_t* v, hipStream_t stream);
+
+struct KvAttentionProblem {
+  moe_nvfp4_kv_cache_t cache;
+  const uint16_t* q;        // [T][Hq][D], q_stride elements per token
+  int64_t q_stride;
+  int32_t T, Hq, G;         // G = Hq / kv_heads
+  const int32_t* offsets;   // [R + 1]
+  const int32_t* lens;      // [R]
+  int32_t R;
+  const int32_t* table;     // [R][width]
+  int32_t width;
+  float scale;              // softmax scale times the keys' global scale
+  int32_t window;           // 0: none
+  uint16_t* out;            // [T][Hq][D]
+  float* lse;               // [T][Hq] or NULL
+};
+size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);
+moe_status_t launch_kv_attention(const KvAttentionProblem& p, void* workspace, hipStream_t stream);
 
 }  // namespace moe

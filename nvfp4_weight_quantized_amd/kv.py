@@ -1,0 +1,248 @@
+"""torch-facing wrappers of the paged NVFP4 key/value cache: argument checks and marshalling only.
+
+One decode or prefill step of an attention layer, on tensors of one GPU:
+
+    plan = kv_plan(kv_lens, new_lens, block_table, free_pages, page_size, num_pages, num_tokens)
+    kv_append(cache, k, v, plan.slots)                       # per layer: quantize the new rows
+    out = kv_attention(cache, q, plan.query_offsets, plan.seq_lens, block_table)
+
+The plan holds for every layer of the step (all layers share the block table).  Every call only
+enqueues kernels on the current stream of its tensors' device and can be captured in a HIP graph.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib as L
+from .ops import _need, _same_device, _shape
+
+_UNIT = 32              # positions per unit of a page
+HEAD_DIMS = (64, 128, 256)
+
+
+def _on(dev: torch.device):
+    """The context in which a launch goes to ``dev`` (nothing to do on the current device)."""
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _raw_stream(dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+class NvFp4KvCache:
+    """Pages of keys and values in NVFP4 (layout: include/moe_nvfp4.h), one attention layer's.
+
+    ``pages`` uint8 [num_pages, kv_heads, page_size / 32, 36 * head_dim], contiguous; ``page_size``
+    positions per page (a multiple of 32); ``k_gscale`` and ``v_gscale`` the dequant global scales
+    (a cached element is e2m1 * e4m3 * gscale).  The content of new pages does not matter: positions
+    past a request's length are never used.
+    """
+    __slots__ = ("pages", "page_size", "k_gscale", "v_gscale", "_struct")
+
+    def __init__(self, pages: torch.Tensor, page_size: int, k_gscale: float = 1.0, v_gscale: float = 1.0):
+        _need(pages, "pages", torch.uint8, 4)
+        p, h, u, b = pages.shape
+        if b % 36 or b // 36 not in HEAD_DIMS:
+            raise ValueError(f"pages: last dimension {b}, expected 36 * head_dim with head_dim in {HEAD_DIMS}")
+        if page_size % _UNIT or page_size != u * _UNIT:
+            raise ValueError(f"pages: {u} units of {_UNIT} positions do not make a page of {page_size}")
+        if L.lib().moe_nvfp4_kv_cache_bytes(p, page_size, h, b // 36) == 0:
+            raise ValueError(f"pages: sizes {tuple(pages.shape)} outside the cache's limits")
+        for name, d in (("k_gscale", k_gscale), ("v_gscale", v_gscale)):
+            if not 2.0 ** -64 <= d <= 2.0 ** 64:      # also refuses NaN
+                raise ValueError(f"{name}: a dequant global scale lies in [2^-64, 2^64], got {d!r}")
+        self.pages, self.page_size, self.k_gscale, self.v_gscale = pages, page_size, float(k_gscale), float(v_gscale)
+        self._struct = L.KvCache(p, page_size, h, b // 36, k_gscale, v_gscale, pages.data_ptr())
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_gscale: float = 1.0,
+                 v_gscale: float = 1.0, device="cuda") -> "NvFp4KvCache":
+        """A cache of ``num_pages`` new pages."""
+        if head_dim not in HEAD_DIMS or page_size <= 0 or page_size % _UNIT:
+            raise ValueError(f"head_dim in {HEAD_DIMS} and page_size a multiple of {_UNIT} expected")
+        return cls(torch.zeros(num_pages, kv_heads, page_size // _UNIT, 36 * head_dim, dtype=torch.uint8,
+                               device=device), page_size, k_gscale, v_gscale)
+
+    @property
+    def num_pages(self) -> int:
+        return self._struct.num_pages
+
+    @property
+    def kv_heads(self) -> int:
+        return self._struct.kv_heads
+
+    @property
+    def head_dim(self) -> int:
+        return self._struct.head_dim
+
+
+class KvPlan(NamedTuple):
+    """One step's index tensors (int32): offsets [R+1], lengths after the step [R], positions and slots
+    [num_tokens] (0 and -1 past the last token), and the number of free pages the step takes [1]."""
+    query_offsets: torch.Tensor
+    seq_lens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    pages_used: torch.Tensor
+
+
+def kv_plan(kv_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+            page_size: int, num_pages: int, num_tokens: int) -> KvPlan:
+    """Plan a step: requests hold ``kv_lens`` positions and add ``new_lens`` tokens (int32 [R]).
+
+    Pages that open are taken from ``free_pages`` (int32) in order and entered into ``block_table``
+    (int32 [R, width], in place).  ``num_tokens`` is the row count of the step's tensors; it may exceed
+    the sum of ``new_lens`` (a padded batch).  A shortage shows in ``pages_used`` > len(free_pages) and
+    in slots of -1, which the append skips.
+    """
+    _need(kv_lens, "kv_lens", torch.int32, 1)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(free_pages, "free_pages", torch.int32, 1)
+    r = kv_lens.shape[0]
+    _shape(new_lens, "new_lens", (r,))
+    if block_table.shape[0] != r:
+        raise ValueError(f"block_table: {block_table.shape[0]} rows for {r} requests")
+    _same_device(kv_lens, ("new_lens", new_lens), ("block_table", block_table), ("free_pages", free_pages))
+    dev = kv_lens.device
+    # one allocation for the outputs
+    sizes = (r + 1, r, num_tokens, num_tokens, 1)
+    if num_tokens < 0:
+        raise ValueError(f"num_tokens {num_tokens}")
+    plan = KvPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+    with _on(dev):
+        L.check("moe_kv_plan", L.lib().moe_kv_plan(
+            kv_lens.data_ptr(), new_lens.data_ptr(), r, page_size, num_pages, free_pages.data_ptr(),
+            free_pages.shape[0], block_table.data_ptr(), block_table.shape[1], num_tokens,
+            plan.query_offsets.data_ptr(), plan.seq_lens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
+            plan.pages_used.data_ptr(), _raw_stream(dev)))
+    return plan
+
+
+def _rows(t: torch.Tensor, name: str, dim: int, dev: torch.device) -> None:
+    """Token rows [T, heads, dim] bf16: heads contiguous, any token stride of a multiple of 8 elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected a bfloat16 tensor")
+    if t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected [tokens, heads, {dim}], got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if t.shape[0] == 0:
+        return
+    s = t.stride()
+    if s[2] != 1 or (t.shape[1] > 1 and s[1] != dim):
+        raise ValueError(f"{name}: heads must be contiguous, got strides {s}")
+    if t.shape[0] > 1 and (s[0] < t.shape[1] * dim or s[0] % 8):
+        raise ValueError(f"{name}: token stride {s[0]}, expected a multiple of 8 of at least {t.shape[1] * dim}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must start at 16-byte boundaries")
+
+
+def _slots(slots: torch.Tensor, dev: torch.device) -> int:
+    _need(slots, "slots", torch.int32, 1)
+    if slots.device != dev:
+        raise ValueError(f"slots: on {slots.device}, expected {dev}")
+    return slots.shape[0]
+
+
+def kv_append(cache: NvFp4KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize rows k, v (bf16 [T, kv_heads, head_dim]) into the cache at ``slots`` (int32 [T]).
+
+    Slots outside the cache (-1: a padded row) are skipped; slots of one call must be distinct.  k and v
+    may be slices of a fused projection's output (contiguous heads, any token stride that is a multiple
+    of 8).
+    """
+    c, dev = cache._struct, cache.pages.device
+    _rows(k, "k", c.head_dim, dev)
+    _rows(v, "v", c.head_dim, dev)
+    t = _slots(slots, dev)
+    for name, x in (("k", k), ("v", v)):
+        if x.shape[0] != t or x.shape[1] != c.kv_heads:
+            raise ValueError(f"{name}: expected {(t, c.kv_heads, c.head_dim)}, got {tuple(x.shape)}")
+    with _on(dev):
+        L.check("moe_nvfp4_kv_append", L.lib().moe_nvfp4_kv_append(
+            c, k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), slots.data_ptr(), t, _raw_stream(dev)))
+
+
+def kv_gather(cache: NvFp4KvCache, slots: torch.Tensor):
+    """Dequantize the rows at ``slots`` (int32 [n]): (k, v), each bf16 [n, kv_heads, head_dim].
+
+    A slot outside the cache gives a NaN row.
+    """
+    c, dev = cache._struct, cache.pages.device
+    n = _slots(slots, dev)
+    kv = torch.empty(2, n, c.kv_heads, c.head_dim, dtype=torch.bfloat16, device=dev)
+    k, v = kv[0], kv[1]
+    with _on(dev):
+        L.check("moe_nvfp4_kv_gather", L.lib().moe_nvfp4_kv_gather(c, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                                                   _raw_stream(dev)))
+    return k, v
+
+
+def kv_attention_workspace_size(T: int, R: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of ``kv_attention`` for T query rows of R requests."""
+    return int(L.lib().moe_nvfp4_kv_attention_workspace_size(T, R, heads, kv_heads, head_dim))
+
+
+def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                 block_table: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+                 return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None):
+    """Causal attention of query rows q (bf16 [T, heads, head_dim]) over the cache -> bf16 [T, heads, head_dim].
+
+    Rows [query_offsets[r], query_offsets[r+1]) are the last rows of request r, whose cache holds
+    ``seq_lens[r]`` positions (these rows' included: append first).  A row sees the positions up to its
+    own, with ``window`` > 0 only the last ``window`` of them.  ``scale`` defaults to head_dim^-0.5.
+    ``return_lse``: also the natural log-sum-exp of each row's scores, fp32 [T, heads] (-inf for a row
+    that sees nothing, whose output is zero).  Rows outside every request (a padded batch) are left as
+    they were in ``out``.  q may be a slice of a fused projection's output.  Without ``workspace`` the
+    call takes one from torch's allocator, so calls on several streams do not share it.
+    """
+    c, dev = cache._struct, cache.pages.device
+    _rows(q, "q", c.head_dim, dev)
+    t, heads = q.shape[0], q.shape[1]
+    if heads % c.kv_heads or not 1 <= heads // c.kv_heads <= 64:
+        raise ValueError(f"q: {heads} heads are no multiple (1 to 64) of the cache's {c.kv_heads}")
+    _need(query_offsets, "query_offsets", torch.int32, 1)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    r = seq_lens.shape[0]
+    _shape(query_offsets, "query_offsets", (r + 1,))
+    if block_table.shape[0] != r:
+        raise ValueError(f"block_table: {block_table.shape[0]} rows for {r} requests")
+    _same_device(cache.pages, ("query_offsets", query_offsets), ("seq_lens", seq_lens), ("block_table", block_table))
+    if scale is None:
+        scale = c.head_dim ** -0.5
+    if not (scale > 0.0 and math.isfinite(scale)):
+        raise ValueError(f"scale must be finite and positive, got {scale!r}")
+    if window < 0:
+        raise ValueError(f"window {window}")
+    if out is None:
+        out = torch.empty(t, heads, c.head_dim, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        _shape(out, "out", (t, heads, c.head_dim))
+        _same_device(cache.pages, ("out", out))
+    lse = torch.empty(t, heads, dtype=torch.float32, device=dev) if return_lse else None
+    need = L.lib().moe_nvfp4_kv_attention_workspace_size(t, r, heads, c.kv_heads, c.head_dim)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(cache.pages, ("workspace", workspace))
+    with _on(dev):
+        L.check("moe_nvfp4_kv_attention", L.lib().moe_nvfp4_kv_attention(
+            c, q.data_ptr(), q.stride(0), t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
+            block_table.data_ptr(), block_table.shape[1], scale, window, out.data_ptr(),
+            lse.data_ptr() if return_lse else None, workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0, _raw_stream(dev)))
+    return (out, lse) if return_lse else out
