@@ -117,17 +117,18 @@ def slots_of(table_row, page_size: int, first: int, last: int) -> np.ndarray:
 
 
 def attention(q, pages, page_size, k_gscale, v_gscale, offsets, lens, table, scale, window=0):
-    """float64 attention of q [T, heads, dim]: (out, lse, bound on |out|'s sum terms, score magnitude).
+    """float64 attention of q [T, heads, dim]: (out, lse, (terms, plain, mag)).
 
-    Rows outside every request are NaN.  ``terms`` is sum_j p_j |v_j| per output element and ``mag``
-    the largest sum_d |scale q_d k_d| over the positions a row sees (what rounding bounds scale with).
+    Rows outside every request are NaN.  What rounding bounds scale with: ``terms`` is
+    sum_j p_j |v_j| / sum p and ``plain`` sum_j |v_j| / sum p per output element, with p_j = 1 at the
+    largest score, and ``mag`` the largest sum_d |scale q_d k_d| over the positions a row sees.
     """
     q = np.asarray(q, np.float64)
     t_n, heads, dim = q.shape
     g = heads // pages.shape[1]
     out = np.full(q.shape, np.nan)
     lse = np.full((t_n, heads), np.nan)
-    terms = np.zeros(q.shape)
+    terms, plain = np.zeros(q.shape), np.zeros(q.shape)
     mag = np.zeros((t_n, heads))
     for r in range(len(lens)):
         a, b = int(offsets[r]), int(offsets[r + 1])
@@ -152,5 +153,6 @@ def attention(q, pages, page_size, k_gscale, v_gscale, offsets, lens, table, sca
                 out[t, h] = (p @ vv) / l
                 lse[t, h] = m + np.log(l)
                 terms[t, h] = (p @ np.abs(vv)) / l
+                plain[t, h] = np.abs(vv).sum(0) / l
                 mag[t, h] = (np.abs(kk) @ np.abs(q[t, h])).max() * scale
-    return out, lse, terms, mag
+    return out, lse, (terms, plain, mag)

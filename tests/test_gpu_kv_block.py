@@ -62,9 +62,9 @@ def test_steps_of_a_decoder_block_match_the_oracle():
         okv.append(pages, PAGE, _values(k), slots, 0.002, False)
         okv.append(pages, PAGE, _values(v), slots, 0.002, True)
         assert np.array_equal(block.cache.pages.cpu().numpy(), pages)
-        ref, lse, terms, mag = okv.attention(_values(q), pages, PAGE, 0.002, 0.002, off, after, table, DIM ** -0.5)
+        ref, lse, mags = okv.attention(_values(q), pages, PAGE, 0.002, 0.002, off, after, table, DIM ** -0.5)
         n = int(off[-1])
-        tol, _ = kh.bounds(ref[:n], lse[:n], terms[:n], mag[:n], int(after.max()), DIM)
+        tol, _ = kh.bounds(ref, lse, mags, slice(0, n), int(after.max()), DIM)
         assert np.all(np.abs(_values(att)[:n] - ref[:n]) <= tol), step
         assert (att[n:] == 0).all() and torch.isfinite(out).all()
         # what the cache hands back is what was stored

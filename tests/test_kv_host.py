@@ -79,7 +79,7 @@ def test_oracle_attention_is_softmax():
     okv.append(pages, page, v, slots, 0.02, True)
     kd, vd = okv.decode(pages, page, slots, 0.01, False)[:, 0], okv.decode(pages, page, slots, 0.02, True)[:, 0]
     q = rng.normal(0, 1, (4, 2, dim))
-    out, lse, _, _ = okv.attention(q, pages, page, 0.01, 0.02, [0, 4], [75], table, 0.125, window=9)
+    out, lse, _ = okv.attention(q, pages, page, 0.01, 0.02, [0, 4], [75], table, 0.125, window=9)
     for i in range(4):
         for h in range(2):
             s = 0.125 * kd @ q[i, h]
