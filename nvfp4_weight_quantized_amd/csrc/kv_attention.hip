@@ -371,6 +371,296 @@ __global__ __launch_bounds__(256) void kv_attention_rows_kernel(KvAttentionProbl
   }
 }
 
+// ------------------------------------------------------------------------ many rows per request
+// One workgroup (NW waves of 32 rows) per (kv head, row tile, split).  Two units (64 positions) at a
+// time are dequantized once into LDS, as fp16 operands of the 32x32x16 instruction in fragment order
+// (lane l's 16 bytes at 16*l), and multiplied by every wave; the next pair's codes are in registers and
+// its operands written to the other LDS buffer meanwhile.
+//   key operand, unit b, step t (16 elements): lane 32z + p holds position p, elements [16t + 8z, +8)
+//   value operand, unit b, step t (16 positions), range r: lane 32z + d holds element 32r + d, positions
+//     16t + 4z + {0..3} and 16t + 8 + 4z + {0..3}: the ones whose scores lane 32z + n holds after S^T.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_kernel(KvAttentionProblem a,
+                                                                                      KvSchedule s, KvPartials part) {
+  using U = KvUnit<D>;
+  constexpr int NS = D / 32, NT = D / 16, BM = 32 * NW, THREADS = 64 * NW;
+  constexpr int kPieces = 8 * D / THREADS;          // 8-byte code pieces per thread and pair of units
+  __shared__ __align__(16) uint8_t lds[2][256 * D];   // 64 positions: keys 128*D bytes, then values
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int z = lane >> 5, n32 = lane & 31;
+  const int hkv = a.cache.kv_heads;
+  const int h = blockIdx.x % hkv;
+  KvItem it;
+  if (!kv_find<false>(a, s, blockIdx.x / hkv, &it)) return;
+  {
+    // late rows see the most: their tiles first
+    const int t = it.q.tiles - 1 - it.tile;
+    it.slot += (t - it.tile) * it.splits;
+    it.tile = t;
+  }
+  const int rows = it.q.n * a.G, row_base = it.tile * BM;
+  const int pos0 = it.q.len - it.q.n;
+
+  // query operand: row n32 of the wave, elements [16t + 8z, +8)
+  const int row = row_base + 32 * wave + n32;
+  const bool valid = row < rows;
+  const int tok = valid ? row / a.G : 0, g = valid ? row - tok * a.G : 0;
+  int pos = valid ? pos0 + tok : -1;
+  f16x8 qf[NT];
+  float c;
+  {
+    const uint16_t* src = a.q + (int64_t)(it.q.row0 + tok) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * z;
+    u32x4 w[NT];
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      w[t] = *reinterpret_cast<const u32x4*>(src + 16 * t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[t][j] & 0x7FFFu, (w[t][j] >> 16) & 0x7FFFu));
+    }
+    int e = (int)(top >> 7);
+    e = max(e, __shfl_xor(e, 32));
+    const int sh = 141 - e;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f16x2 p0 = bf16x2_to_f16(w[t][0], sh), p1 = bf16x2_to_f16(w[t][1], sh);
+      const f16x2 p2 = bf16x2_to_f16(w[t][2], sh), p3 = bf16x2_to_f16(w[t][3], sh);
+      qf[t] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    }
+    c = ldexpf(a.scale * kLog2e, -sh);
+  }
+  // positions that the rows of [first, last) see: all of [*see_all, *pos_min], none outside
+  // [*see_any, *pos_max]
+  auto reach = [&](int first, int last, int* pos_min, int* pos_max, int* see_all, int* see_any) {
+    *pos_min = pos0 + first / a.G;
+    *pos_max = pos0 + (min(last, rows) - 1) / a.G;
+    *see_all = a.window > 0 ? (int)max(0ll, (long long)*pos_max - a.window + 1) : 0;
+    *see_any = a.window > 0 ? (int)max(0ll, (long long)*pos_min - a.window + 1) : 0;
+  };
+  int pos_min, pos_max, see_all, see_any, u0, u1;
+  {
+    int t0, t1, t2, t3;
+    reach(row_base, row_base + BM, &t0, &t1, &t2, &t3);
+    u0 = max(it.q.lo + it.split * it.chunk, t3 / kKvUnit);
+    u1 = t1 < 0 ? u0 : min(min(it.q.lo + it.split * it.chunk + it.chunk, it.q.hi), t1 / kKvUnit + 1);
+  }
+  const int wrow = row_base + 32 * wave;
+  const bool live = wrow < rows;                    // the wave has rows
+  reach(min(wrow, rows - 1), wrow + 32, &pos_min, &pos_max, &see_all, &see_any);
+  // the last pair may reach into the unit behind this split: nothing from `end` on counts
+  const int end = min(it.q.len, (int)min((long long)u1 * kKvUnit, 0x7FFFFFFFll));
+  const int low = a.window > 0 ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
+  pos = min(pos, end - 1);
+  pos_min = min(pos_min, end - 1);
+
+  f32x16 o[NS];
+  float m = kNone, l = 0.f;
+#pragma unroll
+  for (int r = 0; r < NS; ++r)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[r][i] = 0.f;
+
+  const int upp = a.cache.page_size / kKvUnit;
+  const int32_t* table = a.table + (size_t)it.r * a.width;
+  auto page_of = [&](int u) {
+    const int b = u / upp;
+    const int p = b < a.width ? table[b] : -1;
+    return p >= 0 && p < a.cache.num_pages ? p : -1;
+  };
+  int pages = -1;        // lane i: page of unit u0 + 64*batch + i, -1 bad
+  // code pieces of the pair of units at u: piece p < 4D key words, then value words
+  u32x2 code[kPieces];
+  u32x2 sc[kPieces];
+  uint32_t bad_now = 0, bad_next = 0;               // bit b: unit b of the pair has a bad page
+  auto load = [&](int u) {
+    const int i = u - u0;
+    if ((i & 63) == 0) {
+      const int uu = u + lane;
+      pages = uu < u1 ? page_of(uu) : 0;
+    }
+    const uint8_t* base[2];
+    bad_next = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int p = __builtin_amdgcn_readlane(pages, (i & 63) + b);
+      bad_next |= p < 0 ? 1u << b : 0u;
+      base[b] = a.cache.pages + (((size_t)max(p, 0) * hkv + h) * upp + (u + b) % upp) * (size_t)U::kBytes;
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int p = tid + THREADS * j;
+      const bool is_v = p >= 4 * D;
+      const int pp = p & (4 * D - 1), b = pp / (2 * D), x = pp & (2 * D - 1);   // 8-byte piece x of unit b
+      const uint8_t* ub = b ? base[1] : base[0];
+      code[j] = *reinterpret_cast<const u32x2*>(ub + (is_v ? U::kVCodes : 0) + 8 * x);
+      const int ln = (x >> 1) & 63, w = 4 * (x >> 7) + 2 * (x & 1);      // lane of the 16-row operand, word / 2*range
+      if (is_v)
+        sc[j] = *reinterpret_cast<const u32x2*>(ub + U::kVScales +
+                                                ((2 * (ln >> 4) + ((ln & 15) >> 3)) * NS + (w >> 1)) * 8);
+      else
+        sc[j][0] = *reinterpret_cast<const uint16_t*>(ub + U::kKScales + (16 * (ln >> 5) + (ln & 15)) * 2 * NS + w);
+    }
+  };
+  // the pair at u from registers to LDS buffer `buf`
+  auto store = [&](int u, int buf) {
+    uint8_t* kl = lds[buf];
+    uint8_t* vl = lds[buf] + 128 * D;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int p = tid + THREADS * j;
+      const bool is_v = p >= 4 * D;
+      const int pp = p & (4 * D - 1), b = pp / (2 * D), x = pp & (2 * D - 1);
+      const int ln = (x >> 1) & 63, w = 4 * (x >> 7) + 2 * (x & 1), q4 = ln >> 4, n16 = ln & 15;
+      if (is_v) {
+        const int r = w >> 1, key0 = kKvUnit * (u + b);
+        u32x2 sv = sc[j];
+        if (bad_now & (1u << b)) sv[0] = sv[1] = 0;
+        sv[0] &= keep_bytes(key0 + 4 * q4, end);
+        sv[1] &= keep_bytes(key0 + 16 + 4 * q4, end);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          f16x4 even, odd;
+          v_quad(code[j][t], sv[t], &even, &odd);
+          // positions 4*q4..: lane half z = q4 & 1, bytes 8*(q4 >> 1) of its 16
+          uint8_t* dst = vl + ((b * 2 + t) * NS + r) * 1024 + 16 * (32 * (q4 & 1) + 2 * n16) + 8 * (q4 >> 1);
+          *reinterpret_cast<f16x4*>(dst) = even;
+          *reinterpret_cast<f16x4*>(dst + 16) = odd;
+        }
+      } else {
+        const f16x2 sp = scale_pair(sc[j][0], false);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int ww = w + e, kb = ww / NS, i = ww % NS;
+          const f16x8 kf = k_operand(code[j][e], sp[e]);
+          uint8_t* dst = kl + (b * NT + 2 * i + (q4 >> 1)) * 1024 + 16 * (32 * (q4 & 1) + 16 * kb + n16);
+          *reinterpret_cast<f16x8*>(dst) = kf;
+        }
+      }
+    }
+  };
+
+  auto compute = [&](int u, int buf, uint32_t bad) {
+    const int key0 = kKvUnit * u;
+    const uint8_t* kl = lds[buf] + 16 * lane;
+    const uint8_t* vl = kl + 128 * D;
+    f32x16 sacc[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sacc[b][i] = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        sacc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(kl + (b * NT + t) * 1024),
+                                                         qf[t], sacc[b], 0, 0, 0);
+    }
+    if (key0 + 63 > pos_min || key0 < see_all || bad) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = key0 + 32 * b + 8 * (i >> 2) + 4 * z + (i & 3);
+          const bool seen = key <= pos && key >= low;
+          sacc[b][i] = !seen ? -INFINITY : (bad >> b) & 1u ? NAN : sacc[b][i];
+        }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sacc[b][i] *= c;
+        mx = fmaxf(mx, sacc[b][i]);
+      }
+    if (__any(mx > m + kSlack)) {
+      const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+      mx = fmaxf(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])), m);
+      const float f = exp2_hw(m - mx);
+      m = mx;
+      l *= f;
+#pragma unroll
+      for (int r = 0; r < NS; ++r)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[r][i] *= f;
+    }
+    const float ref = m - kPExp;
+    f16x8 pf[2][2];
+    float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = exp2_hw(sacc[b][i] - ref), p1 = exp2_hw(sacc[b][i + 1] - ref);
+        part_sum[(i >> 1) & 3] += p0 + p1;
+        const f16x2 pr = __builtin_convertvector((f32x2){p0, p1}, f16x2);
+        pf[b][i >> 3][i & 7] = pr[0];
+        pf[b][i >> 3][(i & 7) + 1] = pr[1];
+      }
+    l += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < NS; ++r)
+          o[r] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              *reinterpret_cast<const f16x8*>(vl + ((b * 2 + t) * NS + r) * 1024), pf[b][t], o[r], 0, 0, 0);
+  };
+
+  if (u0 < u1) {
+    load(u0);
+    bad_now = bad_next;
+    store(u0, 0);
+    uint32_t bad = bad_now;
+    if (u0 + 2 < u1) load(u0 + 2);
+    __syncthreads();
+    int buf = 0;
+    for (int u = u0; u < u1; u += 2) {
+      if (live && kKvUnit * u <= pos_max && kKvUnit * u + 63 >= see_any) compute(u, buf, bad);
+      if (u + 2 < u1) {
+        bad_now = bad_next;
+        bad = bad_now;
+        store(u + 2, buf ^ 1);
+        if (u + 4 < u1) load(u + 4);
+      }
+      __syncthreads();
+      buf ^= 1;
+    }
+  }
+
+  {
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+  }
+  if (!valid) return;
+  const size_t at = (size_t)(it.q.row0 + tok) * a.Hq + h * a.G + g;
+  if (it.splits == 1) {
+    const bool any = l > 0.f || l != l;
+    const float norm = any ? a.cache.v_gscale / l : 0.f;
+    if (a.lse && z == 0) a.lse[at] = any ? kLn2 * (m + (__builtin_amdgcn_logf(l) - kPExp)) : -INFINITY;
+#pragma unroll
+    for (int r = 0; r < NS; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2*>(a.out + at * D + 32 * r + 8 * i + 4 * z) =
+            u32x2{f32x2_to_bf16x2(o[r][4 * i] * norm, o[r][4 * i + 1] * norm),
+                  f32x2_to_bf16x2(o[r][4 * i + 2] * norm, o[r][4 * i + 3] * norm)};
+  } else {
+    const size_t slot = (size_t)(it.slot + it.split) * hkv + h;
+    const int lrow = 32 * wave + n32;
+    if (z == 0) {
+      part.ml[slot * 2 * BM + lrow] = m;
+      part.ml[slot * 2 * BM + BM + lrow] = l;
+    }
+    float* dst = part.o + (slot * BM + lrow) * D + 4 * z;
+#pragma unroll
+    for (int r = 0; r < NS; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(dst + 32 * r + 8 * i) =
+            float4{o[r][4 * i], o[r][4 * i + 1], o[r][4 * i + 2], o[r][4 * i + 3]};
+  }
+}
+
 // ------------------------------------------------------------------------- combine
 // Sixteen rows of one tile per workgroup: the partial sums of its splits added in split order.
 template <int D>
@@ -420,57 +710,91 @@ struct Launch {
   KvSchedule s;
   int64_t tiles;    // bound on the row tiles of a kv head
   int64_t items;    // bound on the items of a kv head
-  int64_t slots;    // bound on the partial slots of a kv head
-  size_t o_bytes, ml_bytes;
+  size_t o_bytes, bytes;
 };
-
-constexpr int kRowsTarget = 1024;
-constexpr int kRowsMinChunk = 4;
 
 // bm rows per tile, about `target` items over all heads.  With chunk >= sum(tiles*units)/target the
 // items are sum tiles*ceil(units/chunk) <= tiles + target; those of requests with two splits or more
 // number at most twice target.
-Launch plan_launch(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int bm, int target, int min_chunk) {
+Launch plan_launch(const KvSchedule& s, int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D) {
   Launch p{};
-  p.s.bm = bm;
-  p.s.target = std::max(1, target / hkv);
-  p.s.min_chunk = min_chunk;
-  p.s.min_rows = 0;
-  p.s.max_rows = 0x7FFFFFFF;
-  p.tiles = std::min((int64_t)R, (int64_t)T) + (int64_t)T * G / bm;
+  p.s = s;
+  p.s.target = std::max(1, s.target / hkv);
+  p.tiles = std::min((int64_t)R, (int64_t)T) + (int64_t)T * G / s.bm;
   p.items = p.tiles + p.s.target;
-  p.slots = 2 * (int64_t)p.s.target;
-  p.o_bytes = (size_t)p.slots * hkv * bm * D * 4;
-  p.ml_bytes = (size_t)p.slots * hkv * 2 * bm * 4;
+  const size_t slots = 2 * (size_t)p.s.target * hkv;
+  p.o_bytes = slots * s.bm * D * 4;
+  p.bytes = p.o_bytes + slots * 2 * s.bm * 4;
   return p;
 }
 
-int rows_tile(int32_t T, int32_t R, int32_t G) { return (int64_t)T * G > 16 * (int64_t)R ? 32 : 16; }
+constexpr int kRowsTarget = 1024;      // items of the few-row kernel over all heads
+constexpr int kRowsMinChunk = 4;       // units: one per wave
+constexpr int kTilesTarget = 512;
+constexpr int kTilesMinChunk = 16;
+constexpr int kRowsSplit = 64;         // requests of more rows go to the tile kernel where both run
+
+// The launches of a call: the few-row kernel, the tile kernel, or both, each on its requests.
+struct Launches {
+  int n;
+  bool tiles[2];
+  Launch l[2];
+};
+
+Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D) {
+  Launches x{};
+  const int64_t rows = (int64_t)T * G;
+  const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
+  const bool few = !tiles || R > 1;
+  if (tiles) {
+    const int bm = D == 256 ? 128 : 256;
+    x.tiles[x.n] = true;
+    x.l[x.n++] = plan_launch(KvSchedule{bm, kTilesTarget, kTilesMinChunk, few ? kRowsSplit : 0, 0x7FFFFFFF}, T, R, G,
+                             hkv, D);
+  }
+  if (few) {
+    const int bm = tiles || rows > 16 * (int64_t)R ? 32 : 16;
+    x.l[x.n++] = plan_launch(KvSchedule{bm, kRowsTarget, kRowsMinChunk, 0, tiles ? kRowsSplit : 0x7FFFFFFF}, T, R, G,
+                             hkv, D);
+  }
+  return x;
+}
 
 }  // namespace
 
 size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int32_t D) {
   if (T == 0 || R == 0) return 0;
-  const int G = Hq / hkv;
-  const Launch p = plan_launch(T, R, G, hkv, D, rows_tile(T, R, G), kRowsTarget, kRowsMinChunk);
-  return p.o_bytes + p.ml_bytes;
+  const Launches x = plan_launches(T, R, Hq / hkv, hkv, D);
+  size_t bytes = 0;
+  for (int i = 0; i < x.n; ++i) bytes = std::max(bytes, x.l[i].bytes);
+  return bytes;
 }
 
 moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, hipStream_t stream) {
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
-  const Launch p = plan_launch(a.T, a.R, a.G, hkv, D, rows_tile(a.T, a.R, a.G), kRowsTarget, kRowsMinChunk);
-  if (p.items * hkv > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
-  KvPartials part{static_cast<float*>(workspace), nullptr};
-  part.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_bytes);
-  with_head_dim(D, [&](auto tag) {
-    constexpr int DD = decltype(tag)::value;
-    if (p.s.bm == 16)
-      hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1>), dim3(p.items * hkv), dim3(256), 0, stream, a, p.s, part);
-    else
-      hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 2>), dim3(p.items * hkv), dim3(256), 0, stream, a, p.s, part);
-    hipLaunchKernelGGL(kv_combine_kernel<DD>, dim3(p.tiles * hkv, p.s.bm / 16), dim3(256), 0, stream, a, p.s, part);
-  });
-  return launch_status();
+  const Launches x = plan_launches(a.T, a.R, a.G, hkv, D);
+  for (int i = 0; i < x.n; ++i)
+    if (x.l[i].items * hkv > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < x.n; ++i) {
+    const Launch& p = x.l[i];
+    KvPartials part{static_cast<float*>(workspace), nullptr};
+    part.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_bytes);
+    with_head_dim(D, [&](auto tag) {
+      constexpr int DD = decltype(tag)::value;
+      constexpr int NW = DD == 256 ? 4 : 8;
+      const dim3 grid((unsigned)(p.items * hkv));
+      if (x.tiles[i])
+        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, NW>), grid, dim3(64 * NW), 0, stream, a, p.s, part);
+      else if (p.s.bm == 16)
+        hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1>), grid, dim3(256), 0, stream, a, p.s, part);
+      else
+        hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 2>), grid, dim3(256), 0, stream, a, p.s, part);
+      hipLaunchKernelGGL(kv_combine_kernel<DD>, dim3((unsigned)(p.tiles * hkv), p.s.bm / 16), dim3(256), 0, stream, a,
+                         p.s, part);
+    });
+    if (moe_status_t st = launch_status()) return st;
+  }
+  return MOE_OK;
 }
 
 }  // namespace moe
