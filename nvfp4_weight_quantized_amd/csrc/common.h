@@ -31,6 +31,14 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
 
+// This lane's index in its wave, computed where it is used (the mask count is opaque to the
+// optimizer, so no register holds it, or values derived from it, across the code in between).
+__device__ __forceinline__ int lane_now() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
 // 16 bytes per lane from global memory straight to LDS (global_load_lds_dwordx4): lane i's bytes
 // land at lds_addr + 16*i.  The global address is a wave-uniform base plus a 32-bit per-lane byte
 // offset; lds_addr must be wave-uniform (it is passed in M0).  Issued from inline assembly, so the
@@ -40,10 +48,19 @@ __device__ __forceinline__ void direct_load16(const void* base, uint32_t offset,
   asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(offset), "s"(base), "{m0}"(lds_addr) : "memory");
 }
 
+// direct_load16 of data that is read once (non-temporal: it does not displace what the caches hold).
+__device__ __forceinline__ void direct_load16_nt(const void* base, uint32_t offset, uint32_t lds_addr) {
+  asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(offset), "s"(base), "{m0}"(lds_addr) : "memory");
+}
+
 // 4 bytes per lane from global memory straight to LDS (global_load_lds_dword): lane i's dword lands
 // at lds_addr + 4*i; otherwise as direct_load16.
 __device__ __forceinline__ void direct_load4(const void* base, uint32_t offset, uint32_t lds_addr) {
   asm volatile("global_load_lds_dword %0, %1" : : "v"(offset), "s"(base), "{m0}"(lds_addr) : "memory");
+}
+
+__device__ __forceinline__ void direct_load4_nt(const void* base, uint32_t offset, uint32_t lds_addr) {
+  asm volatile("global_load_lds_dword %0, %1 nt" : : "v"(offset), "s"(base), "{m0}"(lds_addr) : "memory");
 }
 
 // Host-side launch helpers -----------------------------------------------------------------

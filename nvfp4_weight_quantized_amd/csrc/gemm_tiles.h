@@ -30,14 +30,6 @@ __device__ __forceinline__ float silu(float g) {
 
 constexpr int kXcds = 8;
 
-// This lane's index in its wave, computed where it is used (the mask count is opaque to the
-// optimizer, so no register holds it, or values derived from it, across the code in between).
-__device__ __forceinline__ int lane_now() {
-  int l;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-  return l;
-}
-
 template <int N>
 struct IntC {
   static constexpr int value = N;

@@ -96,277 +96,337 @@ __device__ __forceinline__ uint32_t keep_bytes(int first, int len) {
 }
 
 struct KvPartials {
-  float* o;    // [slot * Hkv + h][BM][D], unnormalised
-  float* ml;   // [slot * Hkv + h][2][BM]: reference maximum, sum
+  float* o;    // [slot][BM][D], unnormalised
+  float* ml;   // [slot][2][BM]: reference maximum, sum
 };
 
 // ------------------------------------------------------------------------- few rows per request
-// One workgroup (four waves) per (kv head, row tile of 16*MI rows, split of the units); each wave takes
-// every fourth unit of the split, from 36*D contiguous bytes straight into registers, the next unit's
-// loads in flight while this one is multiplied.  The four waves' sums meet in LDS at the end.
+// Workgroups of four waves with an equal share of the units each (KvShare); of a segment (one kv head and
+// row tile of 16*MI rows) each wave takes every fourth unit.  A unit's 36*D contiguous bytes go straight
+// to LDS, into a ring of kRing units of the wave's own (no barrier, no registers held for loads in
+// flight), and from there to registers when their turn comes.  The four waves' sums meet in LDS at the
+// end of the segment.
+constexpr int kRing = 2;
+
+// Waves per SIMD the kernel is built for (registers, ring), and so its resident workgroups per compute unit.
 template <int D, int MI>
-__global__ __launch_bounds__(256) void kv_attention_rows_kernel(KvAttentionProblem a, KvSchedule s, KvPartials part) {
+constexpr int rows_occupancy() {
+  return D == 256 ? (MI == 2 ? 1 : 2) : D == 128 ? (MI == 2 ? 2 : 4) : (MI == 2 ? 3 : 4);
+}
+
+// Waits until at most n units' loads (PER instructions each) of this wave are in flight.
+template <int PER>
+__device__ __forceinline__ void wait_units(int n) {
+  static_assert(3 * PER <= 63, "the counter of loads in flight");
+  if (n <= 0) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  else if (n == 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(PER) : "memory");
+  else if (n == 2) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * PER) : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * PER) : "memory");
+}
+
+template <int D, int MI>
+__global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_rows_kernel(KvAttentionProblem a,
+                                                                                          KvSchedule s,
+                                                                                          KvPartials part) {
   using U = KvUnit<D>;
   constexpr int NS = D / 32, BM = 16 * MI, NL = NS / 2;
-  __shared__ float o_lds[4][BM][36];    // one 32-element range at a time; rows padded to 36 floats
+  constexpr int kFull = U::kBytes / 1024, kTail = U::kBytes % 1024 / 256;   // 1024- and 256-byte loads of a unit
+  constexpr int kOut = 4 * BM * 36 * 4, kRings = 4 * kRing * U::kBytes;
+  // the waves' rings; at the end of a segment one 32-element range of the sums (rows padded to 36 floats)
+  __shared__ __align__(16) uint8_t lds[kOut > kRings ? kOut : kRings];
   __shared__ float m_lds[4][BM], l_lds[4][BM];
+  using lds_bytes = __attribute__((address_space(3))) uint8_t*;
+  float(*o_lds)[BM][36] = reinterpret_cast<float(*)[BM][36]>(lds);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q4 = lane >> 4, n16 = lane & 15;
   const int hkv = a.cache.kv_heads;
-  const int h = blockIdx.x % hkv;
-  KvItem it;
-  if (!kv_find<false>(a, s, blockIdx.x / hkv, &it)) return;
-  const int rows = it.q.n * a.G, row_base = it.tile * BM;
-  const int pos0 = it.q.len - it.q.n;          // position of the request's first row
-
-  // query operands: row n16 of block mi, elements [32s + 8*q4, +8)
-  f16x8 qf[MI][NS];
-  float c[MI];
-  int pos[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    const int row = row_base + 16 * mi + n16;
-    const bool valid = row < rows;
-    const int tok = valid ? row / a.G : 0, g = valid ? row - tok * a.G : 0;
-    pos[mi] = valid ? pos0 + tok : -1;
-    const uint16_t* src = a.q + (int64_t)(it.q.row0 + tok) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * q4;
-    u32x4 w[NS];
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      w[i] = *reinterpret_cast<const u32x4*>(src + 32 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, max(w[i][j] & 0x7FFFu, (w[i][j] >> 16) & 0x7FFFu));
-    }
-    int e = (int)(top >> 7);    // the row's largest exponent field
-    e = max(e, __shfl_xor(e, 16));
-    e = max(e, __shfl_xor(e, 32));
-    const int sh = 141 - e;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const f16x2 p0 = bf16x2_to_f16(w[i][0], sh), p1 = bf16x2_to_f16(w[i][1], sh);
-      const f16x2 p2 = bf16x2_to_f16(w[i][2], sh), p3 = bf16x2_to_f16(w[i][3], sh);
-      qf[mi][i] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-    }
-    c[mi] = ldexpf(a.scale * kLog2e, -sh);
-  }
-  // positions seen by the tile's rows
-  const int tok_first = row_base / a.G, tok_last = (min(row_base + BM, rows) - 1) / a.G;
-  const int pos_min = pos0 + tok_first, pos_max = pos0 + tok_last;
-  int u0 = it.q.lo + it.split * it.chunk, u1 = min(u0 + it.chunk, it.q.hi);
-  // every row sees [see_all, pos_min], none anything before see_any
-  const int see_all = a.window > 0 ? (int)max(0ll, (long long)pos_max - a.window + 1) : 0;
-  const int see_any = a.window > 0 ? (int)max(0ll, (long long)pos_min - a.window + 1) : 0;
-  u0 = max(u0, see_any / kKvUnit);
-  u1 = pos_max < 0 ? u0 : min(u1, pos_max / kKvUnit + 1);
-
-  f32x4 o[MI][NS][2];
-  float m[MI], l[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    m[mi] = kNone;
-    l[mi] = 0.f;
-#pragma unroll
-    for (int r = 0; r < NS; ++r) o[mi][r][0] = o[mi][r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
+  const lds_bytes ring = (lds_bytes)lds + wave * kRing * U::kBytes;
+  KvShare sh;
+  KvWhere at;
+  long long local;
+  if (!kv_locate<false>(a, s, blockIdx.x, &sh, &at, &local)) return;
+  const long long begin = (long long)blockIdx.x * sh.chunk;
+  int left = (int)min(sh.chunk, sh.total - begin);
   const int upp = a.cache.page_size / kKvUnit;
-  const int32_t* table = a.table + (size_t)it.r * a.width;
-  // page of unit u, -1 for a bad entry
-  auto page_of = [&](int u) {
-    const int b = u / upp;
-    const int p = b < a.width ? table[b] : -1;
-    return p >= 0 && p < a.cache.num_pages ? p : -1;
-  };
-  struct Regs {
-    u32x4 k[NL], v[NL];
-    uint32_t ks[NS / 2];      // 2*NS scale bytes
-    u32x2 vs[NS];
-    int bad;
-  };
-  int pages = -1;   // lane i: page of the wave's unit u0 + wave + 4*(64*batch + i)
-  auto load = [&](int u, int i, Regs& x) {
-    if ((i & 63) == 0) {
-      const int uu = u + 4 * lane;
-      pages = uu < u1 ? page_of(uu) : 0;
-    }
-    const int p = __builtin_amdgcn_readlane(pages, i & 63);
-    x.bad = p < 0;
-    const uint8_t* base = a.cache.pages + (((size_t)max(p, 0) * hkv + h) * upp + u % upp) * (size_t)U::kBytes;
-#pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      x.k[j] = *reinterpret_cast<const u32x4*>(base + 1024 * j + 16 * lane);
-      x.v[j] = *reinterpret_cast<const u32x4*>(base + U::kVCodes + 1024 * j + 16 * lane);
-    }
-    const uint32_t* ks = reinterpret_cast<const uint32_t*>(base + U::kKScales + (16 * (q4 >> 1) + n16) * 2 * NS);
-#pragma unroll
-    for (int j = 0; j < NS / 2; ++j) x.ks[j] = ks[j];
-    const u32x2* vs = reinterpret_cast<const u32x2*>(base + U::kVScales + (2 * q4 + (n16 >> 3)) * NS * 8);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) x.vs[j] = vs[j];
-  };
+  bool first = true;
 
-  auto compute = [&](int u, Regs& x) {
-    const int key0 = kKvUnit * u;
-    f32x4 sc[MI][2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) sc[mi][kb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int w = kb * NS + i;
-        const f16x2 sp = scale_pair(x.ks[w >> 2], (w & 2) != 0);
-        const f16x8 kf = k_operand(x.k[w >> 2][w & 3], (w & 1) ? sp[1] : sp[0]);
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-          sc[mi][kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mi][i], sc[mi][kb], 0, 0, 0);
+  while (true) {
+    const int units = max(1, at.q.hi - at.q.lo);
+    const long long step = kv_step(at.q, sh), nth = div_i64(local, step);
+    const int unit = (int)(local - nth * step);
+    const int h = (int)div_i64(nth, at.q.tiles), tile = (int)(nth - (long long)h * at.q.tiles);
+    const int count = min(left, units - unit);
+
+    const int rows = at.q.n * a.G, row_base = tile * BM;
+    const int pos0 = at.q.len - at.q.n;          // position of the request's first row
+    // positions seen by the tile's rows: every row sees [see_all, pos_min], none anything before see_any
+    const int pos_min = pos0 + row_base / a.G, pos_max = pos0 + (min(row_base + BM, rows) - 1) / a.G;
+    const int see_all = a.window > 0 ? (int)max(0ll, (long long)pos_max - a.window + 1) : 0;
+    const int see_any = a.window > 0 ? (int)max(0ll, (long long)pos_min - a.window + 1) : 0;
+    const int u0 = max(at.q.lo + unit, see_any / kKvUnit);
+    const int u1 = pos_max < 0 ? u0 : min(at.q.lo + unit + count, pos_max / kKvUnit + 1);
+    const int32_t* table = a.table + (size_t)at.r * a.width;
+
+    // the wave's units u0 + wave + 4*i, i < mine; lane i & 63 holds the address of unit i of a batch of 64
+    // (0 for a bad table entry), bad[batch & 1] the bad ones
+    const int ufirst = u0 + wave, mine = ufirst < u1 ? (u1 - ufirst + 3) >> 2 : 0;
+    uint64_t where = 0, bad[2] = {0, 0};
+    auto issue = [&](int i, int slot) {
+      if ((i & 63) == 0) {
+        const int uu = ufirst + 4 * (i + lane);
+        where = 0;
+        if (i + lane < mine) {
+          const int b = uu / upp, p = b < a.width ? table[b] : -1;
+          if (p >= 0 && p < a.cache.num_pages)
+            where = reinterpret_cast<uint64_t>(a.cache.pages) +
+                    (((uint64_t)p * hkv + h) * upp + (uu - b * upp)) * (uint64_t)U::kBytes;
+        }
+        const uint64_t none = __ballot(where == 0);
+        if (i & 64) bad[1] = none;
+        else bad[0] = none;
       }
-    }
-    // units that some row does not see whole: masks, and nothing from positions past the length
-    const bool whole = key0 + kKvUnit - 1 <= pos_min && key0 >= see_all;
-    if (!whole || x.bad) {
+      const uint64_t at_unit = (uint64_t)lane_i64((long long)where, i & 63);
+      const uint8_t* base = at_unit ? reinterpret_cast<const uint8_t*>(at_unit) : a.cache.pages;
+      const uint32_t dst = (uint32_t)(uintptr_t)ring + slot * U::kBytes;
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
+      for (int j = 0; j < kFull; ++j) direct_load16_nt(base + 1024 * j, 16 * lane, dst + 1024 * j);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 16 * kb + 4 * q4 + i;
-            const bool seen = key <= pos[mi] && (a.window == 0 || pos[mi] - key < a.window);
-            sc[mi][kb][i] = !seen ? -INFINITY : x.bad ? NAN : sc[mi][kb][i];
-          }
-      const uint32_t k0 = x.bad ? 0u : keep_bytes(key0 + 4 * q4, it.q.len);
-      const uint32_t k1 = x.bad ? 0u : keep_bytes(key0 + 16 + 4 * q4, it.q.len);
-#pragma unroll
-      for (int r = 0; r < NS; ++r) {
-        x.vs[r][0] &= k0;
-        x.vs[r][1] &= k1;
-      }
-    }
-    f16x8 pf[MI];
+      for (int j = 0; j < kTail; ++j)
+        direct_load4_nt(base + 1024 * kFull + 256 * j, 4 * lane, dst + 1024 * kFull + 256 * j);
+    };
+    if (!first) __syncthreads();      // the previous segment's reads of LDS
+    for (int i = 0; i < min(mine, kRing); ++i) issue(i, i);
+
+    // query operands: row n16 of block mi, elements [32s + 8*q4, +8)
+    f16x8 qf[MI][NS];
+    float c[MI];
+    int pos[MI];
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      float t[8];
+      const int row = row_base + 16 * mi + n16;
+      const bool valid = row < rows;
+      const int tok = valid ? row / a.G : 0, g = valid ? row - tok * a.G : 0;
+      pos[mi] = valid ? pos0 + tok : -1;
+      const uint16_t* src = a.q + (int64_t)(at.q.row0 + tok) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * q4;
+      u32x4 w[NS];
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = sc[mi][i >> 2][i & 3] * c[mi];
-      float mx = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-      if (__any(mx > m[mi] + kSlack)) {
-        mx = fmaxf(quarter_max(mx), m[mi]);
-        const float f = exp2_hw(m[mi] - mx);
-        m[mi] = mx;
-        l[mi] *= f;
+      for (int k = 0; k < NS; ++k) {
+        w[k] = *reinterpret_cast<const u32x4*>(src + 32 * k);
 #pragma unroll
-        for (int r = 0; r < NS; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[mi][r][e][i] *= f;
+        for (int j = 0; j < 4; ++j) top = max(top, max(w[k][j] & 0x7FFFu, (w[k][j] >> 16) & 0x7FFFu));
       }
-      const float ref = m[mi] - kPExp;
+      int e = (int)(top >> 7);    // the row's largest exponent field
+      e = max(e, __shfl_xor(e, 16));
+      e = max(e, __shfl_xor(e, 32));
+      const int shift = 141 - e;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = exp2_hw(t[i] - ref);
-      l[mi] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+      for (int k = 0; k < NS; ++k) {
+        const f16x2 p0 = bf16x2_to_f16(w[k][0], shift), p1 = bf16x2_to_f16(w[k][1], shift);
+        const f16x2 p2 = bf16x2_to_f16(w[k][2], shift), p3 = bf16x2_to_f16(w[k][3], shift);
+        qf[mi][k] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+      }
+      c[mi] = ldexpf(a.scale * kLog2e, -shift);
+    }
+
+    f32x4 o[MI][NS][2];
+    float m[MI], l[MI];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f16x2 pr = __builtin_convertvector((f32x2){t[2 * i], t[2 * i + 1]}, f16x2);
-        pf[mi][2 * i] = pr[0];
-        pf[mi][2 * i + 1] = pr[1];
+    for (int mi = 0; mi < MI; ++mi) {
+      m[mi] = kNone;
+      l[mi] = 0.f;
+#pragma unroll
+      for (int r = 0; r < NS; ++r) o[mi][r][0] = o[mi][r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // `off`: byte of the ring where the unit begins
+    auto compute = [&](int uu, int off, bool bad_page) {
+      const int key0 = kKvUnit * uu;
+      const lds_bytes unit_lds = ring + off;
+      u32x4 kc[NL];
+      uint32_t ks[NS / 2];      // 2*NS scale bytes: word w = block*NS + step
+#pragma unroll
+      for (int j = 0; j < NL; ++j)
+        kc[j] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(unit_lds + 1024 * j + 16 * lane);
+#pragma unroll
+      for (int j = 0; j < NS / 2; ++j)
+        ks[j] = *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(
+            unit_lds + U::kKScales + (16 * (q4 >> 1) + n16) * 2 * NS + 4 * j);
+      f32x4 sc[MI][2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) sc[mi][kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          const int w = kb * NS + k;
+          const f16x2 sp = scale_pair(ks[w >> 2], (w & 2) != 0);
+          const f16x8 kf = k_operand(kc[w >> 2][w & 3], (w & 1) ? sp[1] : sp[0]);
+#pragma unroll
+          for (int mi = 0; mi < MI; ++mi)
+            sc[mi][kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mi][k], sc[mi][kb], 0, 0, 0);
+        }
+      }
+      // units that some row does not see whole: masks, and nothing from positions past the length
+      const bool whole = key0 + kKvUnit - 1 <= pos_min && key0 >= see_all;
+      uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
+      if (!whole || bad_page) {
+        const int quarter = 4 * (lane_now() >> 4);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int key = key0 + 16 * kb + quarter + k;
+              const bool seen = key <= pos[mi] && (a.window == 0 || pos[mi] - key < a.window);
+              sc[mi][kb][k] = !seen ? -INFINITY : bad_page ? NAN : sc[mi][kb][k];
+            }
+        keep0 = bad_page ? 0u : keep_bytes(key0 + quarter, at.q.len);
+        keep1 = bad_page ? 0u : keep_bytes(key0 + 16 + quarter, at.q.len);
+      }
+      f16x8 pf[MI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        float t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = sc[mi][k >> 2][k & 3] * c[mi];
+        float mx = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+        if (__any(mx > m[mi] + kSlack)) {
+          mx = fmaxf(quarter_max(mx), m[mi]);
+          const float f = exp2_hw(m[mi] - mx);
+          m[mi] = mx;
+          l[mi] *= f;
+#pragma unroll
+          for (int r = 0; r < NS; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[mi][r][e][k] *= f;
+        }
+        const float ref = m[mi] - kPExp;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = exp2_hw(t[k] - ref);
+        l[mi] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f16x2 pr = __builtin_convertvector((f32x2){t[2 * k], t[2 * k + 1]}, f16x2);
+          pf[mi][2 * k] = pr[0];
+          pf[mi][2 * k + 1] = pr[1];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < NS; ++r) {
+        const u32x2 vc = *reinterpret_cast<const __attribute__((address_space(3))) u32x2*>(
+            unit_lds + U::kVCodes + 1024 * (r >> 1) + 16 * lane + 8 * (r & 1));
+        const u32x2 vs = *reinterpret_cast<const __attribute__((address_space(3))) u32x2*>(
+            unit_lds + U::kVScales + ((2 * q4 + (n16 >> 3)) * NS + r) * 8);
+        f16x4 e0, o0, e1, o1;
+        v_quad(vc[0], vs[0] & keep0, &e0, &o0);
+        v_quad(vc[1], vs[1] & keep1, &e1, &o1);
+        const f16x8 ve = __builtin_shufflevector(e0, e1, 0, 1, 2, 3, 4, 5, 6, 7);
+        const f16x8 vo = __builtin_shufflevector(o0, o1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          o[mi][r][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ve, pf[mi], o[mi][r][0], 0, 0, 0);
+          o[mi][r][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo, pf[mi], o[mi][r][1], 0, 0, 0);
+        }
+      }
+    };
+
+    for (int i = 0, slot = 0; i < mine; ++i) {
+      wait_units<kFull + kTail>(min(kRing, mine - i) - 1);
+      compute(ufirst + 4 * i, slot * U::kBytes, (bad[(i >> 6) & 1] >> (i & 63)) & 1);
+      if (i + kRing < mine) {
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the slot has been read
+        issue(i + kRing, slot);
+      }
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
+
+    // the four waves' sums: common reference maximum per row, then range by range through LDS
+    __syncthreads();      // every wave has read its ring
+    const int elane = lane_now(), eq = elane >> 4, en = elane & 15, etid = 64 * wave + elane;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const float ls = quarter_sum(l[mi]);
+      if (eq == 0) {
+        m_lds[wave][16 * mi + en] = m[mi];
+        l_lds[wave][16 * mi + en] = ls;
+      }
+    }
+    __syncthreads();
+    float f[MI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int rr = 16 * mi + en;
+      const float top = fmaxf(fmaxf(m_lds[0][rr], m_lds[1][rr]), fmaxf(m_lds[2][rr], m_lds[3][rr]));
+      f[mi] = exp2_hw(m[mi] - top);
+    }
+    const bool direct = count == units;
+    // thread -> row tid / (256 / BM), consecutive elements of the range
+    constexpr int TPR = 256 / BM, EPT = 32 / TPR;
+    const int orow = etid / TPR, oc = (etid % TPR) * EPT;
+    float top = kNone, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, m_lds[w][orow]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += l_lds[w][orow] * exp2_hw(m_lds[w][orow] - top);
+    const int grow = row_base + orow;
+    const bool valid = grow < rows;
+    const int tok = grow / a.G, g = grow - tok * a.G;
+    const size_t dst_row = (size_t)(at.q.row0 + tok) * a.Hq + h * a.G + g;
+    const size_t slot = 2 * (size_t)blockIdx.x + (unit == 0 ? 1 : 0);
+    const float norm = sum > 0.f || sum != sum ? a.cache.v_gscale / sum : 0.f;
+    if (etid % TPR == 0 && valid) {
+      if (direct) {
+        if (a.lse)
+          a.lse[dst_row] = sum > 0.f || sum != sum ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+      } else {
+        part.ml[slot * 2 * BM + orow] = top;
+        part.ml[slot * 2 * BM + BM + orow] = sum;
       }
     }
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
-      f16x4 e0, o0, e1, o1;
-      v_quad(x.v[r >> 1][2 * (r & 1)], x.vs[r][0], &e0, &o0);
-      v_quad(x.v[r >> 1][2 * (r & 1) + 1], x.vs[r][1], &e1, &o1);
-      const f16x8 ve = __builtin_shufflevector(e0, e1, 0, 1, 2, 3, 4, 5, 6, 7);
-      const f16x8 vo = __builtin_shufflevector(o0, o1, 0, 1, 2, 3, 4, 5, 6, 7);
+      if (r > 0) __syncthreads();
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
-        o[mi][r][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ve, pf[mi], o[mi][r][0], 0, 0, 0);
-        o[mi][r][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo, pf[mi], o[mi][r][1], 0, 0, 0);
+        float* dst = &o_lds[wave][16 * mi + en][8 * eq];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dst[2 * k] = o[mi][r][0][k] * f[mi];
+          dst[2 * k + 1] = o[mi][r][1][k] * f[mi];
+        }
+      }
+      __syncthreads();
+      float v[EPT];
+#pragma unroll
+      for (int e = 0; e < EPT; ++e)
+        v[e] = (o_lds[0][orow][oc + e] + o_lds[1][orow][oc + e]) + (o_lds[2][orow][oc + e] + o_lds[3][orow][oc + e]);
+      if (valid) {
+        if (direct) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + dst_row * D + 32 * r + oc);
+#pragma unroll
+          for (int e = 0; e < EPT / 2; ++e) dst[e] = f32x2_to_bf16x2(v[2 * e] * norm, v[2 * e + 1] * norm);
+        } else {
+          float* dst = part.o + (slot * BM + orow) * D + 32 * r + oc;
+#pragma unroll
+          for (int e = 0; e < EPT; ++e) dst[e] = v[e];
+        }
       }
     }
-  };
 
-  {
-    int u = u0 + wave, i = 0;
-    Regs cur, nxt;
-    if (u < u1) load(u, 0, cur);
-    for (; u < u1; u += 4, ++i) {
-      if (u + 4 < u1) load(u + 4, i + 1, nxt);
-      compute(u, cur);
-      cur = nxt;
-    }
-  }
-
-  // the four waves' sums: common reference maximum per row, then range by range through LDS
-  float f[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    const float ls = quarter_sum(l[mi]);
-    if (q4 == 0) {
-      m_lds[wave][16 * mi + n16] = m[mi];
-      l_lds[wave][16 * mi + n16] = ls;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    const int rr = 16 * mi + n16;
-    const float top = fmaxf(fmaxf(m_lds[0][rr], m_lds[1][rr]), fmaxf(m_lds[2][rr], m_lds[3][rr]));
-    f[mi] = exp2_hw(m[mi] - top);
-  }
-  const bool direct = it.splits == 1;
-  // thread -> row tid / (256 / BM), consecutive elements of the range
-  constexpr int TPR = 256 / BM, EPT = 32 / TPR;
-  const int orow = tid / TPR, oc = (tid % TPR) * EPT;
-  float top = kNone, sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, m_lds[w][orow]);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) sum += l_lds[w][orow] * exp2_hw(m_lds[w][orow] - top);
-  const int grow = row_base + orow;
-  const bool valid = grow < rows;
-  const int tok = grow / a.G, g = grow - tok * a.G;
-  const size_t at = (size_t)(it.q.row0 + tok) * a.Hq + h * a.G + g;
-  const size_t slot = (size_t)(it.slot + it.split) * hkv + h;
-  const float norm = sum > 0.f || sum != sum ? a.cache.v_gscale / sum : 0.f;
-  if (tid % TPR == 0 && valid) {
-    if (direct) {
-      if (a.lse) a.lse[at] = sum > 0.f || sum != sum ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
-    } else {
-      part.ml[slot * 2 * BM + orow] = top;
-      part.ml[slot * 2 * BM + BM + orow] = sum;
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < NS; ++r) {
-    __syncthreads();
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      float* dst = &o_lds[wave][16 * mi + n16][8 * q4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dst[2 * i] = o[mi][r][0][i] * f[mi];
-        dst[2 * i + 1] = o[mi][r][1][i] * f[mi];
-      }
-    }
-    __syncthreads();
-    float v[EPT];
-#pragma unroll
-    for (int e = 0; e < EPT; ++e)
-      v[e] = (o_lds[0][orow][oc + e] + o_lds[1][orow][oc + e]) + (o_lds[2][orow][oc + e] + o_lds[3][orow][oc + e]);
-    if (valid) {
-      if (direct) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + 32 * r + oc);
-#pragma unroll
-        for (int e = 0; e < EPT / 2; ++e) dst[e] = f32x2_to_bf16x2(v[2 * e] * norm, v[2 * e + 1] * norm);
-      } else {
-        float* dst = part.o + (slot * BM + orow) * D + 32 * r + oc;
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) dst[e] = v[e];
-      }
+    // the next segment: of this request, or of the next one with rows
+    left -= count;
+    if (left == 0 || sh.aligned) return;
+    first = false;
+    local += count;
+    if (local == kv_units(at.q, sh) * hkv) {
+      local = 0;
+      do {
+        at.q = lane_request(kv_request(a, s, ++at.r), 0);      // the share ends within the last request
+      } while (at.q.tiles == 0);
     }
   }
 }
@@ -662,82 +722,141 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 }
 
 // ------------------------------------------------------------------------- combine
-// Sixteen rows of one tile per workgroup: the partial sums of its splits added in split order.
-template <int D>
+// One wave per row of a cut tile: lane i reads the maximum and sum of partial i, then D / 4 lanes take four
+// elements each, 256 / D partials at a time, added in a fixed order.
+template <int D, bool SHARES>
 __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttentionProblem a, KvSchedule s, KvPartials part) {
-  const int hkv = a.cache.kv_heads, tid = threadIdx.x;
-  const int h = blockIdx.x % hkv;
-  KvItem it;
-  if (!kv_find<true>(a, s, blockIdx.x / hkv, &it)) return;
-  if (it.splits == 1) return;
-  const int row = 16 * blockIdx.y + tid / 16, grow = it.tile * s.bm + row;
-  if (grow >= it.q.n * a.G) return;
-  constexpr int EPT = D / 16;
-  const int d0 = (tid % 16) * EPT;
-  const size_t stride = (size_t)hkv * 2 * s.bm, first = ((size_t)it.slot * hkv + h) * 2 * s.bm + row;
-  float top = kNone;
-  for (int i = 0; i < it.splits; ++i) top = fmaxf(top, part.ml[first + i * stride]);
-  float sum = 0.f, v[EPT];
-#pragma unroll
-  for (int e = 0; e < EPT; ++e) v[e] = 0.f;
-  for (int i = 0; i < it.splits; ++i) {
-    const float w = exp2_hw(part.ml[first + i * stride] - top);
-    sum += w * part.ml[first + i * stride + s.bm];
-    const float4* src = reinterpret_cast<const float4*>(
-        part.o + (((size_t)(it.slot + i) * hkv + h) * s.bm + row) * D + d0);
-#pragma unroll
-    for (int e = 0; e < EPT / 4; ++e) {
-      const float4 x = src[e];
-      v[4 * e] += w * x.x;
-      v[4 * e + 1] += w * x.y;
-      v[4 * e + 2] += w * x.z;
-      v[4 * e + 3] += w * x.w;
-    }
+  const int hkv = a.cache.kv_heads, lane = threadIdx.x & 63;
+  KvRequest q;
+  int h, tile, count;
+  size_t first, step, odd;      // slots: first, then first + step*i + odd
+  if (SHARES) {
+    KvShare sh;
+    KvWhere at;
+    long long within;
+    if (!kv_locate<true>(a, s, blockIdx.x, &sh, &at, &within)) return;
+    q = at.q;
+    h = (int)within / q.tiles;
+    tile = (int)within - h * q.tiles;
+    const int units = max(1, q.hi - q.lo);
+    const long long begin = at.base + within * kv_step(q, sh), i0 = div_i64(begin, sh.chunk),
+                    i1 = div_i64(begin + units - 1, sh.chunk);
+    if (i0 == i1) return;
+    count = (int)(i1 - i0) + 1;
+    first = 2 * (size_t)i0 + 1;     // the share it begins in ends with it; the later ones begin with it
+    step = 2;
+    odd = 1;
+  } else {
+    KvItem it;
+    if (!kv_find<true>(a, s, blockIdx.x / hkv, &it)) return;
+    if (it.splits == 1) return;
+    q = it.q;
+    h = blockIdx.x % hkv;
+    tile = it.tile;
+    count = it.splits;
+    first = (size_t)it.slot * hkv + h;
+    step = hkv;
+    odd = 0;
   }
-  const bool any = sum > 0.f || sum != sum;
-  const float norm = any ? a.cache.v_gscale / sum : 0.f;
-  const int tok = grow / a.G, g = grow - tok * a.G;
-  const size_t at = (size_t)(it.q.row0 + tok) * a.Hq + h * a.G + g;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D + d0);
+  auto slot = [&](int i) { return first + step * i - (i > 0 ? odd : 0); };
+  const int rows = min(s.bm, q.n * a.G - tile * s.bm);
+  for (int row = 4 * blockIdx.y + (threadIdx.x >> 6); row < rows; row += 4 * gridDim.y) {
+    const int grow = tile * s.bm + row;
+    float top = kNone;
+    for (int i0 = 0; i0 < count; i0 += 64)
+      if (i0 + lane < count) top = fmaxf(top, part.ml[slot(i0 + lane) * 2 * s.bm + row]);
 #pragma unroll
-  for (int e = 0; e < EPT / 2; ++e) dst[e] = f32x2_to_bf16x2(v[2 * e] * norm, v[2 * e + 1] * norm);
-  if (a.lse && tid % 16 == 0)
-    a.lse[at] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    constexpr int LPR = D / 4, PER = 64 / LPR;      // lanes per partial row, partials at a time
+    const int sub = lane / LPR, d0 = 4 * (lane % LPR);
+    float sum = 0.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < count; i0 += 64) {
+      float w = 0.f;
+      if (i0 + lane < count) {
+        const float* ml = part.ml + slot(i0 + lane) * 2 * s.bm + row;
+        w = exp2_hw(ml[0] - top);
+        sum += w * ml[s.bm];
+      }
+      const int n = min(64, count - i0);
+      for (int j = 0; j < n; j += 8 * PER) {
+        f32x4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = j + k * PER + sub;
+          x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (i < n) x[k] = *reinterpret_cast<const f32x4*>(part.o + (slot(i0 + i) * s.bm + row) * D + d0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += __shfl(w, min(j + k * PER + sub, 63)) * x[k];
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+#pragma unroll
+    for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], off);
+    const bool any = sum > 0.f || sum != sum;
+    const float norm = any ? a.cache.v_gscale / sum : 0.f;
+    const int tok = grow / a.G, g = grow - tok * a.G;
+    const size_t dst = (size_t)(q.row0 + tok) * a.Hq + h * a.G + g;
+    if (sub == 0)
+      *reinterpret_cast<u32x2*>(a.out + dst * D + d0) =
+          u32x2{f32x2_to_bf16x2(v[0] * norm, v[1] * norm), f32x2_to_bf16x2(v[2] * norm, v[3] * norm)};
+    if (a.lse && lane == 0) a.lse[dst] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+  }
 }
 
 // Host side of one launch: schedule, grid and workspace.
 struct Launch {
+  bool shares;        // few-row kernel (equal shares) or tile kernel (items)
   KvSchedule s;
-  int64_t tiles;    // bound on the row tiles of a kv head
-  int64_t items;    // bound on the items of a kv head
+  int64_t grid;       // workgroups
+  int64_t tiles;      // bound on the row tiles over all heads
   size_t o_bytes, bytes;
 };
 
-// bm rows per tile, about `target` items over all heads.  With chunk >= sum(tiles*units)/target the
-// items are sum tiles*ceil(units/chunk) <= tiles + target; those of requests with two splits or more
-// number at most twice target.
-Launch plan_launch(const KvSchedule& s, int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D) {
-  Launch p{};
-  p.s = s;
-  p.s.target = std::max(1, s.target / hkv);
-  p.tiles = std::min((int64_t)R, (int64_t)T) + (int64_t)T * G / s.bm;
-  p.items = p.tiles + p.s.target;
-  const size_t slots = 2 * (size_t)p.s.target * hkv;
-  p.o_bytes = slots * s.bm * D * 4;
-  p.bytes = p.o_bytes + slots * 2 * s.bm * 4;
-  return p;
-}
-
-constexpr int kRowsTarget = 1024;      // items of the few-row kernel over all heads
+constexpr int kCus = 256;              // compute units of the card
 constexpr int kRowsMinChunk = 4;       // units: one per wave
 constexpr int kTilesTarget = 512;
 constexpr int kTilesMinChunk = 16;
 constexpr int kRowsSplit = 64;         // requests of more rows go to the tile kernel where both run
 
+int rows_resident(int D, int bm) {
+  if (D == 64) return bm == 16 ? rows_occupancy<64, 1>() : rows_occupancy<64, 2>();
+  if (D == 128) return bm == 16 ? rows_occupancy<128, 1>() : rows_occupancy<128, 2>();
+  return bm == 16 ? rows_occupancy<256, 1>() : rows_occupancy<256, 2>();
+}
+
+// Requests with min_rows < rows <= max_rows in tiles of bm rows.  Few rows: as many shares as workgroups
+// are resident at once.  Many rows: with chunk >= sum(tiles * units) / target the items are
+// sum tiles * ceil(units / chunk) <= tiles + target per kv head; those of requests with two splits or
+// more number at most twice target.
+Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, int32_t R, int32_t G, int32_t hkv,
+                   int32_t D) {
+  Launch p{};
+  p.shares = shares;
+  const int64_t tiles = std::min((int64_t)R, (int64_t)T) + (int64_t)T * G / bm;
+  p.tiles = tiles * hkv;
+  size_t slots;
+  if (shares) {
+    p.s = KvSchedule{bm, kCus * rows_resident(D, bm), kRowsMinChunk, min_rows, max_rows};
+    p.grid = p.s.target;
+    slots = 2 * (size_t)p.s.target;
+  } else {
+    p.s = KvSchedule{bm, std::max(1, kTilesTarget / hkv), kTilesMinChunk, min_rows, max_rows};
+    p.grid = (tiles + p.s.target) * hkv;
+    slots = 2 * (size_t)p.s.target * hkv;
+  }
+  p.o_bytes = slots * bm * D * 4;
+  p.bytes = p.o_bytes + slots * 2 * bm * 4;
+  return p;
+}
+
 // The launches of a call: the few-row kernel, the tile kernel, or both, each on its requests.
 struct Launches {
   int n;
-  bool tiles[2];
   Launch l[2];
 };
 
@@ -746,16 +865,10 @@ Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D) 
   const int64_t rows = (int64_t)T * G;
   const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
   const bool few = !tiles || R > 1;
-  if (tiles) {
-    const int bm = D == 256 ? 128 : 256;
-    x.tiles[x.n] = true;
-    x.l[x.n++] = plan_launch(KvSchedule{bm, kTilesTarget, kTilesMinChunk, few ? kRowsSplit : 0, 0x7FFFFFFF}, T, R, G,
-                             hkv, D);
-  }
+  if (tiles) x.l[x.n++] = plan_launch(false, D == 256 ? 128 : 256, few ? kRowsSplit : 0, 0x7FFFFFFF, T, R, G, hkv, D);
   if (few) {
     const int bm = tiles || rows > 16 * (int64_t)R ? 32 : 16;
-    x.l[x.n++] = plan_launch(KvSchedule{bm, kRowsTarget, kRowsMinChunk, 0, tiles ? kRowsSplit : 0x7FFFFFFF}, T, R, G,
-                             hkv, D);
+    x.l[x.n++] = plan_launch(true, bm, 0, tiles ? kRowsSplit : 0x7FFFFFFF, T, R, G, hkv, D);
   }
   return x;
 }
@@ -774,7 +887,7 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
   const Launches x = plan_launches(a.T, a.R, a.G, hkv, D);
   for (int i = 0; i < x.n; ++i)
-    if (x.l[i].items * hkv > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
+    if (x.l[i].grid > 0x7FFFFFFFLL || x.l[i].tiles > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < x.n; ++i) {
     const Launch& p = x.l[i];
     KvPartials part{static_cast<float*>(workspace), nullptr};
@@ -782,15 +895,17 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
     with_head_dim(D, [&](auto tag) {
       constexpr int DD = decltype(tag)::value;
       constexpr int NW = DD == 256 ? 4 : 8;
-      const dim3 grid((unsigned)(p.items * hkv));
-      if (x.tiles[i])
+      const dim3 grid((unsigned)p.grid), rows((unsigned)p.tiles, p.shares ? p.s.bm / 8 : 4);
+      if (!p.shares) {
         hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, NW>), grid, dim3(64 * NW), 0, stream, a, p.s, part);
-      else if (p.s.bm == 16)
-        hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1>), grid, dim3(256), 0, stream, a, p.s, part);
-      else
-        hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 2>), grid, dim3(256), 0, stream, a, p.s, part);
-      hipLaunchKernelGGL(kv_combine_kernel<DD>, dim3((unsigned)(p.tiles * hkv), p.s.bm / 16), dim3(256), 0, stream, a,
-                         p.s, part);
+        hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
+      } else {
+        if (p.s.bm == 16)
+          hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1>), grid, dim3(256), 0, stream, a, p.s, part);
+        else
+          hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 2>), grid, dim3(256), 0, stream, a, p.s, part);
+        hipLaunchKernelGGL((kv_combine_kernel<DD, true>), rows, dim3(256), 0, stream, a, p.s, part);
+      }
     });
     if (moe_status_t st = launch_status()) return st;
   }

@@ -1,5 +1,7 @@
-// Work items of the attention over the paged cache, found on the device from the request lengths.
+// Work of the attention over the paged cache, divided on the device from the request lengths: equal
+// shares of a linear order (few rows per request, kv_locate), or items (many rows, kv_find).
 //
+// Items:
 // A request r with n query tokens has n * G rows per kv head (row = token * G + head of the group), cut
 // into tiles of BM rows, and the units (32 positions) [lo, hi) that its rows see.  The units are cut
 // into splits of C units, C chosen so that the items of one kv head number about `target`:
@@ -10,7 +12,9 @@
 // list in memory, no atomics).
 #pragma once
 
-#include "common.h"
+#include <type_traits>
+
+#include "device_util.h"
 
 namespace moe {
 namespace {
@@ -56,10 +60,152 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttentionProblem& a, con
   return q;
 }
 
-__device__ __forceinline__ long long wave_sum_i64(long long v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+// Inclusive wave scan (lane order) of 64-bit integers, and a quotient that is a 32-bit one where it can be.
+__device__ __forceinline__ long long wave_scan_i64(long long v) {
+  auto step = [&](auto dpp) { v += dpp(v); };
+  auto move = [](long long x, auto ctrl, auto mask) {
+    constexpr int C = decltype(ctrl)::value, M = decltype(mask)::value;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, C, M, 0xF, M == 0xF);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)((uint64_t)x >> 32), C, M, 0xF, M == 0xF);
+    return (long long)(((uint64_t)hi << 32) | lo);
+  };
+  using All = std::integral_constant<int, 0xF>;
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x111>{}, All{}); });   // row_shr:1
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x112>{}, All{}); });
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x114>{}, All{}); });
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x118>{}, All{}); });
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{}); });
+  step([&](long long x) { return move(x, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{}); });
   return v;
+}
+__device__ __forceinline__ long long lane_i64(long long v, int src) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, src);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), src);
+  return (long long)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ long long wave_sum_i64(long long v) { return lane_i64(wave_scan_i64(v), 63); }
+__device__ __forceinline__ long long div_i64(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// Linear order of a launch's work: requests in order, in each its kv heads, row tiles and units
+// (at least one unit per tile, so that a row that sees nothing is written too).  Workgroup i of `target`
+// takes the units [i * chunk, (i + 1) * chunk) of that order: an equal share, whatever the lengths.
+// A tile cut between workgroups leaves one partial sum per workgroup; a workgroup has at most two
+// unfinished tiles, the one it begins with (slot 2i) and the one it ends with (slot 2i + 1).
+// Aligned: each tile's units are padded to whole chunks in the order, so that no workgroup crosses from
+// one tile into the next (which costs it about as much as kSwitch units: the new rows, the table and the
+// first units arrive one after the other).  Taken where the chunks that padding needs, work / (target -
+// tiles), are at most that much longer: with few tiles, that is, while many tiles of unequal lengths
+// are shared out evenly.
+struct KvShare {
+  long long total, chunk;
+  bool aligned;
+};
+struct KvWhere {
+  int r;
+  KvRequest q;
+  long long base;    // order position of the request's first unit
+};
+constexpr int kSwitch = 8;
+// units of a tile, its length in the order, and a request's per kv head
+__device__ __forceinline__ long long kv_step(const KvRequest& q, const KvShare& sh) {
+  const int units = max(1, q.hi - q.lo);
+  return sh.aligned ? div_i64(units + sh.chunk - 1, sh.chunk) * sh.chunk : units;
+}
+__device__ __forceinline__ long long kv_units(const KvRequest& q, const KvShare& sh) {
+  return q.tiles * kv_step(q, sh);
+}
+
+__device__ __forceinline__ KvRequest lane_request(const KvRequest& q, int src) {
+  KvRequest o;
+  o.n = __builtin_amdgcn_readlane(q.n, src);
+  o.row0 = __builtin_amdgcn_readlane(q.row0, src);
+  o.len = __builtin_amdgcn_readlane(q.len, src);
+  o.tiles = __builtin_amdgcn_readlane(q.tiles, src);
+  o.lo = __builtin_amdgcn_readlane(q.lo, src);
+  o.hi = __builtin_amdgcn_readlane(q.hi, src);
+  return o;
+}
+
+__device__ __forceinline__ int wave_scan(int v) { return wave_inclusive_scan(v); }
+__device__ __forceinline__ long long wave_scan(long long v) { return wave_scan_i64(v); }
+__device__ __forceinline__ int lane_value(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
+__device__ __forceinline__ long long lane_value(long long v, int src) { return lane_i64(v, src); }
+
+// kv_locate in integers of type I, which hold the whole work; `q` is lane r's request when R <= 64.
+template <bool BY_TILE, typename I>
+__device__ __forceinline__ bool kv_locate_in(const KvAttentionProblem& a, const KvSchedule& s, int index, KvRequest q,
+                                             I work, I all_tiles, KvShare* sh, KvWhere* out, long long* within) {
+  const int lane = threadIdx.x & 63, hkv = a.cache.kv_heads;
+  auto quot = [](I x, I y) { return (I)(sizeof(I) == 4 ? (uint32_t)x / (uint32_t)y : div_i64(x, y)); };
+  // whole rounds of the four waves
+  auto chunk_of = [&](I workgroups) { return max((I)s.min_chunk, (quot(work + workgroups - 1, workgroups) + 3) & ~(I)3); };
+  I chunk = chunk_of(s.target);
+  bool aligned = false;
+  if (all_tiles < s.target) {
+    const I longer = chunk_of(s.target - all_tiles);
+    aligned = longer <= chunk + kSwitch;
+    if (aligned) chunk = longer;
+  }
+  sh->chunk = chunk;
+  sh->aligned = aligned;
+  const long long at = BY_TILE ? index : (long long)index * sh->chunk;
+  I base = 0, tiles = 0;
+  bool found = false;
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    if (a.R > 64) {
+      q = KvRequest{};
+      if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
+    }
+    const I units = max(1, q.hi - q.lo), step = aligned ? quot(units + chunk - 1, chunk) * chunk : units;
+    const I mine = step * q.tiles * hkv, scan = wave_scan(mine);
+    I key = scan, own = mine, first = base;
+    if (BY_TILE) {
+      own = (I)q.tiles * hkv;
+      key = wave_scan(own);
+      first = tiles;
+    }
+    const I excl = first + key - own;
+    const uint64_t hit = found ? 0 : __ballot(excl <= at && at < excl + own);
+    if (hit) {
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      out->r = r0 + src;
+      out->q = lane_request(q, src);
+      out->base = base + lane_value(scan - mine, src);
+      *within = at - lane_value(excl, src);
+      found = true;
+      if (BY_TILE) return true;      // the total is not needed
+    }
+    base += lane_value(scan, 63);
+    if (BY_TILE) tiles += lane_value(key, 63);
+  }
+  sh->total = base;
+  return found;
+}
+
+// The shares, and the request that holds order position index * chunk (BY_TILE: tile `index` of the
+// launch, counted over requests, heads and tiles), with the place in it.  One whole wave; false past the
+// end.  Up to 64 requests of less than 2^23 units each go the short way, in 32 bits (padding to
+// chunks at most doubles the work).
+template <bool BY_TILE>
+__device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvSchedule& s, int index, KvShare* sh,
+                                          KvWhere* out, long long* within) {
+  const int lane = threadIdx.x & 63, hkv = a.cache.kv_heads;
+  KvRequest q{};
+  long long work = 0, all_tiles = 0;
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    q = KvRequest{};
+    if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
+    work += (long long)q.tiles * max(1, q.hi - q.lo);
+    all_tiles += q.tiles;
+  }
+  work *= hkv;
+  all_tiles *= hkv;
+  if (a.R <= 64 && !__any(work >= (1 << 23) || all_tiles >= (1 << 23)))
+    return kv_locate_in<BY_TILE, int>(a, s, index, q, lane_value(wave_scan((int)work), 63),
+                                      lane_value(wave_scan((int)all_tiles), 63), sh, out, within);
+  return kv_locate_in<BY_TILE, long long>(a, s, index, q, wave_sum_i64(work), wave_sum_i64(all_tiles), sh, out, within);
 }
 
 // Item `index` (BY_TILE: all splits of tile `index`); false past the last.  One whole wave.
