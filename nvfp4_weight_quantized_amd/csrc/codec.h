@@ -67,5 +67,48 @@ __device__ __forceinline__ void quantize_group16(const float (&v)[16], float d, 
   }
 }
 
+// quantize_group16 with the hardware conversions, bit for bit, for 2^-64 <= d <= 2^64 (every
+// intermediate below that decides a code is then a normal number).  v_cvt_pk_fp8_f32 and
+// v_cvt_scalef32_pk_fp4_f32 round to nearest, ties to even.  The quotients v / (s*d) are correctly rounded:
+// with y the correctly rounded reciprocal, two steps q += y * (v - q * sd), the residual exact in the
+// fused multiply-add, leave the nearest value (Markstein's theorem: the first step brings q within one
+// unit in the last place, the second rounds it correctly).  Values are first limited to 6*s*d, which
+// keeps infinities out and turns a NaN into the largest code, as the general routine does; adding +0
+// turns -0 into +0, whose code has no sign.
+__device__ __forceinline__ void quantize_group16_fast(const float (&v)[16], float d, uint32_t* lo, uint32_t* hi,
+                                                      uint32_t* scode) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  const float t = fminf(__fdiv_rn(amax, __fmul_rn(6.0f, d)), 448.0f);
+  const uint32_t sc = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0xFFu;
+  const float s = __builtin_amdgcn_cvt_f32_fp8((int)sc, 0);
+  const float sd = __fmul_rn(s, d);
+  *scode = sc;
+  *lo = *hi = 0;
+  if (sd > 0.f) {
+    const float y = __fdiv_rn(1.0f, sd), top = 6.0f * sd;
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = fmaxf(fminf(v[i], top), -top);
+      float z = x * y;
+      z = __fmaf_rn(__fmaf_rn(-z, sd, x), y, z);
+      z = __fmaf_rn(__fmaf_rn(-z, sd, x), y, z);
+      q[i] = z + 0.0f;
+    }
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], q[8 * k], q[8 * k + 1], 1.0f, 0);
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], q[8 * k + 2], q[8 * k + 3], 1.0f, 1);
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], q[8 * k + 4], q[8 * k + 5], 1.0f, 2);
+      w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], q[8 * k + 6], q[8 * k + 7], 1.0f, 3);
+    }
+    *lo = w[0];
+    *hi = w[1];
+  }
+}
+
 }  // namespace
 }  // namespace moe

@@ -115,25 +115,15 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
 }
 
 // ------------------------------------------------------------------------------------ append
-// One thread per (token, head, K or V, 16-element group).
-template <int D>
-__global__ __launch_bounds__(256) void kv_append_kernel(moe_nvfp4_kv_cache_t c, const uint16_t* __restrict__ k,
-                                                        const uint16_t* __restrict__ v, int64_t k_stride,
-                                                        int64_t v_stride, const int32_t* __restrict__ slots, int T) {
-  using U = KvUnit<D>;
-  constexpr int NG = D / 16;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int per_token = 2 * c.kv_heads * NG;
-  const long long tl = i / per_token;
-  if (tl >= T) return;
-  const int t = (int)tl, rest = (int)(i % per_token);
-  const int g = rest % NG, h = (rest / NG) % c.kv_heads;
-  const bool is_v = rest / NG >= c.kv_heads;
-  const int slot = slots[t];
-  if (slot < 0 || slot >= c.num_pages * c.page_size) return;
-  const uint16_t* row = is_v ? v + t * v_stride : k + t * k_stride;
-  const uint4* src = reinterpret_cast<const uint4*>(row + h * D + g * 16);
-  float x[16];
+// One thread per (window of W consecutive rows, head, K or V, 16-element group).  The value codes of four
+// positions 4c..4c+3 share dwords, so W = 4 quantizes such a quad together and stores dwords: the thread
+// takes every quad that begins among its W rows (a row whose slot is a multiple of 4 or does not follow
+// the row before it), with the rows after it that continue it, also those of the next window.  W = 1
+// stores bytes, row by row: for steps of few rows, where the threads of the quads would not fill the card.
+constexpr long long kAppendQuadThreads = 1 << 18;      // rows * groups from which quads are taken
+
+__device__ __forceinline__ void load_group16(const uint16_t* __restrict__ row, float (&x)[16]) {
+  const uint4* src = reinterpret_cast<const uint4*>(row);
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     const uint4 w = src[a];
@@ -144,59 +134,152 @@ __global__ __launch_bounds__(256) void kv_append_kernel(moe_nvfp4_kv_cache_t c, 
       x[8 * a + 2 * b + 1] = __uint_as_float(u[b] & 0xFFFF0000u);
     }
   }
-  uint32_t lo, hi, sc;
-  quantize_group16(x, is_v ? c.v_gscale : c.k_gscale, &lo, &hi, &sc);
-  uint8_t* unit = c.pages + kv_unit_offset<D>(c, slot, h);
-  const int p = slot % kKvUnit;
-  if (is_v) {
+}
+
+template <int D, int W>
+__global__ __launch_bounds__(256) void kv_append_kernel(moe_nvfp4_kv_cache_t c, const uint16_t* __restrict__ k,
+                                                        const uint16_t* __restrict__ v, int64_t k_stride,
+                                                        int64_t v_stride, const int32_t* __restrict__ slots, int T) {
+  using U = KvUnit<D>;
+  constexpr int NG = D / 16;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int per = 2 * c.kv_heads * NG;
+  const long long wl = i / per;
+  if (wl * W >= T) return;
+  const int t0 = (int)wl * W, rest = (int)(i % per);
+  const int g = rest % NG, h = (rest / NG) % c.kv_heads;
+  const bool is_v = rest / NG >= c.kv_heads;
+  const int cap = c.num_pages * c.page_size;
+  const uint16_t* src = (is_v ? v : k) + h * D + g * 16;
+  const int64_t stride = is_v ? v_stride : k_stride;
+  const float d = is_v ? c.v_gscale : c.k_gscale;
+  for (int t = t0; t < min(t0 + W, T);) {
+    const int s = slots[t];
+    int n = 1;
+    if (s < 0 || s >= cap) {
+      ++t;
+      continue;
+    }
+    if (W > 1) {
+      if ((s & 3) != 0 && t > 0 && slots[t - 1] == s - 1) {      // the quad's first row takes this one
+        ++t;
+        continue;
+      }
+      while (n < 4 && ((s + n) & 3) != 0 && t + n < T && slots[t + n] == s + n) ++n;
+    }
+    uint8_t* unit = c.pages + kv_unit_offset<D>(c, s, h);
+    const int p = s % kKvUnit;
+    uint32_t lo[W], hi[W], sc[W];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) unit[U::v_byte(p, 8 * g + b)] = (uint8_t)((b < 4 ? lo >> (8 * b) : hi >> (8 * b - 32)) & 255u);
-    unit[U::v_scale(p, g)] = (uint8_t)sc;
-  } else {
-    *reinterpret_cast<uint32_t*>(unit + U::k_word(p, 2 * g)) = lo;
-    *reinterpret_cast<uint32_t*>(unit + U::k_word(p, 2 * g + 1)) = hi;
-    unit[U::k_scale(p, g)] = (uint8_t)sc;
+    for (int r = 0; r < W; ++r) {
+      if (r < n) {
+        float x[16];
+        load_group16(src + (int64_t)(t + r) * stride, x);
+        quantize_group16_fast(x, d, &lo[r], &hi[r], &sc[r]);
+      }
+    }
+    if (!is_v) {
+#pragma unroll
+      for (int r = 0; r < W; ++r) {
+        if (r < n) {
+          *reinterpret_cast<uint32_t*>(unit + U::k_word(p + r, 2 * g)) = lo[r];
+          *reinterpret_cast<uint32_t*>(unit + U::k_word(p + r, 2 * g + 1)) = hi[r];
+          unit[U::k_scale(p + r, g)] = (uint8_t)sc[r];
+        }
+      }
+    } else if (W == 4 && n == 4) {
+      // byte b of the four rows' words -> one dword
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const uint32_t(&w)[W] = b < 4 ? lo : hi;
+        const uint32_t sel = 0x0C0C0400u + 0x0101u * (b & 3);      // byte b & 3 of the second and of the first operand
+        const uint32_t a01 = __builtin_amdgcn_perm(w[1 % W], w[0], sel), a23 = __builtin_amdgcn_perm(w[3 % W], w[2 % W], sel);
+        *reinterpret_cast<uint32_t*>(unit + U::v_byte(p, 8 * g + b)) = a01 | (a23 << 16);
+      }
+      *reinterpret_cast<uint32_t*>(unit + U::v_scale(p, g)) = sc[0] | (sc[1 % W] << 8) | (sc[2 % W] << 16) | (sc[3 % W] << 24);
+    } else {
+#pragma unroll
+      for (int r = 0; r < W; ++r) {
+        if (r < n) {
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            unit[U::v_byte(p + r, 8 * g + b)] = (uint8_t)((b < 4 ? lo[r] >> (8 * b) : hi[r] >> (8 * b - 32)) & 255u);
+          unit[U::v_scale(p + r, g)] = (uint8_t)sc[r];
+        }
+      }
+    }
+    t += n;
   }
 }
 
 // ------------------------------------------------------------------------------------ gather
-__device__ __forceinline__ float e2m1_f32(uint32_t code) {
-  const uint32_t m = code & 7u;
-  const float v = m < 4u ? 0.5f * (float)m : (m < 6u ? (float)(m - 2u) : (m == 6u ? 4.f : 6.f));
-  return (code & 8u) ? -v : v;
-}
+// A workgroup takes 32 rows of the list for one head.  Where they lie in at most two units (consecutive
+// positions, whatever their alignment), both units come to LDS whole and in order and every thread
+// assembles 16-byte pieces of the output rows from there; otherwise the pieces are assembled from global
+// memory.
+constexpr int kGatherRows = 32;
 
 template <int D>
 __global__ __launch_bounds__(256) void kv_gather_kernel(moe_nvfp4_kv_cache_t c, const int32_t* __restrict__ slots,
                                                         int n, uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
   using U = KvUnit<D>;
-  constexpr int NG = D / 16;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int per_token = 2 * c.kv_heads * NG;
-  const long long tl = i / per_token;
-  if (tl >= n) return;
-  const int t = (int)tl, rest = (int)(i % per_token);
-  const int g = rest % NG, h = (rest / NG) % c.kv_heads;
-  const bool is_v = rest / NG >= c.kv_heads;
-  uint16_t* dst = (is_v ? v : k) + ((size_t)t * c.kv_heads + h) * D + g * 16;
-  const int slot = slots[t];
-  uint32_t w[8];
-  if (slot < 0 || slot >= c.num_pages * c.page_size) {
-#pragma unroll
-    for (int b = 0; b < 8; ++b) w[b] = 0x7FC07FC0u;
-  } else {
-    const uint8_t* unit = c.pages + kv_unit_offset<D>(c, slot, h);
-    const int p = slot % kKvUnit;
-    const float s = __builtin_amdgcn_cvt_f32_fp8((int)unit[is_v ? U::v_scale(p, g) : U::k_scale(p, g)], 0);
-    const float d = is_v ? c.v_gscale : c.k_gscale;
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const uint32_t byte = is_v ? unit[U::v_byte(p, 8 * g + b)] : unit[U::k_word(p, 2 * g + (b >> 2)) + (b & 3)];
-      w[b] = f32x2_to_bf16x2(e2m1_f32(byte & 15u) * s * d, e2m1_f32(byte >> 4) * s * d);
+  __shared__ __align__(16) uint8_t lds[2 * U::kBytes];
+  __shared__ int row_slot[kGatherRows];
+  const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.y;
+  const int t0 = blockIdx.x * kGatherRows, rows = min(kGatherRows, n - t0);
+  const int cap = c.num_pages * c.page_size;
+  // every wave: lane r holds row r's slot (-1 outside the cache)
+  int slot = -1;
+  if (lane < rows) slot = slots[t0 + lane];
+  if (slot < 0 || slot >= cap) slot = -1;
+  if (tid < kGatherRows) row_slot[tid] = slot;
+  const uint64_t have = __ballot(slot >= 0);
+  int ua = 0, ub = 0;          // units of the first and the last row inside the cache
+  if (have) {
+    ua = __builtin_amdgcn_readlane(slot, __ffsll((unsigned long long)have) - 1) / kKvUnit;
+    ub = __builtin_amdgcn_readlane(slot, 63 - __clzll((long long)have)) / kKvUnit;
+  }
+  const int unit = slot / kKvUnit;
+  const bool two = !__any(slot >= 0 && unit != ua && unit != ub) && rows > 1;
+  if (two) {
+    const uint8_t* pa = c.pages + kv_unit_offset<D>(c, ua * kKvUnit, h);
+    const uint8_t* pb = c.pages + kv_unit_offset<D>(c, ub * kKvUnit, h);
+    for (int i = tid; i < U::kBytes / 16; i += 256) {
+      reinterpret_cast<uint4*>(lds)[i] = reinterpret_cast<const uint4*>(pa)[i];
+      if (ub != ua) reinterpret_cast<uint4*>(lds + U::kBytes)[i] = reinterpret_cast<const uint4*>(pb)[i];
     }
   }
-  reinterpret_cast<uint4*>(dst)[0] = uint4{w[0], w[1], w[2], w[3]};
-  reinterpret_cast<uint4*>(dst)[1] = uint4{w[4], w[5], w[6], w[7]};
+  __syncthreads();
+  // pieces of eight elements: D / 8 per row of K, then of V
+  constexpr int PIECES = D / 8;
+  for (int i = tid; i < 2 * rows * PIECES; i += 256) {
+    const bool is_v = i >= rows * PIECES;
+    const int x = is_v ? i - rows * PIECES : i, r = x / PIECES, g8 = x % PIECES;
+    const int s = row_slot[r];
+    uint32_t w[4];
+    if (s < 0) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w[b] = 0x7FC07FC0u;
+    } else {
+      const uint8_t* u = two ? lds + (s / kKvUnit == ua ? 0 : U::kBytes) : c.pages + kv_unit_offset<D>(c, s, h);
+      const int p = s % kKvUnit;
+      uint32_t codes;
+      if (is_v)
+        codes = (uint32_t)u[U::v_byte(p, 4 * g8)] | ((uint32_t)u[U::v_byte(p, 4 * g8 + 1)] << 8) |
+                ((uint32_t)u[U::v_byte(p, 4 * g8 + 2)] << 16) | ((uint32_t)u[U::v_byte(p, 4 * g8 + 3)] << 24);
+      else
+        codes = *reinterpret_cast<const uint32_t*>(u + U::k_word(p, g8));
+      const float sc = __builtin_amdgcn_cvt_f32_fp8((int)u[is_v ? U::v_scale(p, g8 >> 1) : U::k_scale(p, g8 >> 1)], 0);
+      const float d = is_v ? c.v_gscale : c.k_gscale;
+      const f32x2 e[4] = {
+          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
+          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3)};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w[b] = f32x2_to_bf16x2(e[b][0] * sc * d, e[b][1] * sc * d);
+    }
+    *reinterpret_cast<uint4*>((is_v ? v : k) + ((size_t)(t0 + r) * c.kv_heads + h) * D + 8 * g8) =
+        uint4{w[0], w[1], w[2], w[3]};
+  }
 }
 
 }  // namespace
@@ -214,22 +297,28 @@ moe_status_t launch_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int
 
 moe_status_t launch_kv_append(const moe_nvfp4_kv_cache_t& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                               int64_t v_stride, const int32_t* slots, int32_t T, hipStream_t stream) {
-  const long long total = (long long)T * 2 * c.kv_heads * (c.head_dim / 16), blocks = (total + 255) / 256;
+  const long long per = 2LL * c.kv_heads * (c.head_dim / 16);
+  const bool quads = T * per >= kAppendQuadThreads;
+  const long long total = (quads ? (T + 3LL) / 4 : T) * per, blocks = (total + 255) / 256;
   if (blocks > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   with_head_dim(c.head_dim, [&](auto tag) {
-    hipLaunchKernelGGL(kv_append_kernel<decltype(tag)::value>, dim3((unsigned)blocks), dim3(256), 0, stream, c, k, v,
-                       k_stride, v_stride, slots, T);
+    constexpr int D = decltype(tag)::value;
+    if (quads)
+      hipLaunchKernelGGL((kv_append_kernel<D, 4>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, v, k_stride,
+                         v_stride, slots, T);
+    else
+      hipLaunchKernelGGL((kv_append_kernel<D, 1>), dim3((unsigned)blocks), dim3(256), 0, stream, c, k, v, k_stride,
+                         v_stride, slots, T);
   });
   return launch_status();
 }
 
 moe_status_t launch_kv_gather(const moe_nvfp4_kv_cache_t& c, const int32_t* slots, int32_t n, uint16_t* k,
                               uint16_t* v, hipStream_t stream) {
-  const long long total = (long long)n * 2 * c.kv_heads * (c.head_dim / 16), blocks = (total + 255) / 256;
-  if (blocks > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   with_head_dim(c.head_dim, [&](auto tag) {
-    hipLaunchKernelGGL(kv_gather_kernel<decltype(tag)::value>, dim3((unsigned)blocks), dim3(256), 0, stream, c, slots,
-                       n, k, v);
+    hipLaunchKernelGGL(kv_gather_kernel<decltype(tag)::value>,
+                       dim3((unsigned)(((int64_t)n + kGatherRows - 1) / kGatherRows), c.kv_heads), dim3(256), 0, stream,
+                       c, slots, n, k, v);
   });
   return launch_status();
 }

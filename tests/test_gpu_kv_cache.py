@@ -100,7 +100,7 @@ def _rows(rng, t, heads, dim):
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("heads,page,t", [(1, 32, 1), (3, 96, 37), (8, 64, 200), (2, 256, 515)])
+@pytest.mark.parametrize("heads,page,t", [(1, 32, 1), (3, 96, 37), (8, 64, 200), (2, 256, 515), (8, 128, 2051)])
 @pytest.mark.parametrize("d_k,d_v", [(1.0, 0.0625), (0.0371, 3.1e-3)])
 def test_append_writes_the_oracles_bytes(dim, heads, page, t, d_k, d_v):
     rng = np.random.default_rng(dim + heads + t)
@@ -133,6 +133,33 @@ def test_append_writes_the_oracles_bytes(dim, heads, page, t, d_k, d_v):
     assert np.array_equal(p_ref.cpu().numpy(), pk) and np.array_equal(s_ref.cpu().numpy(), sk)
 
 
+@pytest.mark.parametrize("d", [1.0, 2.0 ** -64, 2.0 ** 64, 3.3e-4, 0.0371, 1.0 / 2688.0])
+def test_append_of_every_largest_magnitude(d):
+    """Groups whose largest element runs over every finite bf16 magnitude, the others random below it or
+    on the midpoints of the E2M1 grid: scales and codes bit for bit."""
+    d = float(np.float32(d))
+    rng = np.random.default_rng(7)
+    bits = np.arange(0x7F80, dtype=np.uint16)
+    top = omoe.bf16_to_float(bits)
+    t, dim, page = len(top) // 4, 64, 256
+    x = rng.uniform(-1, 1, (t, 1, dim))
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) / 6
+    x[::2, 0, 1::2] = rng.choice(ties, (len(x[::2]), dim // 2)) * rng.choice([-1, 1], (len(x[::2]), dim // 2))
+    x[:, :, 0::16] = 1.0
+    with np.errstate(over="ignore"):
+        x = omoe.bf16_to_float(oa4.float_to_bf16_bits(x * np.repeat(top.reshape(t, 4), 16, 1)[:, None, :]))
+    n_pages = -(-t // page)
+    slots = np.arange(t, dtype=np.int32)
+    want = okv.new_pages(n_pages, page, 1, dim)
+    with np.errstate(over="ignore", under="ignore"):
+        okv.append(want, page, x, slots, d, False)
+        okv.append(want, page, x, slots, d, True)
+    cache = kv.NvFp4KvCache.allocate(n_pages, page, 1, dim, d, d)
+    kv.kv_append(cache, kh.to_bf16(x), kh.to_bf16(x), _i32(slots))
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+    assert len(np.unique(want[..., 32 * dim:])) > 100 or d > 1e6 or d < 1e-6
+
+
 def test_append_of_nonfinite_rows_stays_finite():
     """Infinities saturate, a NaN takes the code of 6: the bytes of the activation quantizer."""
     dim, page = 64, 32
@@ -151,12 +178,16 @@ def test_append_of_nonfinite_rows_stays_finite():
         assert np.all(np.isfinite(got)) and np.array_equal(got, want)
 
 
-@pytest.mark.parametrize("dim,heads,page,n", [(64, 1, 32, 1), (64, 5, 96, 77), (128, 8, 64, 300), (256, 2, 128, 129)])
-def test_gather_matches_the_decoded_cache(dim, heads, page, n):
+@pytest.mark.parametrize("dim,heads,page,n", [(64, 1, 32, 1), (64, 5, 96, 77), (128, 8, 64, 300), (256, 2, 128, 129),
+                                              (64, 2, 64, 29), (64, 1, 256, 31), (128, 3, 32, 61)])
+@pytest.mark.parametrize("runs", [False, True])
+def test_gather_matches_the_decoded_cache(dim, heads, page, n, runs):
     rng = np.random.default_rng(n)
     pages = rng.integers(0, 256, (5, heads, page // 32, 36 * dim)).astype(np.uint8)
     pages[..., 32 * dim:] &= 0x7E                  # no NaN scale
     slots = rng.integers(0, 5 * page, n).astype(np.int32)   # any order, repeats
+    if runs:                                                # positions 5.. of a request, as a prefix is read
+        slots = ((np.array([3, 0, 4, 1, 2])[(np.arange(n) + 5) // page % 5]) * page + (np.arange(n) + 5) % page).astype(np.int32)
     d_k, d_v = float(np.float32(0.0371)), 2.0 ** -7
     cache = kv.NvFp4KvCache(torch.from_numpy(pages).to(DEV), page, d_k, d_v)
     k, v = kv.kv_gather(cache, _i32(slots))
