@@ -13,7 +13,6 @@ enqueues kernels on the current stream of its tensors' device and can be capture
 from __future__ import annotations
 
 import contextlib
-import ctypes
 import math
 from typing import NamedTuple, Optional
 
@@ -26,15 +25,24 @@ _UNIT = 32              # positions per unit of a page
 HEAD_DIMS = (64, 128, 256)
 
 
-def _on(dev: torch.device):
-    """The context in which a launch goes to ``dev`` (nothing to do on the current device)."""
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+_I32, _BF16 = torch.int32, torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream      # device index -> hipStream_t
+_NOTHING = contextlib.nullcontext()
 
 
-def _raw_stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _on(index: int):
+    """The context in which a launch goes to GPU ``index`` (nothing to do on the current one)."""
+    return _NOTHING if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+def _ints(t: torch.Tensor, name: str, ndim: int, dev: Optional[torch.device] = None) -> torch.device:
+    """A contiguous int32 GPU tensor (on ``dev``, when given); its device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.is_cuda and t.dim() == ndim and t.is_contiguous()):
+        _need(t, name, _I32, ndim)
+    d = t.device
+    if dev is not None and d != dev:
+        raise ValueError(f"{name}: on {d}, expected {dev}")
+    return d
 
 
 class NvFp4KvCache:
@@ -45,7 +53,7 @@ class NvFp4KvCache:
     (a cached element is e2m1 * e4m3 * gscale).  The content of new pages does not matter: positions
     past a request's length are never used.
     """
-    __slots__ = ("pages", "page_size", "k_gscale", "v_gscale", "_struct")
+    __slots__ = ("pages", "page_size", "k_gscale", "v_gscale", "_struct", "_dev")
 
     def __init__(self, pages: torch.Tensor, page_size: int, k_gscale: float = 1.0, v_gscale: float = 1.0):
         _need(pages, "pages", torch.uint8, 4)
@@ -61,6 +69,7 @@ class NvFp4KvCache:
                 raise ValueError(f"{name}: a dequant global scale lies in [2^-64, 2^64], got {d!r}")
         self.pages, self.page_size, self.k_gscale, self.v_gscale = pages, page_size, float(k_gscale), float(v_gscale)
         self._struct = L.KvCache(p, page_size, h, b // 36, k_gscale, v_gscale, pages.data_ptr())
+        self._dev = pages.device
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_gscale: float = 1.0,
@@ -103,54 +112,52 @@ def kv_plan(kv_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
     the sum of ``new_lens`` (a padded batch).  A shortage shows in ``pages_used`` > len(free_pages) and
     in slots of -1, which the append skips.
     """
-    _need(kv_lens, "kv_lens", torch.int32, 1)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(free_pages, "free_pages", torch.int32, 1)
+    dev = _ints(kv_lens, "kv_lens", 1)
+    _ints(new_lens, "new_lens", 1, dev)
+    _ints(block_table, "block_table", 2, dev)
+    _ints(free_pages, "free_pages", 1, dev)
     r = kv_lens.shape[0]
-    _shape(new_lens, "new_lens", (r,))
-    if block_table.shape[0] != r:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows for {r} requests")
-    _same_device(kv_lens, ("new_lens", new_lens), ("block_table", block_table), ("free_pages", free_pages))
-    dev = kv_lens.device
-    # one allocation for the outputs
-    sizes = (r + 1, r, num_tokens, num_tokens, 1)
+    rows, width = block_table.shape
+    if new_lens.shape[0] != r:
+        _shape(new_lens, "new_lens", (r,))
+    if rows != r:
+        raise ValueError(f"block_table: {rows} rows for {r} requests")
     if num_tokens < 0:
         raise ValueError(f"num_tokens {num_tokens}")
-    plan = KvPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
-    with _on(dev):
-        L.check("moe_kv_plan", L.lib().moe_kv_plan(
+    # one allocation for the outputs
+    sizes = (r + 1, r, num_tokens, num_tokens, 1)
+    buf = torch.empty(2 * r + 2 * num_tokens + 2, dtype=_I32, device=dev)
+    at = buf.data_ptr()
+    with _on(dev.index):
+        st = L.lib().moe_kv_plan(
             kv_lens.data_ptr(), new_lens.data_ptr(), r, page_size, num_pages, free_pages.data_ptr(),
-            free_pages.shape[0], block_table.data_ptr(), block_table.shape[1], num_tokens,
-            plan.query_offsets.data_ptr(), plan.seq_lens.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr(),
-            plan.pages_used.data_ptr(), _raw_stream(dev)))
-    return plan
+            free_pages.shape[0], block_table.data_ptr(), width, num_tokens, at, at + 4 * (r + 1),
+            at + 4 * (2 * r + 1), at + 4 * (2 * r + 1 + num_tokens), at + 4 * (2 * r + 1 + 2 * num_tokens),
+            _raw_stream(dev.index))
+    if st:
+        L.check("moe_kv_plan", st)
+    return KvPlan(*buf.split_with_sizes(sizes))
 
 
-def _rows(t: torch.Tensor, name: str, dim: int, dev: torch.device) -> None:
-    """Token rows [T, heads, dim] bf16: heads contiguous, any token stride of a multiple of 8 elements."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+def _rows(t: torch.Tensor, name: str, dim: int, dev: torch.device):
+    """Token rows [T, heads, dim] bf16: heads contiguous, any token stride of a multiple of 8 elements.
+    (T, heads, token stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
         raise TypeError(f"{name}: expected a bfloat16 tensor")
     if t.dim() != 3 or t.shape[2] != dim:
         raise ValueError(f"{name}: expected [tokens, heads, {dim}], got {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    if t.shape[0] == 0:
-        return
-    s = t.stride()
-    if s[2] != 1 or (t.shape[1] > 1 and s[1] != dim):
-        raise ValueError(f"{name}: heads must be contiguous, got strides {s}")
-    if t.shape[0] > 1 and (s[0] < t.shape[1] * dim or s[0] % 8):
-        raise ValueError(f"{name}: token stride {s[0]}, expected a multiple of 8 of at least {t.shape[1] * dim}")
-    if t.data_ptr() % 16:
-        raise ValueError(f"{name}: rows must start at 16-byte boundaries")
-
-
-def _slots(slots: torch.Tensor, dev: torch.device) -> int:
-    _need(slots, "slots", torch.int32, 1)
-    if slots.device != dev:
-        raise ValueError(f"slots: on {slots.device}, expected {dev}")
-    return slots.shape[0]
+    tokens, heads, _ = t.shape
+    s0, s1, s2 = t.stride()
+    if tokens:
+        if s2 != 1 or (heads > 1 and s1 != dim):
+            raise ValueError(f"{name}: heads must be contiguous, got strides {(s0, s1, s2)}")
+        if tokens > 1 and (s0 < heads * dim or s0 % 8):
+            raise ValueError(f"{name}: token stride {s0}, expected a multiple of 8 of at least {heads * dim}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name}: rows must start at 16-byte boundaries")
+    return tokens, heads, s0
 
 
 def kv_append(cache: NvFp4KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
@@ -160,16 +167,18 @@ def kv_append(cache: NvFp4KvCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     may be slices of a fused projection's output (contiguous heads, any token stride that is a multiple
     of 8).
     """
-    c, dev = cache._struct, cache.pages.device
-    _rows(k, "k", c.head_dim, dev)
-    _rows(v, "v", c.head_dim, dev)
-    t = _slots(slots, dev)
-    for name, x in (("k", k), ("v", v)):
-        if x.shape[0] != t or x.shape[1] != c.kv_heads:
-            raise ValueError(f"{name}: expected {(t, c.kv_heads, c.head_dim)}, got {tuple(x.shape)}")
-    with _on(dev):
-        L.check("moe_nvfp4_kv_append", L.lib().moe_nvfp4_kv_append(
-            c, k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0), slots.data_ptr(), t, _raw_stream(dev)))
+    c, dev = cache._struct, cache._dev
+    kt, kh, ks = _rows(k, "k", c.head_dim, dev)
+    vt, vh, vs = _rows(v, "v", c.head_dim, dev)
+    _ints(slots, "slots", 1, dev)
+    t, h = slots.shape[0], c.kv_heads
+    if kt != t or kh != h or vt != t or vh != h:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)}: expected {(t, h, c.head_dim)}")
+    with _on(dev.index):
+        st = L.lib().moe_nvfp4_kv_append(c, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), t,
+                                         _raw_stream(dev.index))
+    if st:
+        L.check("moe_nvfp4_kv_append", st)
 
 
 def kv_gather(cache: NvFp4KvCache, slots: torch.Tensor):
@@ -177,13 +186,14 @@ def kv_gather(cache: NvFp4KvCache, slots: torch.Tensor):
 
     A slot outside the cache gives a NaN row.
     """
-    c, dev = cache._struct, cache.pages.device
-    n = _slots(slots, dev)
-    kv = torch.empty(2, n, c.kv_heads, c.head_dim, dtype=torch.bfloat16, device=dev)
-    k, v = kv[0], kv[1]
-    with _on(dev):
-        L.check("moe_nvfp4_kv_gather", L.lib().moe_nvfp4_kv_gather(c, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                                                   _raw_stream(dev)))
+    c, dev = cache._struct, cache._dev
+    _ints(slots, "slots", 1, dev)
+    n = slots.shape[0]
+    k, v = torch.empty(2, n, c.kv_heads, c.head_dim, dtype=_BF16, device=dev).unbind(0)
+    with _on(dev.index):
+        st = L.lib().moe_nvfp4_kv_gather(c, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _raw_stream(dev.index))
+    if st:
+        L.check("moe_nvfp4_kv_gather", st)
     return k, v
 
 
@@ -206,43 +216,45 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
     they were in ``out``.  q may be a slice of a fused projection's output.  Without ``workspace`` the
     call takes one from torch's allocator, so calls on several streams do not share it.
     """
-    c, dev = cache._struct, cache.pages.device
-    _rows(q, "q", c.head_dim, dev)
-    t, heads = q.shape[0], q.shape[1]
-    if heads % c.kv_heads or not 1 <= heads // c.kv_heads <= 64:
-        raise ValueError(f"q: {heads} heads are no multiple (1 to 64) of the cache's {c.kv_heads}")
-    _need(query_offsets, "query_offsets", torch.int32, 1)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
+    c, dev = cache._struct, cache._dev
+    dim, kv_heads = c.head_dim, c.kv_heads
+    t, heads, stride = _rows(q, "q", dim, dev)
+    if heads % kv_heads or not 1 <= heads // kv_heads <= 64:
+        raise ValueError(f"q: {heads} heads are no multiple (1 to 64) of the cache's {kv_heads}")
+    _ints(query_offsets, "query_offsets", 1, dev)
+    _ints(seq_lens, "seq_lens", 1, dev)
+    _ints(block_table, "block_table", 2, dev)
     r = seq_lens.shape[0]
-    _shape(query_offsets, "query_offsets", (r + 1,))
-    if block_table.shape[0] != r:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows for {r} requests")
-    _same_device(cache.pages, ("query_offsets", query_offsets), ("seq_lens", seq_lens), ("block_table", block_table))
+    rows, width = block_table.shape
+    if query_offsets.shape[0] != r + 1:
+        _shape(query_offsets, "query_offsets", (r + 1,))
+    if rows != r:
+        raise ValueError(f"block_table: {rows} rows for {r} requests")
     if scale is None:
-        scale = c.head_dim ** -0.5
+        scale = dim ** -0.5
     if not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError(f"scale must be finite and positive, got {scale!r}")
     if window < 0:
         raise ValueError(f"window {window}")
     if out is None:
-        out = torch.empty(t, heads, c.head_dim, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((t, heads, dim), dtype=_BF16, device=dev)
     else:
-        _need(out, "out", torch.bfloat16, 3)
-        _shape(out, "out", (t, heads, c.head_dim))
+        _need(out, "out", _BF16, 3)
+        _shape(out, "out", (t, heads, dim))
         _same_device(cache.pages, ("out", out))
-    lse = torch.empty(t, heads, dtype=torch.float32, device=dev) if return_lse else None
-    need = L.lib().moe_nvfp4_kv_attention_workspace_size(t, r, heads, c.kv_heads, c.head_dim)
+    lse = torch.empty((t, heads), dtype=torch.float32, device=dev) if return_lse else None
+    lib = L.lib()
     if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.moe_nvfp4_kv_attention_workspace_size(t, r, heads, kv_heads, dim),
+                                dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8)
         _same_device(cache.pages, ("workspace", workspace))
-    with _on(dev):
-        L.check("moe_nvfp4_kv_attention", L.lib().moe_nvfp4_kv_attention(
-            c, q.data_ptr(), q.stride(0), t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
-            block_table.data_ptr(), block_table.shape[1], scale, window, out.data_ptr(),
-            lse.data_ptr() if return_lse else None, workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() if workspace is not None else 0, _raw_stream(dev)))
+    with _on(dev.index):
+        st = lib.moe_nvfp4_kv_attention(
+            c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
+            block_table.data_ptr(), width, scale, window, out.data_ptr(), lse.data_ptr() if return_lse else None,
+            workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
+    if st:
+        L.check("moe_nvfp4_kv_attention", st)
     return (out, lse) if return_lse else out
