@@ -87,6 +87,11 @@ __device__ __forceinline__ f16x2 bf16x2_to_f16(uint32_t w, int sh) {
   return __builtin_convertvector(v, f16x2);
 }
 
+// Power of two that brings a row with largest bf16 exponent field e to [2^14, 2^15), held below the one
+// that would take the scores' factor c0 * 2^-shift out of the normal range (a row that small, zeros
+// included, has scores of 0 for every purpose).
+__device__ __forceinline__ int row_shift(int e, float c0) { return min(141 - e, ilogbf(c0) + 120); }
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Keys of dword `first`.. of a unit that lie before position len: byte mask of four scale bytes.
@@ -219,7 +224,7 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
       int e = (int)(top >> 7);    // the row's largest exponent field
       e = max(e, __shfl_xor(e, 16));
       e = max(e, __shfl_xor(e, 32));
-      const int shift = 141 - e;
+      const int shift = row_shift(e, a.scale * kLog2e);
 #pragma unroll
       for (int k = 0; k < NS; ++k) {
         const f16x2 p0 = bf16x2_to_f16(w[k][0], shift), p1 = bf16x2_to_f16(w[k][1], shift);
@@ -289,11 +294,19 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
         float t[8];
+        auto exponents = [&]() {
+          const float ref = m[mi] - kPExp;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = sc[mi][k >> 2][k & 3] * c[mi];
-        float mx = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-        if (__any(mx > m[mi] + kSlack)) {
-          mx = fmaxf(quarter_max(mx), m[mi]);
+          for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(sc[mi][k >> 2][k & 3], c[mi], -ref);
+        };
+        exponents();
+        const float most =
+            fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+        if (__any(most > kSlack + kPExp)) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sc[mi][k >> 2][k & 3]);
+          mx = fmaxf(quarter_max(mx) * c[mi], m[mi]);
           const float f = exp2_hw(m[mi] - mx);
           m[mi] = mx;
           l[mi] *= f;
@@ -303,10 +316,10 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[mi][r][e][k] *= f;
+          exponents();
         }
-        const float ref = m[mi] - kPExp;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = exp2_hw(t[k] - ref);
+        for (int k = 0; k < 8; ++k) t[k] = exp2_hw(t[k]);
         l[mi] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -432,20 +445,21 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
 }
 
 // ------------------------------------------------------------------------ many rows per request
-// One workgroup (NW waves of 32 rows) per (kv head, row tile, split).  Two units (64 positions) at a
+// One workgroup (NW waves of 32 rows) per (kv head, row tile, split).  NU units (32 positions each) at a
 // time are dequantized once into LDS, as fp16 operands of the 32x32x16 instruction in fragment order
-// (lane l's 16 bytes at 16*l), and multiplied by every wave; the next pair's codes are in registers and
+// (lane l's 16 bytes at 16*l), and multiplied by every wave; the next step's codes are in registers and
 // its operands written to the other LDS buffer meanwhile.
 //   key operand, unit b, step t (16 elements): lane 32z + p holds position p, elements [16t + 8z, +8)
 //   value operand, unit b, step t (16 positions), range r: lane 32z + d holds element 32r + d, positions
 //     16t + 4z + {0..3} and 16t + 8 + 4z + {0..3}: the ones whose scores lane 32z + n holds after S^T.
-template <int D, int NW>
+template <int D, int NW, int NU>
 __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_kernel(KvAttentionProblem a,
                                                                                       KvSchedule s, KvPartials part) {
   using U = KvUnit<D>;
   constexpr int NS = D / 32, NT = D / 16, BM = 32 * NW, THREADS = 64 * NW;
-  constexpr int kPieces = 8 * D / THREADS;          // 8-byte code pieces per thread and pair of units
-  __shared__ __align__(16) uint8_t lds[2][256 * D];   // 64 positions: keys 128*D bytes, then values
+  constexpr int kHalf = 2 * D * NU;                   // 8-byte code pieces of the keys (and of the values) of a step
+  constexpr int kKeys = 64 * D * NU;                  // bytes of the keys' (and of the values') operands
+  __shared__ __align__(16) uint8_t key_lds0[kKeys], key_lds1[kKeys], value_lds0[kKeys], value_lds1[kKeys];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int z = lane >> 5, n32 = lane & 31;
   const int hkv = a.cache.kv_heads;
@@ -480,7 +494,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
     }
     int e = (int)(top >> 7);
     e = max(e, __shfl_xor(e, 32));
-    const int sh = 141 - e;
+    const int sh = row_shift(e, a.scale * kLog2e);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const f16x2 p0 = bf16x2_to_f16(w[t][0], sh), p1 = bf16x2_to_f16(w[t][1], sh);
@@ -505,9 +519,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
     u1 = t1 < 0 ? u0 : min(min(it.q.lo + it.split * it.chunk + it.chunk, it.q.hi), t1 / kKvUnit + 1);
   }
   const int wrow = row_base + 32 * wave;
-  const bool live = wrow < rows;                    // the wave has rows
   reach(min(wrow, rows - 1), wrow + 32, &pos_min, &pos_max, &see_all, &see_any);
-  // the last pair may reach into the unit behind this split: nothing from `end` on counts
+  // the last step may reach into the unit behind this split: nothing from `end` on counts
   const int end = min(it.q.len, (int)min((long long)u1 * kKvUnit, 0x7FFFFFFFll));
   const int low = a.window > 0 ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
   pos = min(pos, end - 1);
@@ -522,142 +535,187 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 
   const int upp = a.cache.page_size / kKvUnit;
   const int32_t* table = a.table + (size_t)it.r * a.width;
-  auto page_of = [&](int u) {
-    const int b = u / upp;
-    const int p = b < a.width ? table[b] : -1;
-    return p >= 0 && p < a.cache.num_pages ? p : -1;
+  // addresses of a step's units (any valid unit past the end or for a bad table entry) and the bad ones' bits
+  struct Step {
+    uint64_t at[NU];
+    uint32_t none;
   };
-  int pages = -1;        // lane i: page of unit u0 + 64*batch + i, -1 bad
-  // code pieces of the pair of units at u: piece p < 4D key words, then value words
-  u32x2 code[kPieces];
-  u32x2 sc[kPieces];
-  uint32_t bad_now = 0, bad_next = 0;               // bit b: unit b of the pair has a bad page
-  auto load = [&](int u) {
-    const int i = u - u0;
-    if ((i & 63) == 0) {
-      const int uu = u + lane;
-      pages = uu < u1 ? page_of(uu) : 0;
+  uint64_t where = 0;      // lane i: address of unit u0 + 64*batch + i, 0 for a bad table entry
+  auto locate = [&](int u) __attribute__((always_inline)) {
+    if (((u - u0) & 63) == 0) {
+      const int uu = u + lane, b = uu / upp;
+      where = reinterpret_cast<uint64_t>(a.cache.pages);
+      if (uu < u1) {
+        const int p = b < a.width ? table[b] : -1;
+        where = p >= 0 && p < a.cache.num_pages ? where + (((uint64_t)p * hkv + h) * upp + (uu - b * upp)) * (uint64_t)U::kBytes
+                                                : 0;
+      }
     }
-    const uint8_t* base[2];
-    bad_next = 0;
+    Step x;
+    x.none = 0;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int p = __builtin_amdgcn_readlane(pages, (i & 63) + b);
-      bad_next |= p < 0 ? 1u << b : 0u;
-      base[b] = a.cache.pages + (((size_t)max(p, 0) * hkv + h) * upp + (u + b) % upp) * (size_t)U::kBytes;
+    for (int b = 0; b < NU; ++b) {
+      x.at[b] = (uint64_t)lane_i64((long long)where, (u + b - u0) & 63);
+      x.none |= x.at[b] == 0 ? 1u << b : 0u;
+      if (x.at[b] == 0) x.at[b] = reinterpret_cast<uint64_t>(a.cache.pages);
     }
+    return x;
+  };
+  // 8-byte code pieces of the keys (values) of a step: piece p = tid + THREADS*j, of unit b = p / 2D the piece
+  // x = p % 2D: lane (x / 2) % 64 of the 16-row operand, words 2*(x%2).. of its 16-byte load x / 128
+  // (a wave's pieces are all of one unit)
+  constexpr int kPieces = (kHalf + THREADS - 1) / THREADS;
+  u32x2 kcode[kPieces], vcode[kPieces], vscale[kPieces];
+  uint32_t kscale[kPieces];
+  auto first_piece = [&](int j) { return 64 * wave + THREADS * j; };
+  auto beyond = [&](int j) { return kHalf < THREADS && first_piece(j) >= kHalf; };      // fewer pieces than threads
+  auto load_keys = [&](const Step& st) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const int p = tid + THREADS * j;
-      const bool is_v = p >= 4 * D;
-      const int pp = p & (4 * D - 1), b = pp / (2 * D), x = pp & (2 * D - 1);   // 8-byte piece x of unit b
-      const uint8_t* ub = b ? base[1] : base[0];
-      code[j] = *reinterpret_cast<const u32x2*>(ub + (is_v ? U::kVCodes : 0) + 8 * x);
-      const int ln = (x >> 1) & 63, w = 4 * (x >> 7) + 2 * (x & 1);      // lane of the 16-row operand, word / 2*range
-      if (is_v)
-        sc[j] = *reinterpret_cast<const u32x2*>(ub + U::kVScales +
-                                                ((2 * (ln >> 4) + ((ln & 15) >> 3)) * NS + (w >> 1)) * 8);
-      else
-        sc[j][0] = *reinterpret_cast<const uint16_t*>(ub + U::kKScales + (16 * (ln >> 5) + (ln & 15)) * 2 * NS + w);
+      if (beyond(j)) continue;
+      const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
+      const uint8_t* ub = reinterpret_cast<const uint8_t*>(b ? st.at[NU - 1] : st.at[0]);
+      const int ln = (x >> 1) & 63, w = 4 * (x >> 7) + 2 * (x & 1);
+      kcode[j] = *reinterpret_cast<const u32x2*>(ub + 8 * x);
+      kscale[j] = *reinterpret_cast<const uint16_t*>(ub + U::kKScales + (16 * (ln >> 5) + (ln & 15)) * 2 * NS + w);
     }
   };
-  // the pair at u from registers to LDS buffer `buf`
-  auto store = [&](int u, int buf) {
-    uint8_t* kl = lds[buf];
-    uint8_t* vl = lds[buf] + 128 * D;
+  auto load_values = [&](const Step& st) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const int p = tid + THREADS * j;
-      const bool is_v = p >= 4 * D;
-      const int pp = p & (4 * D - 1), b = pp / (2 * D), x = pp & (2 * D - 1);
+      if (beyond(j)) continue;
+      const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
+      const uint8_t* ub = reinterpret_cast<const uint8_t*>(b ? st.at[NU - 1] : st.at[0]);
+      const int ln = (x >> 1) & 63, r = 2 * (x >> 7) + (x & 1);
+      vcode[j] = *reinterpret_cast<const u32x2*>(ub + U::kVCodes + 8 * x);
+      vscale[j] = *reinterpret_cast<const u32x2*>(ub + U::kVScales +
+                                                  ((2 * (ln >> 4) + ((ln & 15) >> 3)) * NS + r) * 8);
+    }
+  };
+  auto store_keys = [&](uint8_t* dst) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      if (beyond(j)) continue;
+      const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
       const int ln = (x >> 1) & 63, w = 4 * (x >> 7) + 2 * (x & 1), q4 = ln >> 4, n16 = ln & 15;
-      if (is_v) {
-        const int r = w >> 1, key0 = kKvUnit * (u + b);
-        u32x2 sv = sc[j];
-        if (bad_now & (1u << b)) sv[0] = sv[1] = 0;
-        sv[0] &= keep_bytes(key0 + 4 * q4, end);
-        sv[1] &= keep_bytes(key0 + 16 + 4 * q4, end);
+      const f16x2 sp = scale_pair(kscale[j], false);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          f16x4 even, odd;
-          v_quad(code[j][t], sv[t], &even, &odd);
-          // positions 4*q4..: lane half z = q4 & 1, bytes 8*(q4 >> 1) of its 16
-          uint8_t* dst = vl + ((b * 2 + t) * NS + r) * 1024 + 16 * (32 * (q4 & 1) + 2 * n16) + 8 * (q4 >> 1);
-          *reinterpret_cast<f16x4*>(dst) = even;
-          *reinterpret_cast<f16x4*>(dst + 16) = odd;
-        }
-      } else {
-        const f16x2 sp = scale_pair(sc[j][0], false);
+      for (int e = 0; e < 2; ++e) {
+        const int kb = (w + e) / NS, i = (w + e) % NS;
+        *reinterpret_cast<f16x8*>(dst + (b * NT + 2 * i + (q4 >> 1)) * 1024 + 16 * (32 * (q4 & 1) + 16 * kb + n16)) =
+            k_operand(kcode[j][e], sp[e]);
+      }
+    }
+  };
+  auto store_values = [&](int u, const Step& st, uint8_t* dst) __attribute__((always_inline)) {
+    if (__builtin_expect(kKvUnit * (u + NU) > end || st.none != 0, 0)) {
+      // nothing from positions past the end or of bad pages
+      asm volatile("");      // keeps this a branch
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int ww = w + e, kb = ww / NS, i = ww % NS;
-          const f16x8 kf = k_operand(code[j][e], sp[e]);
-          uint8_t* dst = kl + (b * NT + 2 * i + (q4 >> 1)) * 1024 + 16 * (32 * (q4 & 1) + 16 * kb + n16);
-          *reinterpret_cast<f16x8*>(dst) = kf;
-        }
+      for (int j = 0; j < kPieces; ++j) {
+        if (beyond(j)) continue;
+        const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
+        const int key0 = kKvUnit * (u + b) + 4 * ((x >> 5) & 3);
+        vscale[j][0] &= (st.none >> b) & 1u ? 0u : keep_bytes(key0, end);
+        vscale[j][1] &= (st.none >> b) & 1u ? 0u : keep_bytes(key0 + 16, end);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      if (beyond(j)) continue;
+      const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
+      const int ln = (x >> 1) & 63, r = 2 * (x >> 7) + (x & 1), q4 = ln >> 4, n16 = ln & 15;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f16x4 even, odd;
+        v_quad(vcode[j][t], vscale[j][t], &even, &odd);
+        // positions 4*q4..: lane half z = q4 & 1, bytes 8*(q4 >> 1) of its 16
+        uint8_t* d = dst + ((b * 2 + t) * NS + r) * 1024 + 16 * (32 * (q4 & 1) + 2 * n16) + 8 * (q4 >> 1);
+        *reinterpret_cast<f16x4*>(d) = even;
+        *reinterpret_cast<f16x4*>(d + 16) = odd;
       }
     }
   };
 
-  auto compute = [&](int u, int buf, uint32_t bad) {
+  f32x16 sacc[NU];
+  // raw scores of the step whose keys are in `src`
+  auto scores = [&](const uint8_t* src, f32x16 (&x)[NU]) __attribute__((always_inline)) {
+    const uint8_t* kl = src + 16 * lane;
+#pragma unroll
+    for (int b = 0; b < NU; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[b][i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int b = 0; b < NU; ++b)
+        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(kl + (b * NT + t) * 1024), qf[t],
+                                                      x[b], 0, 0, 0);
+  };
+  // masks of the step at u
+  auto mask = [&](int u, uint32_t none) __attribute__((always_inline)) {
     const int key0 = kKvUnit * u;
-    const uint8_t* kl = lds[buf] + 16 * lane;
-    const uint8_t* vl = kl + 128 * D;
-    f32x16 sacc[2];
+    if (key0 + NU * kKvUnit - 1 > pos_min || key0 < see_all || none) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sacc[b][i] = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        sacc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(kl + (b * NT + t) * 1024),
-                                                         qf[t], sacc[b], 0, 0, 0);
-    }
-    if (key0 + 63 > pos_min || key0 < see_all || bad) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NU; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = key0 + 32 * b + 8 * (i >> 2) + 4 * z + (i & 3);
           const bool seen = key <= pos && key >= low;
-          sacc[b][i] = !seen ? -INFINITY : (bad >> b) & 1u ? NAN : sacc[b][i];
+          sacc[b][i] = !seen ? -INFINITY : (none >> b) & 1u ? NAN : sacc[b][i];
         }
     }
+  };
+  // raw scores to exponents of p (base 2) under the current reference maximum; their largest
+  auto exponents = [&]() __attribute__((always_inline)) {
+    const float ref = m - kPExp;
     float mx = -INFINITY;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        sacc[b][i] *= c;
-        mx = fmaxf(mx, sacc[b][i]);
-      }
-    if (__any(mx > m + kSlack)) {
-      const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-      mx = fmaxf(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])), m);
-      const float f = exp2_hw(m - mx);
-      m = mx;
-      l *= f;
-#pragma unroll
-      for (int r = 0; r < NS; ++r)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[r][i] *= f;
-    }
-    const float ref = m - kPExp;
-    f16x8 pf[2][2];
-    float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NU; ++b)
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        const float p0 = exp2_hw(sacc[b][i] - ref), p1 = exp2_hw(sacc[b][i + 1] - ref);
-        part_sum[(i >> 1) & 3] += p0 + p1;
+        sacc[b][i] = __fmaf_rn(sacc[b][i], c, -ref);
+        sacc[b][i + 1] = __fmaf_rn(sacc[b][i + 1], c, -ref);
+        mx = fmaxf(mx, fmaxf(sacc[b][i], sacc[b][i + 1]));
+      }
+    return mx;
+  };
+  // the reference maximum moved to the largest of the raw scores, sums and outputs rescaled
+  auto move_reference = [&]() __attribute__((always_inline)) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NU; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sacc[b][i]);
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+    mx = fmaxf(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])) * c, m);
+    const float f = exp2_hw(m - mx);
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int r = 0; r < NS; ++r)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[r][i] *= f;
+  };
+  f16x8 pf[NU][2];
+  auto probabilities = [&]() __attribute__((always_inline)) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b = 0; b < NU; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = exp2_hw(sacc[b][i]), p1 = exp2_hw(sacc[b][i + 1]);
+        sum[(i >> 1) & 3] += p0 + p1;
         const f16x2 pr = __builtin_convertvector((f32x2){p0, p1}, f16x2);
         pf[b][i >> 3][i & 7] = pr[0];
         pf[b][i >> 3][(i & 7) + 1] = pr[1];
       }
-    l += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  };
+  auto products = [&](const uint8_t* src) __attribute__((always_inline)) {
+    const uint8_t* vl = src + 16 * lane;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NU; ++b)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -666,24 +724,66 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
               *reinterpret_cast<const f16x8*>(vl + ((b * 2 + t) * NS + r) * 1024), pf[b][t], o[r], 0, 0, 0);
   };
 
+  // Keys run one step ahead of values: while a step's probabilities are formed the next step's scores are
+  // multiplied, and while its products run the operands of the keys two steps ahead and of the next
+  // values are written.  Step i uses key buffer i & 1 and value buffer i & 1; one barrier per step.
   if (u0 < u1) {
-    load(u0);
-    bad_now = bad_next;
-    store(u0, 0);
-    uint32_t bad = bad_now;
-    if (u0 + 2 < u1) load(u0 + 2);
-    __syncthreads();
-    int buf = 0;
-    for (int u = u0; u < u1; u += 2) {
-      if (live && kKvUnit * u <= pos_max && kKvUnit * u + 63 >= see_any) compute(u, buf, bad);
-      if (u + 2 < u1) {
-        bad_now = bad_next;
-        bad = bad_now;
-        store(u + 2, buf ^ 1);
-        if (u + 4 < u1) load(u + 4);
-      }
+    Step s1, s2, s3;      // the next step, the one after, the third
+    {
+      const Step s0 = locate(u0);
+      load_keys(s0);
+      load_values(s0);
+      s1 = locate(u0 + NU);
+      store_keys(key_lds0);
+      store_values(u0, s0, value_lds0);
+      load_keys(s1);
+      store_keys(key_lds1);
+      load_values(s1);
+      s2 = locate(u0 + 2 * NU);
+      load_keys(s2);
       __syncthreads();
-      buf ^= 1;
+      scores(key_lds0, sacc);
+      mask(u0, s0.none);
+      move_reference();
+      exponents();
+      __syncthreads();
+    }
+    // step u in buffers (kc, vc), the next step's in (kn, vn)
+    auto step = [&](int u, uint8_t* kc, const uint8_t* kn, const uint8_t* vc, uint8_t* vn) __attribute__((always_inline)) {
+      s3 = locate(u + 3 * NU);
+      f32x16 next[NU];
+      probabilities();
+      scores(kn, next);
+      store_keys(kc);                     // keys of u + 2*NU
+      store_values(u + NU, s1, vn);
+      load_keys(s3);
+      load_values(s2);
+      products(vc);
+#pragma unroll
+      for (int b = 0; b < NU; ++b) sacc[b] = next[b];
+      mask(u + NU, s1.none);
+      if (__builtin_expect(__any(exponents() > kSlack + kPExp), 0)) {
+        scores(kn, sacc);      // the raw scores are gone
+        mask(u + NU, s1.none);
+        move_reference();
+        exponents();
+      }
+      s1 = s2;
+      s2 = s3;
+      __syncthreads();
+    };
+    int u = u0;
+    for (; u + 2 * NU < u1; u += 2 * NU) {
+      step(u, key_lds0, key_lds1, value_lds0, value_lds1);
+      step(u + NU, key_lds1, key_lds0, value_lds1, value_lds0);
+    }
+    if (u + NU < u1) {
+      step(u, key_lds0, key_lds1, value_lds0, value_lds1);
+      probabilities();
+      products(value_lds1);
+    } else {
+      probabilities();
+      products(value_lds0);
     }
   }
 
@@ -897,7 +997,7 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
       constexpr int NW = DD == 256 ? 4 : 8;
       const dim3 grid((unsigned)p.grid), rows((unsigned)p.tiles, p.shares ? p.s.bm / 8 : 4);
       if (!p.shares) {
-        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, NW>), grid, dim3(64 * NW), 0, stream, a, p.s, part);
+        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, NW, DD == 256 ? 1 : 2>), grid, dim3(64 * NW), 0, stream, a, p.s, part);
         hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
       } else {
         if (p.s.bm == 16)
