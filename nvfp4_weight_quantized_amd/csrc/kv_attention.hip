@@ -81,6 +81,16 @@ __device__ __forceinline__ float quarter_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// the same over the two lanes 32 apart (a row of a 32-row block)
+__device__ __forceinline__ float half_max(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // bf16 pair times 2^sh as fp16
 __device__ __forceinline__ f16x2 bf16x2_to_f16(uint32_t w, int sh) {
   const f32x2 v = {ldexpf(__uint_as_float(w << 16), sh), ldexpf(__uint_as_float(w & 0xFFFF0000u), sh)};
@@ -445,23 +455,31 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
 }
 
 // ------------------------------------------------------------------------ many rows per request
-// One workgroup (NW waves of 32 rows) per (kv head, row tile, split).  NU units (32 positions each) at a
-// time are dequantized once into LDS, as fp16 operands of the 32x32x16 instruction in fragment order
-// (lane l's 16 bytes at 16*l), and multiplied by every wave; the next step's codes are in registers and
-// its operands written to the other LDS buffer meanwhile.
+// One workgroup (NW waves of RS rows) per (kv head, row tile, split).  NU units (32 positions each) at a
+// time are dequantized once into LDS, as fp16 operands in fragment order (lane l's 16 bytes at 16*l), and
+// multiplied by every wave; the next step's codes are in registers and its operands written to the other
+// LDS buffer meanwhile.
+// RS = 32, the 32x32x16 instruction:
 //   key operand, unit b, step t (16 elements): lane 32z + p holds position p, elements [16t + 8z, +8)
 //   value operand, unit b, step t (16 positions), range r: lane 32z + d holds element 32r + d, positions
 //     16t + 4z + {0..3} and 16t + 8 + 4z + {0..3}: the ones whose scores lane 32z + n holds after S^T.
-template <int D, int NW, int NU>
-__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_kernel(KvAttentionProblem a,
+// RS = 16, the 16x16x32 instruction: the operands as the cache holds them (value operand, range r: the
+//   even elements, then the odd ones).  Half the rows per operand read, which LDS bandwidth then bounds at
+//   half the matrix rate; taken for head dimension 256, whose 32-row outputs and queries leave no registers
+//   to overlap anything (128 + 64 of 256; measured 263 us against RSTIME us for chunks of 5 requests).
+template <int D, int NW, int NU, int RS>
+__global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttentionProblem a,
                                                                                       KvSchedule s, KvPartials part) {
   using U = KvUnit<D>;
-  constexpr int NS = D / 32, NT = D / 16, BM = 32 * NW, THREADS = 64 * NW;
+  constexpr int NS = D / 32, NT = D / 16, BM = RS * NW, THREADS = 64 * NW;
+  constexpr bool kWide = RS == 32;
+  constexpr int NQ = kWide ? NT : NS;                 // query operands
+  constexpr int NSC = kWide ? 16 : 8;                 // scores of a lane and unit
   constexpr int kHalf = 2 * D * NU;                   // 8-byte code pieces of the keys (and of the values) of a step
   constexpr int kKeys = 64 * D * NU;                  // bytes of the keys' (and of the values') operands
   __shared__ __align__(16) uint8_t key_lds0[kKeys], key_lds1[kKeys], value_lds0[kKeys], value_lds1[kKeys];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int z = lane >> 5, n32 = lane & 31;
+  const int z = lane / RS, nrow = lane & (RS - 1);     // part of the contraction, row
   const int hkv = a.cache.kv_heads;
   const int h = blockIdx.x % hkv;
   KvItem it;
@@ -475,28 +493,29 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
   const int rows = it.q.n * a.G, row_base = it.tile * BM;
   const int pos0 = it.q.len - it.q.n;
 
-  // query operand: row n32 of the wave, elements [16t + 8z, +8)
-  const int row = row_base + 32 * wave + n32;
+  // query operands: row nrow of the wave, elements [16t + 8z, +8) (RS = 16: [32t + 8z, +8))
+  const int row = row_base + RS * wave + nrow;
   const bool valid = row < rows;
   const int tok = valid ? row / a.G : 0, g = valid ? row - tok * a.G : 0;
   int pos = valid ? pos0 + tok : -1;
-  f16x8 qf[NT];
+  f16x8 qf[NQ];
   float c;
   {
     const uint16_t* src = a.q + (int64_t)(it.q.row0 + tok) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * z;
-    u32x4 w[NT];
+    u32x4 w[NQ];
     uint32_t top = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      w[t] = *reinterpret_cast<const u32x4*>(src + 16 * t);
+    for (int t = 0; t < NQ; ++t) {
+      w[t] = *reinterpret_cast<const u32x4*>(src + (kWide ? 16 : 32) * t);
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, max(w[t][j] & 0x7FFFu, (w[t][j] >> 16) & 0x7FFFu));
     }
     int e = (int)(top >> 7);
     e = max(e, __shfl_xor(e, 32));
+    if (!kWide) e = max(e, __shfl_xor(e, 16));
     const int sh = row_shift(e, a.scale * kLog2e);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NQ; ++t) {
       const f16x2 p0 = bf16x2_to_f16(w[t][0], sh), p1 = bf16x2_to_f16(w[t][1], sh);
       const f16x2 p2 = bf16x2_to_f16(w[t][2], sh), p3 = bf16x2_to_f16(w[t][3], sh);
       qf[t] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
@@ -518,20 +537,23 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
     u0 = max(it.q.lo + it.split * it.chunk, t3 / kKvUnit);
     u1 = t1 < 0 ? u0 : min(min(it.q.lo + it.split * it.chunk + it.chunk, it.q.hi), t1 / kKvUnit + 1);
   }
-  const int wrow = row_base + 32 * wave;
-  reach(min(wrow, rows - 1), wrow + 32, &pos_min, &pos_max, &see_all, &see_any);
+  const int wrow = row_base + RS * wave;
+  reach(min(wrow, rows - 1), wrow + RS, &pos_min, &pos_max, &see_all, &see_any);
   // the last step may reach into the unit behind this split: nothing from `end` on counts
   const int end = min(it.q.len, (int)min((long long)u1 * kKvUnit, 0x7FFFFFFFll));
   const int low = a.window > 0 ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
   pos = min(pos, end - 1);
   pos_min = min(pos_min, end - 1);
 
-  f32x16 o[NS];
+  // RS = 32: element 32r + 8(i/4) + 4z + i%4 in o[r][i]; RS = 16: 32r + 8z + 2i + e in o[2r + e][i]
+  using Acc = std::conditional_t<kWide, f32x16, f32x4>;
+  constexpr int NO = kWide ? NS : 2 * NS, NA = kWide ? 16 : 4;
+  Acc o[NO];
   float m = kNone, l = 0.f;
 #pragma unroll
-  for (int r = 0; r < NS; ++r)
+  for (int r = 0; r < NO; ++r)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[r][i] = 0.f;
+    for (int i = 0; i < NA; ++i) o[r][i] = 0.f;
 
   const int upp = a.cache.page_size / kKvUnit;
   const int32_t* table = a.table + (size_t)it.r * a.width;
@@ -602,8 +624,9 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int kb = (w + e) / NS, i = (w + e) % NS;
-        *reinterpret_cast<f16x8*>(dst + (b * NT + 2 * i + (q4 >> 1)) * 1024 + 16 * (32 * (q4 & 1) + 16 * kb + n16)) =
-            k_operand(kcode[j][e], sp[e]);
+        uint8_t* d = kWide ? dst + (b * NT + 2 * i + (q4 >> 1)) * 1024 + 16 * (32 * (q4 & 1) + 16 * kb + n16)
+                           : dst + (b * NT + w + e) * 1024 + 16 * ln;
+        *reinterpret_cast<f16x8*>(d) = k_operand(kcode[j][e], sp[e]);
       }
     }
   };
@@ -625,32 +648,48 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
       if (beyond(j)) continue;
       const int b = first_piece(j) / (2 * D), x = (first_piece(j) & (2 * D - 1)) + lane;
       const int ln = (x >> 1) & 63, r = 2 * (x >> 7) + (x & 1), q4 = ln >> 4, n16 = ln & 15;
+      f16x4 even[2], odd[2];
+      v_quad(vcode[j][0], vscale[j][0], &even[0], &odd[0]);
+      v_quad(vcode[j][1], vscale[j][1], &even[1], &odd[1]);
+      if (kWide) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f16x4 even, odd;
-        v_quad(vcode[j][t], vscale[j][t], &even, &odd);
-        // positions 4*q4..: lane half z = q4 & 1, bytes 8*(q4 >> 1) of its 16
-        uint8_t* d = dst + ((b * 2 + t) * NS + r) * 1024 + 16 * (32 * (q4 & 1) + 2 * n16) + 8 * (q4 >> 1);
-        *reinterpret_cast<f16x4*>(d) = even;
-        *reinterpret_cast<f16x4*>(d + 16) = odd;
+        for (int t = 0; t < 2; ++t) {
+          // positions 4*q4..: lane half z = q4 & 1, bytes 8*(q4 >> 1) of its 16
+          uint8_t* d = dst + ((b * 2 + t) * NS + r) * 1024 + 16 * (32 * (q4 & 1) + 2 * n16) + 8 * (q4 >> 1);
+          *reinterpret_cast<f16x4*>(d) = even[t];
+          *reinterpret_cast<f16x4*>(d + 16) = odd[t];
+        }
+      } else {
+        uint8_t* d = dst + (b * 2 * NS + 2 * r) * 1024 + 16 * ln;
+        *reinterpret_cast<f16x8*>(d) = __builtin_shufflevector(even[0], even[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        *reinterpret_cast<f16x8*>(d + 1024) = __builtin_shufflevector(odd[0], odd[1], 0, 1, 2, 3, 4, 5, 6, 7);
       }
     }
   };
 
-  f32x16 sacc[NU];
+  // scores of a lane: RS = 32: position 32b + 8(i/4) + 4z + i%4 in sacc[b][0][i]; RS = 16: 32b + 16k + 4z + i in
+  // sacc[b][k][i]
+  constexpr int NK = kWide ? 1 : 2;
+  Acc sacc[NU][NK];
   // raw scores of the step whose keys are in `src`
-  auto scores = [&](const uint8_t* src, f32x16 (&x)[NU]) __attribute__((always_inline)) {
+  auto scores = [&](const uint8_t* src, Acc (&x)[NU][NK]) __attribute__((always_inline)) {
     const uint8_t* kl = src + 16 * lane;
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[b][i] = 0.f;
+      for (int k = 0; k < NK; ++k)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < NA; ++i) x[b][k][i] = 0.f;
+#pragma unroll
+    for (int t = 0; t < NQ; ++t)
 #pragma unroll
       for (int b = 0; b < NU; ++b)
-        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8*>(kl + (b * NT + t) * 1024), qf[t],
-                                                      x[b], 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const f16x8 kf = *reinterpret_cast<const f16x8*>(kl + (b * NT + k * NS + t) * 1024);
+          if constexpr (kWide) x[b][k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[t], x[b][k], 0, 0, 0);
+          else x[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t], x[b][k], 0, 0, 0);
+        }
   };
   // masks of the step at u
   auto mask = [&](int u, uint32_t none) __attribute__((always_inline)) {
@@ -659,11 +698,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 #pragma unroll
       for (int b = 0; b < NU; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = key0 + 32 * b + 8 * (i >> 2) + 4 * z + (i & 3);
-          const bool seen = key <= pos && key >= low;
-          sacc[b][i] = !seen ? -INFINITY : (none >> b) & 1u ? NAN : sacc[b][i];
-        }
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int i = 0; i < NA; ++i) {
+            const int key = key0 + 32 * b + (kWide ? 8 * (i >> 2) + 4 * z + (i & 3) : 16 * k + 4 * z + i);
+            const bool seen = key <= pos && key >= low;
+            sacc[b][k][i] = !seen ? -INFINITY : (none >> b) & 1u ? NAN : sacc[b][k][i];
+          }
     }
   };
   // raw scores to exponents of p (base 2) under the current reference maximum; their largest
@@ -673,38 +714,42 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        sacc[b][i] = __fmaf_rn(sacc[b][i], c, -ref);
-        sacc[b][i + 1] = __fmaf_rn(sacc[b][i + 1], c, -ref);
-        mx = fmaxf(mx, fmaxf(sacc[b][i], sacc[b][i + 1]));
-      }
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int i = 0; i < NA; i += 2) {
+          sacc[b][k][i] = __fmaf_rn(sacc[b][k][i], c, -ref);
+          sacc[b][k][i + 1] = __fmaf_rn(sacc[b][k][i + 1], c, -ref);
+          mx = fmaxf(mx, fmaxf(sacc[b][k][i], sacc[b][k][i + 1]));
+        }
     return mx;
   };
+  auto row_max = [](float v) { return kWide ? half_max(v) : quarter_max(v); };
   // the reference maximum moved to the largest of the raw scores, sums and outputs rescaled
   auto move_reference = [&]() __attribute__((always_inline)) {
     float mx = -INFINITY;
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sacc[b][i]);
-    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-    mx = fmaxf(fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])) * c, m);
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) mx = fmaxf(mx, sacc[b][k][i]);
+    mx = fmaxf(row_max(mx) * c, m);
     const float f = exp2_hw(m - mx);
     m = mx;
     l *= f;
 #pragma unroll
-    for (int r = 0; r < NS; ++r)
+    for (int r = 0; r < NO; ++r)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[r][i] *= f;
+      for (int i = 0; i < NA; ++i) o[r][i] *= f;
   };
-  f16x8 pf[NU][2];
+  f16x8 pf[NU][NSC / 8];      // RS = 32: 16 positions each; RS = 16: 32
   auto probabilities = [&]() __attribute__((always_inline)) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float p0 = exp2_hw(sacc[b][i]), p1 = exp2_hw(sacc[b][i + 1]);
+      for (int i = 0; i < NSC; i += 2) {
+        const float p0 = exp2_hw(sacc[b][i / NA][i % NA]), p1 = exp2_hw(sacc[b][i / NA][i % NA + 1]);
         sum[(i >> 1) & 3] += p0 + p1;
         const f16x2 pr = __builtin_convertvector((f32x2){p0, p1}, f16x2);
         pf[b][i >> 3][i & 7] = pr[0];
@@ -717,11 +762,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < NSC / 8; ++t)
 #pragma unroll
-        for (int r = 0; r < NS; ++r)
-          o[r] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const f16x8*>(vl + ((b * 2 + t) * NS + r) * 1024), pf[b][t], o[r], 0, 0, 0);
+        for (int r = 0; r < NO; ++r) {
+          if (!kWide && r % 8 == 0) __builtin_amdgcn_sched_barrier(0);
+          const f16x8 vf = *reinterpret_cast<const f16x8*>(vl + (b * 2 * NS + t * NO + r) * 1024);
+          if constexpr (kWide) o[r] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[b][t], o[r], 0, 0, 0);
+          else o[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[b][t], o[r], 0, 0, 0);
+        }
   };
 
   // Keys run one step ahead of values: while a step's probabilities are formed the next step's scores are
@@ -751,16 +799,21 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
     // step u in buffers (kc, vc), the next step's in (kn, vn)
     auto step = [&](int u, uint8_t* kc, const uint8_t* kn, const uint8_t* vc, uint8_t* vn) __attribute__((always_inline)) {
       s3 = locate(u + 3 * NU);
-      f32x16 next[NU];
+      Acc next[NU][NK];
       probabilities();
       scores(kn, next);
+      if (!kWide) __builtin_amdgcn_sched_barrier(0);
       store_keys(kc);                     // keys of u + 2*NU
       store_values(u + NU, s1, vn);
       load_keys(s3);
       load_values(s2);
+      if (!kWide) __builtin_amdgcn_sched_barrier(0);
       products(vc);
+      if (!kWide) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int b = 0; b < NU; ++b) sacc[b] = next[b];
+      for (int b = 0; b < NU; ++b)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) sacc[b][k] = next[b][k];
       mask(u + NU, s1.none);
       if (__builtin_expect(__any(exponents() > kSlack + kPExp), 0)) {
         scores(kn, sacc);      // the raw scores are gone
@@ -787,37 +840,35 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kv_attention_tiles_k
     }
   }
 
-  {
-    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
-    l = __uint_as_float(y[0]) + __uint_as_float(y[1]);
-  }
+  l = kWide ? half_sum(l) : quarter_sum(l);
   if (!valid) return;
   const size_t at = (size_t)(it.q.row0 + tok) * a.Hq + h * a.G + g;
+  // groups of four elements of the lane's row, and where they begin
+  constexpr int NG = kWide ? 4 * NS : 2 * NS;
+  auto group = [&](int k) __attribute__((always_inline)) {
+    if constexpr (kWide) return float4{o[k / 4][4 * (k % 4)], o[k / 4][4 * (k % 4) + 1], o[k / 4][4 * (k % 4) + 2], o[k / 4][4 * (k % 4) + 3]};
+    else return float4{o[k & ~1][2 * (k & 1)], o[k | 1][2 * (k & 1)], o[k & ~1][2 * (k & 1) + 1], o[k | 1][2 * (k & 1) + 1]};
+  };
+  auto place = [&](int k) { return kWide ? 8 * k + 4 * z : 32 * (k >> 1) + 8 * z + 4 * (k & 1); };
   if (it.splits == 1) {
     const bool any = l > 0.f || l != l;
     const float norm = any ? a.cache.v_gscale / l : 0.f;
     if (a.lse && z == 0) a.lse[at] = any ? kLn2 * (m + (__builtin_amdgcn_logf(l) - kPExp)) : -INFINITY;
 #pragma unroll
-    for (int r = 0; r < NS; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2*>(a.out + at * D + 32 * r + 8 * i + 4 * z) =
-            u32x2{f32x2_to_bf16x2(o[r][4 * i] * norm, o[r][4 * i + 1] * norm),
-                  f32x2_to_bf16x2(o[r][4 * i + 2] * norm, o[r][4 * i + 3] * norm)};
+    for (int k = 0; k < NG; ++k) {
+      const float4 v = group(k);
+      *reinterpret_cast<u32x2*>(a.out + at * D + place(k)) =
+          u32x2{f32x2_to_bf16x2(v.x * norm, v.y * norm), f32x2_to_bf16x2(v.z * norm, v.w * norm)};
+    }
   } else {
     const size_t slot = (size_t)(it.slot + it.split) * hkv + h;
-    const int lrow = 32 * wave + n32;
+    const int lrow = RS * wave + nrow;
     if (z == 0) {
       part.ml[slot * 2 * BM + lrow] = m;
       part.ml[slot * 2 * BM + BM + lrow] = l;
     }
-    float* dst = part.o + (slot * BM + lrow) * D + 4 * z;
 #pragma unroll
-    for (int r = 0; r < NS; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(dst + 32 * r + 8 * i) =
-            float4{o[r][4 * i], o[r][4 * i + 1], o[r][4 * i + 2], o[r][4 * i + 3]};
+    for (int k = 0; k < NG; ++k) *reinterpret_cast<float4*>(part.o + (slot * BM + lrow) * D + place(k)) = group(k);
   }
 }
 
@@ -994,10 +1045,9 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
     part.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_bytes);
     with_head_dim(D, [&](auto tag) {
       constexpr int DD = decltype(tag)::value;
-      constexpr int NW = DD == 256 ? 4 : 8;
       const dim3 grid((unsigned)p.grid), rows((unsigned)p.tiles, p.shares ? p.s.bm / 8 : 4);
       if (!p.shares) {
-        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, NW, DD == 256 ? 1 : 2>), grid, dim3(64 * NW), 0, stream, a, p.s, part);
+        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, 8, DD == 256 ? 1 : 2, DD == 256 ? 16 : 32>), grid, dim3(512), 0, stream, a, p.s, part);
         hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
       } else {
         if (p.s.bm == 16)
