@@ -162,15 +162,18 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
   if (!kv_locate<false>(a, s, blockIdx.x, &sh, &at, &local)) return;
   const long long begin = (long long)blockIdx.x * sh.chunk;
   int left = (int)min(sh.chunk, sh.total - begin);
+  const int chunk = (int)min(sh.chunk, (long long)(1 << 28));
   const int upp = a.cache.page_size / kKvUnit;
   bool first = true;
 
   while (true) {
     const int units = max(1, at.q.hi - at.q.lo);
     const long long step = kv_step(at.q, sh), nth = div_i64(local, step);
-    const int unit = (int)(local - nth * step);
+    // place in the tile: `lead` empty places before unit 0
+    const int lead = sh.aligned ? 0 : kSwitch, place = (int)(local - nth * step), unit = max(0, place - lead);
     const int h = (int)div_i64(nth, at.q.tiles), tile = (int)(nth - (long long)h * at.q.tiles);
-    const int count = min(left, units - unit);
+    const int taken = min(left, lead + units - place), count = place + taken - lead - unit;
+    if (count <= 0) return;       // the share ends before the tile's first unit
 
     const int rows = at.q.n * a.G, row_base = tile * BM;
     const int pos0 = at.q.len - at.q.n;          // position of the request's first row
@@ -358,6 +361,14 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
     };
 
     for (int i = 0, slot = 0; i < mine; ++i) {
+      // Waves that have most of their share left go first: the scheduler prefers the oldest wave, which
+      // finishes its share while the youngest has the compute unit to itself at the end, too few to hide
+      // latency (shares of equal length took 22 to 72 us).
+      const int rest = left - 4 * i;
+      if (4 * rest > 3 * chunk) __builtin_amdgcn_s_setprio(3);
+      else if (2 * rest > chunk) __builtin_amdgcn_s_setprio(2);
+      else if (4 * rest > chunk) __builtin_amdgcn_s_setprio(1);
+      else __builtin_amdgcn_s_setprio(0);
       wait_units<kFull + kTail>(min(kRing, mine - i) - 1);
       compute(ufirst + 4 * i, slot * U::kBytes, (bad[(i >> 6) & 1] >> (i & 63)) & 1);
       if (i + kRing < mine) {
@@ -441,10 +452,10 @@ __global__ __launch_bounds__(256, (rows_occupancy<D, MI>())) void kv_attention_r
     }
 
     // the next segment: of this request, or of the next one with rows
-    left -= count;
+    left -= taken;
     if (left == 0 || sh.aligned) return;
     first = false;
-    local += count;
+    local += taken;
     if (local == kv_units(at.q, sh) * hkv) {
       local = 0;
       do {
@@ -890,7 +901,7 @@ __global__ __launch_bounds__(256) void kv_combine_kernel(KvAttentionProblem a, K
     h = (int)within / q.tiles;
     tile = (int)within - h * q.tiles;
     const int units = max(1, q.hi - q.lo);
-    const long long begin = at.base + within * kv_step(q, sh), i0 = div_i64(begin, sh.chunk),
+    const long long begin = at.base + within * kv_step(q, sh) + (sh.aligned ? 0 : kSwitch), i0 = div_i64(begin, sh.chunk),
                     i1 = div_i64(begin + units - 1, sh.chunk);
     if (i0 == i1) return;
     count = (int)(i1 - i0) + 1;

@@ -90,14 +90,16 @@ __device__ __forceinline__ long long div_i64(long long x, long long y) {
 
 // Linear order of a launch's work: requests in order, in each its kv heads, row tiles and units
 // (at least one unit per tile, so that a row that sees nothing is written too).  Workgroup i of `target`
-// takes the units [i * chunk, (i + 1) * chunk) of that order: an equal share, whatever the lengths.
+// takes [i * chunk, (i + 1) * chunk) of that order: an equal share, whatever the lengths.
 // A tile cut between workgroups leaves one partial sum per workgroup; a workgroup has at most two
 // unfinished tiles, the one it begins with (slot 2i) and the one it ends with (slot 2i + 1).
-// Aligned: each tile's units are padded to whole chunks in the order, so that no workgroup crosses from
-// one tile into the next (which costs it about as much as kSwitch units: the new rows, the table and the
-// first units arrive one after the other).  Taken where the chunks that padding needs, work / (target -
-// tiles), are at most that much longer: with few tiles, that is, while many tiles of unequal lengths
-// are shared out evenly.
+// Beginning a tile costs a workgroup about as much as kSwitch units (the rows, the table and the first
+// units arrive one after the other), so every tile's units are preceded by kSwitch empty places in the
+// order: without them a share of many short tiles ended 15 us after the others (64 requests of 90 to
+// 8100 positions, 77 us).
+// Aligned: no empty places, each tile's units padded to whole chunks, so that no workgroup crosses from
+// one tile into the next.  Taken where the chunks this needs, work / (target - tiles), are no longer than
+// the shares: with few tiles, that is.
 struct KvShare {
   long long total, chunk;
   bool aligned;
@@ -111,7 +113,7 @@ constexpr int kSwitch = 8;
 // units of a tile, its length in the order, and a request's per kv head
 __device__ __forceinline__ long long kv_step(const KvRequest& q, const KvShare& sh) {
   const int units = max(1, q.hi - q.lo);
-  return sh.aligned ? div_i64(units + sh.chunk - 1, sh.chunk) * sh.chunk : units;
+  return sh.aligned ? div_i64(units + sh.chunk - 1, sh.chunk) * sh.chunk : units + kSwitch;
 }
 __device__ __forceinline__ long long kv_units(const KvRequest& q, const KvShare& sh) {
   return q.tiles * kv_step(q, sh);
@@ -140,13 +142,15 @@ __device__ __forceinline__ bool kv_locate_in(const KvAttentionProblem& a, const 
   const int lane = threadIdx.x & 63, hkv = a.cache.kv_heads;
   auto quot = [](I x, I y) { return (I)(sizeof(I) == 4 ? (uint32_t)x / (uint32_t)y : div_i64(x, y)); };
   // whole rounds of the four waves
-  auto chunk_of = [&](I workgroups) { return max((I)s.min_chunk, (quot(work + workgroups - 1, workgroups) + 3) & ~(I)3); };
-  I chunk = chunk_of(s.target);
+  auto chunk_of = [&](I all, I workgroups) {
+    return max((I)s.min_chunk, (quot(all + workgroups - 1, workgroups) + 3) & ~(I)3);
+  };
+  I chunk = chunk_of(work + kSwitch * all_tiles, s.target);
   bool aligned = false;
   if (all_tiles < s.target) {
-    const I longer = chunk_of(s.target - all_tiles);
-    aligned = longer <= chunk + kSwitch;
-    if (aligned) chunk = longer;
+    const I padded = chunk_of(work, s.target - all_tiles);
+    aligned = padded <= chunk;
+    if (aligned) chunk = padded;
   }
   sh->chunk = chunk;
   sh->aligned = aligned;
@@ -158,7 +162,7 @@ __device__ __forceinline__ bool kv_locate_in(const KvAttentionProblem& a, const 
       q = KvRequest{};
       if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
     }
-    const I units = max(1, q.hi - q.lo), step = aligned ? quot(units + chunk - 1, chunk) * chunk : units;
+    const I units = max(1, q.hi - q.lo), step = aligned ? quot(units + chunk - 1, chunk) * chunk : units + kSwitch;
     const I mine = step * q.tiles * hkv, scan = wave_scan(mine);
     I key = scan, own = mine, first = base;
     if (BY_TILE) {
@@ -186,8 +190,8 @@ __device__ __forceinline__ bool kv_locate_in(const KvAttentionProblem& a, const 
 
 // The shares, and the request that holds order position index * chunk (BY_TILE: tile `index` of the
 // launch, counted over requests, heads and tiles), with the place in it.  One whole wave; false past the
-// end.  Up to 64 requests of less than 2^23 units each go the short way, in 32 bits (padding to
-// chunks at most doubles the work).
+// end.  Up to 64 requests of less than 2^23 units and 2^18 tiles each go the short way, in 32 bits (padding
+// to chunks at most doubles the work).
 template <bool BY_TILE>
 __device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvSchedule& s, int index, KvShare* sh,
                                           KvWhere* out, long long* within) {
@@ -202,7 +206,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvS
   }
   work *= hkv;
   all_tiles *= hkv;
-  if (a.R <= 64 && !__any(work >= (1 << 23) || all_tiles >= (1 << 23)))
+  if (a.R <= 64 && !__any(work >= (1 << 23) || all_tiles >= (1 << 18)))
     return kv_locate_in<BY_TILE, int>(a, s, index, q, lane_value(wave_scan((int)work), 63),
                                       lane_value(wave_scan((int)all_tiles), 63), sh, out, within);
   return kv_locate_in<BY_TILE, long long>(a, s, index, q, wave_sum_i64(work), wave_sum_i64(all_tiles), sh, out, within);
