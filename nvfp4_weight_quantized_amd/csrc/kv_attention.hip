@@ -176,13 +176,13 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
   long long local;
   constexpr bool kWhole = NW > 4;     // a whole tile per workgroup
   if (!kv_locate<kWhole>(a, s, blockIdx.x, &sh, &at, &local)) return;
-  int left = kWhole ? max(1, at.q.hi - at.q.lo) : (int)min(sh.chunk, sh.total - (long long)blockIdx.x * sh.chunk);
+  int left = kWhole ? max(1, at.q.units) : (int)min(sh.chunk, sh.total - (long long)blockIdx.x * sh.chunk);
   const int chunk = (int)min(sh.chunk, (long long)(1 << 28));
   const int upp = a.cache.page_size / kKvUnit;
   bool first = true;
 
   while (true) {
-    const int units = max(1, at.q.hi - at.q.lo);
+    const int units = max(1, at.q.units);
     const long long step = kWhole ? 1 : kv_step(at.q, sh), nth = div_i64(local, step);
     // place in the tile: `lead` empty places before unit 0
     const int lead = kWhole || sh.aligned ? 0 : kSwitch, place = (int)(local - nth * step), unit = max(0, place - lead);
@@ -196,8 +196,8 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
     const int pos_min = pos0 + row_base / a.G, pos_max = pos0 + (min(row_base + BM, rows) - 1) / a.G;
     const int see_all = a.window > 0 ? (int)max(0ll, (long long)pos_max - a.window + 1) : 0;
     const int see_any = a.window > 0 ? (int)max(0ll, (long long)pos_min - a.window + 1) : 0;
-    const int u0 = max(at.q.lo + unit, see_any / kKvUnit);
-    const int u1 = pos_max < 0 ? u0 : min(at.q.lo + unit + count, pos_max / kKvUnit + 1);
+    const int u0 = see_any / kKvUnit + unit;
+    const int u1 = pos_max < 0 ? u0 : min(u0 + count, pos_max / kKvUnit + 1);
     const int32_t* table = a.table + (size_t)at.r * a.width;
 
     // the wave's units u0 + wave + NW*i, i < mine; lane i & 63 holds the address of unit i of a batch of 64
@@ -501,8 +501,13 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
 //     16t + 4z + {0..3} and 16t + 8 + 4z + {0..3}: the ones whose scores lane 32z + n holds after S^T.
 // RS = 16, the 16x16x32 instruction: the operands as the cache holds them (value operand, range r: the
 //   even elements, then the odd ones).  Half the rows per operand read, which LDS bandwidth then bounds at
-//   half the matrix rate; taken for head dimension 256, whose 32-row outputs and queries leave no registers
-//   to overlap anything (128 + 64 of 256; measured 263 us against RSTIME us for chunks of 5 requests).
+//   half the matrix rate, and twice the tiles.  Taken where those fill the card better (plan_launches), and
+//   for head dimension 256, whose 32-row outputs and queries (128 + 64 of 256 registers) leave none to
+//   overlap anything: 249 us against 263 us for the chunks of 5 requests (16/2 heads, window 1024).
+// Bound by the vector unit and LDS beside the matrix unit: a prompt of 8192 (32/8 heads, dimension 128)
+// runs at 955-993 TFLOP/s, the matrix unit 45% busy, 7.6 vector instructions per 32-cycle matrix
+// instruction (32 exponentials, 32 fused multiply-adds, 37 additions, 16 conversions, 16 maxima and the
+// wave's eighth of the dequantization per 32 of them).
 template <int D, int NW, int NU, int RS>
 __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttentionProblem a,
                                                                                       KvSchedule s, KvPartials part) {
@@ -528,6 +533,30 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
   }
   const int rows = it.q.n * a.G, row_base = it.tile * BM;
   const int pos0 = it.q.len - it.q.n;
+
+  // positions that the rows of [first, last) see: all of [*see_all, *pos_min], none outside
+  // [*see_any, *pos_max]
+  auto reach = [&](int first, int last, int* pos_min, int* pos_max, int* see_all, int* see_any) {
+    *pos_min = pos0 + first / a.G;
+    *pos_max = pos0 + (min(last, rows) - 1) / a.G;
+    *see_all = a.window > 0 ? (int)max(0ll, (long long)*pos_max - a.window + 1) : 0;
+    *see_any = a.window > 0 ? (int)max(0ll, (long long)*pos_min - a.window + 1) : 0;
+  };
+  int pos_min, pos_max, see_all, see_any, u0, u1;
+  {
+    int t0, t1, t2, t3;
+    reach(row_base, row_base + BM, &t0, &t1, &t2, &t3);
+    u0 = t3 / kKvUnit + it.split * it.chunk;
+    u1 = t1 < 0 ? u0 : min(u0 + min(it.chunk, it.q.units - it.split * it.chunk), t1 / kKvUnit + 1);
+  }
+  if (u0 >= u1 && it.splits > 1) {      // nothing in this split: an empty partial sum, whose outputs are not read
+    const size_t slot = (size_t)(it.slot + it.split) * hkv + h;
+    for (int r = tid; r < min(BM, rows - row_base); r += THREADS) {
+      part.ml[slot * 2 * BM + r] = kNone;
+      part.ml[slot * 2 * BM + BM + r] = 0.f;
+    }
+    return;
+  }
 
   // query operands: row nrow of the wave, elements [16t + 8z, +8) (RS = 16: [32t + 8z, +8))
   const int row = row_base + RS * wave + nrow;
@@ -557,21 +586,6 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
       qf[t] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
     }
     c = ldexpf(a.scale * kLog2e, -sh);
-  }
-  // positions that the rows of [first, last) see: all of [*see_all, *pos_min], none outside
-  // [*see_any, *pos_max]
-  auto reach = [&](int first, int last, int* pos_min, int* pos_max, int* see_all, int* see_any) {
-    *pos_min = pos0 + first / a.G;
-    *pos_max = pos0 + (min(last, rows) - 1) / a.G;
-    *see_all = a.window > 0 ? (int)max(0ll, (long long)*pos_max - a.window + 1) : 0;
-    *see_any = a.window > 0 ? (int)max(0ll, (long long)*pos_min - a.window + 1) : 0;
-  };
-  int pos_min, pos_max, see_all, see_any, u0, u1;
-  {
-    int t0, t1, t2, t3;
-    reach(row_base, row_base + BM, &t0, &t1, &t2, &t3);
-    u0 = max(it.q.lo + it.split * it.chunk, t3 / kKvUnit);
-    u1 = t1 < 0 ? u0 : min(min(it.q.lo + it.split * it.chunk + it.chunk, it.q.hi), t1 / kKvUnit + 1);
   }
   const int wrow = row_base + RS * wave;
   reach(min(wrow, rows - 1), wrow + RS, &pos_min, &pos_max, &see_all, &see_any);
@@ -926,7 +940,7 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
     q = at.q;
     h = (int)within / q.tiles;
     tile = (int)within - h * q.tiles;
-    const int units = max(1, q.hi - q.lo);
+    const int units = max(1, q.units);
     const long long begin = at.base + within * kv_step(q, sh) + (sh.aligned ? 0 : kSwitch), i0 = div_i64(begin, sh.chunk),
                     i1 = div_i64(begin + units - 1, sh.chunk);
     if (i0 == i1) return;
@@ -976,14 +990,17 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
       float most = fmaxf(mi, top);
 #pragma unroll
       for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
-      const float f = exp2_hw(top - most), w = lane < n ? exp2_hw(mi - most) : 0.f;
+      const float f = exp2_hw(top - most), w = li != 0.f ? exp2_hw(mi - most) : 0.f;
       top = most;
       sum = sum * f + w * li;
       v *= f;
       for (int j = 0; j < n; j += kLoads * PER) {
         if (j > 0) load(j);
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) v += __shfl(w, min(j + k * PER + sub, 63)) * x[k];
+        for (int k = 0; k < kLoads; ++k) {
+          const float wk = __shfl(w, min(j + k * PER + sub, 63));
+          v += wk * (wk != 0.f ? x[k] : f32x4{0.f, 0.f, 0.f, 0.f});      // an empty partial's outputs were not written
+        }
       }
     }
 #pragma unroll
@@ -1007,6 +1024,7 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
 struct Launch {
   bool shares;        // few-row kernel (equal shares) or tile kernel (items)
   bool whole;         // few-row kernel, whole tiles: no partial sums, no combine launch
+  int rs;             // tile kernel: rows per wave
   KvSchedule s;
   int64_t grid;       // workgroups
   int64_t tiles;      // bound on the row tiles over all heads
@@ -1016,7 +1034,8 @@ struct Launch {
 constexpr int kCus = 256;              // compute units of the card
 constexpr int kRowsMinChunk = 4;       // units: one per wave
 constexpr int kTilesTarget = 512;
-constexpr int kTilesMinChunk = 16;
+constexpr int kTilesMinChunk = 8;      // units: four steps
+constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
 constexpr int kWholeUnits = 64;        // block tables of at most so many units, and
 constexpr int kWholeTiles = 256;       // at most so many tiles: one workgroup of 8 waves takes a tile whole
 constexpr int kRowsSplit = 64;         // requests of more rows go to the tile kernel where both run
@@ -1071,8 +1090,16 @@ Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, 
   const int64_t rows = (int64_t)T * G;
   const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
   const bool few = !tiles || R > 1;
-  if (tiles) x.l[x.n++] = plan_launch(false, D == 256 ? 128 : 256, few ? kRowsSplit : 0, 0x7FFFFFFF, T, R, G, hkv, D,
-                                     table_units);
+  if (tiles) {
+    // 32 rows per wave (256 per tile) at twice the rate, 16 rows (128) with twice the tiles.  Measured, 32/8
+    // heads, dimension 128: prompt of 8192 (264k units over all tiles) 572 against 849 us, 512 tokens on
+    // 20000 positions (46k) 211 against 275 us, prompt of 2000 (17k) 105 against 75 us.  The host knows the
+    // table's width, not the lengths; a wide table only means the slower of the two for a short step.
+    const int64_t wide = std::min((int64_t)R, (int64_t)T) + rows / 256;
+    const int rs = D != 256 && wide * hkv * std::min(table_units, (int64_t)1 << 26) >= kWideWork ? 32 : 16;
+    x.l[x.n] = plan_launch(false, 8 * rs, few ? kRowsSplit : 0, 0x7FFFFFFF, T, R, G, hkv, D, table_units);
+    x.l[x.n++].rs = rs;
+  }
   if (few) {
     const int bm = tiles || rows > 16 * (int64_t)R ? 32 : 16;
     x.l[x.n++] = plan_launch(true, bm, 0, tiles ? kRowsSplit : 0x7FFFFFFF, T, R, G, hkv, D, table_units);
@@ -1103,7 +1130,12 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
       constexpr int DD = decltype(tag)::value;
       const dim3 grid((unsigned)p.grid), rows((unsigned)p.tiles, p.shares ? p.s.bm / 8 : 4);
       if (!p.shares) {
-        hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, 8, DD == 256 ? 1 : 2, DD == 256 ? 16 : 32>), grid, dim3(512), 0, stream, a, p.s, part);
+        if (DD != 256 && p.rs == 32)
+          hipLaunchKernelGGL((kv_attention_tiles_kernel<DD == 256 ? 128 : DD, 8, 2, 32>), grid, dim3(512), 0, stream, a,
+                             p.s, part);
+        else
+          hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, 8, DD == 256 ? 1 : 2, 16>), grid, dim3(512), 0, stream, a,
+                             p.s, part);
         hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
       } else {
         if (p.whole)

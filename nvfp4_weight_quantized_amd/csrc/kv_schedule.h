@@ -3,7 +3,8 @@
 //
 // Items:
 // A request r with n query tokens has n * G rows per kv head (row = token * G + head of the group), cut
-// into tiles of BM rows, and the units (32 positions) [lo, hi) that its rows see.  The units are cut
+// into tiles of BM rows, each of which sees at most `units` units (32 positions): all of them, or with a
+// window those that its rows' windows reach.  A tile's units, counted from the first one it sees, are cut
 // into splits of C units, C chosen so that the items of one kv head number about `target`:
 //   C = max(min_chunk, ceil(sum_r tiles_r * units_r / target)).
 // Items are ordered by request, tile, split; a tile of a request with one split writes its rows, the
@@ -24,7 +25,7 @@ struct KvRequest {
   int row0;     // first token row
   int len;      // positions held
   int tiles;    // row tiles (0: not of this launch)
-  int lo, hi;   // units seen
+  int units;    // units a tile sees at most
 };
 
 struct KvItem {
@@ -53,10 +54,10 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttentionProblem& a, con
   const int rows = q.n * a.G;
   if (rows <= s.min_rows || rows > s.max_rows) return q;
   q.tiles = (rows + s.bm - 1) / s.bm;
-  // first position that the first row sees
-  const long long first = a.window > 0 ? (long long)q.len - q.n - a.window + 1 : 0;
-  q.lo = (int)(max(first, 0ll) / kKvUnit);
-  q.hi = max(q.lo, (int)(((long long)q.len + kKvUnit - 1) / kKvUnit));
+  long long units = ((long long)q.len + kKvUnit - 1) / kKvUnit;
+  if (a.window > 0)      // a tile spans at most (bm - 1) / G + 2 tokens, their windows that many less 1 + window positions
+    units = min(units, ((long long)((s.bm - 1) / a.G + 1) + a.window + 2 * kKvUnit - 2) / kKvUnit);
+  q.units = (int)units;
   return q;
 }
 
@@ -112,7 +113,7 @@ struct KvWhere {
 constexpr int kSwitch = 8;
 // units of a tile, its length in the order, and a request's per kv head
 __device__ __forceinline__ long long kv_step(const KvRequest& q, const KvShare& sh) {
-  const int units = max(1, q.hi - q.lo);
+  const int units = max(1, q.units);
   return sh.aligned ? div_i64(units + sh.chunk - 1, sh.chunk) * sh.chunk : units + kSwitch;
 }
 __device__ __forceinline__ long long kv_units(const KvRequest& q, const KvShare& sh) {
@@ -125,8 +126,7 @@ __device__ __forceinline__ KvRequest lane_request(const KvRequest& q, int src) {
   o.row0 = __builtin_amdgcn_readlane(q.row0, src);
   o.len = __builtin_amdgcn_readlane(q.len, src);
   o.tiles = __builtin_amdgcn_readlane(q.tiles, src);
-  o.lo = __builtin_amdgcn_readlane(q.lo, src);
-  o.hi = __builtin_amdgcn_readlane(q.hi, src);
+  o.units = __builtin_amdgcn_readlane(q.units, src);
   return o;
 }
 
@@ -162,7 +162,7 @@ __device__ __forceinline__ bool kv_locate_in(const KvAttentionProblem& a, const 
       q = KvRequest{};
       if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
     }
-    const I units = max(1, q.hi - q.lo), step = aligned ? quot(units + chunk - 1, chunk) * chunk : units + kSwitch;
+    const I units = max(1, q.units), step = aligned ? quot(units + chunk - 1, chunk) * chunk : units + kSwitch;
     const I mine = step * q.tiles * hkv, scan = wave_scan(mine);
     I key = scan, own = mine, first = base;
     if (BY_TILE) {
@@ -201,7 +201,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvS
   for (int r0 = 0; r0 < a.R; r0 += 64) {
     q = KvRequest{};
     if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
-    work += (long long)q.tiles * max(1, q.hi - q.lo);
+    work += (long long)q.tiles * max(1, q.units);
     all_tiles += q.tiles;
   }
   work *= hkv;
@@ -219,7 +219,7 @@ __device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSch
   long long work = 0;
   for (int r = lane; r < a.R; r += 64) {
     const KvRequest q = kv_request(a, s, r);
-    work += (long long)q.tiles * (q.hi - q.lo);
+    work += (long long)q.tiles * q.units;
   }
   work = wave_sum_i64(work);
   const int chunk = (int)max((long long)s.min_chunk, (work + s.target - 1) / s.target);
@@ -228,7 +228,7 @@ __device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSch
     const int r = r0 + lane;
     KvRequest q{};
     if (r < a.R) q = kv_request(a, s, r);
-    const int splits = max(1, (int)(((long long)(q.hi - q.lo) + chunk - 1) / chunk));
+    const int splits = max(1, (int)(((long long)q.units + chunk - 1) / chunk));
     const int items = q.tiles * splits, count = BY_TILE ? q.tiles : items;
     const int part = splits > 1 ? items : 0;
     int ic = count, ip = part;
@@ -250,8 +250,7 @@ __device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSch
       out->q.row0 = __builtin_amdgcn_readlane(q.row0, src);
       out->q.len = __builtin_amdgcn_readlane(q.len, src);
       out->q.tiles = __builtin_amdgcn_readlane(q.tiles, src);
-      out->q.lo = __builtin_amdgcn_readlane(q.lo, src);
-      out->q.hi = __builtin_amdgcn_readlane(q.hi, src);
+      out->q.units = __builtin_amdgcn_readlane(q.units, src);
       out->splits = __builtin_amdgcn_readlane(splits, src);
       out->chunk = chunk;
       out->tile = BY_TILE ? within : within / out->splits;
