@@ -212,56 +212,57 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvS
   return kv_locate_in<BY_TILE, long long>(a, s, index, q, wave_sum_i64(work), wave_sum_i64(all_tiles), sh, out, within);
 }
 
-// Item `index` (BY_TILE: all splits of tile `index`); false past the last.  One whole wave.
-template <bool BY_TILE>
-__device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSchedule& s, int index, KvItem* out) {
+// kv_find in integers of type I, which hold the whole work; `q` is lane r's request when R <= 64.
+template <bool BY_TILE, typename I>
+__device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const KvSchedule& s, int index, KvRequest q,
+                                           I work, KvItem* out) {
   const int lane = threadIdx.x & 63;
-  long long work = 0;
-  for (int r = lane; r < a.R; r += 64) {
-    const KvRequest q = kv_request(a, s, r);
-    work += (long long)q.tiles * q.units;
-  }
-  work = wave_sum_i64(work);
-  const int chunk = (int)max((long long)s.min_chunk, (work + s.target - 1) / s.target);
+  auto quot = [](I x, I y) { return (I)(sizeof(I) == 4 ? (uint32_t)x / (uint32_t)y : div_i64(x, y)); };
+  const int chunk = (int)min((I)(1 << 27), max((I)s.min_chunk, quot(work + s.target - 1, s.target)));   // units < 2^27
   int base = 0, slots = 0;
   for (int r0 = 0; r0 < a.R; r0 += 64) {
-    const int r = r0 + lane;
-    KvRequest q{};
-    if (r < a.R) q = kv_request(a, s, r);
-    const int splits = max(1, (int)(((long long)q.units + chunk - 1) / chunk));
+    if (a.R > 64) {
+      q = KvRequest{};
+      if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
+    }
+    const int splits = max(1, (int)(((uint32_t)q.units + chunk - 1) / (uint32_t)chunk));
     const int items = q.tiles * splits, count = BY_TILE ? q.tiles : items;
     const int part = splits > 1 ? items : 0;
-    int ic = count, ip = part;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int x = __shfl_up(ic, off), y = __shfl_up(ip, off);
-      if (lane >= off) {
-        ic += x;
-        ip += y;
-      }
-    }
+    const int ic = wave_scan(count), ip = wave_scan(part);
     const int excl = base + ic - count;
     const uint64_t hit = __ballot(excl <= index && index < excl + count);
     if (hit) {
       const int src = __ffsll((unsigned long long)hit) - 1;
-      const int within = index - __builtin_amdgcn_readlane(excl, src);
+      const int within = index - lane_value(excl, src);
       out->r = r0 + src;
-      out->q.n = __builtin_amdgcn_readlane(q.n, src);
-      out->q.row0 = __builtin_amdgcn_readlane(q.row0, src);
-      out->q.len = __builtin_amdgcn_readlane(q.len, src);
-      out->q.tiles = __builtin_amdgcn_readlane(q.tiles, src);
-      out->q.units = __builtin_amdgcn_readlane(q.units, src);
-      out->splits = __builtin_amdgcn_readlane(splits, src);
+      out->q = lane_request(q, src);
+      out->splits = lane_value(splits, src);
       out->chunk = chunk;
       out->tile = BY_TILE ? within : within / out->splits;
       out->split = BY_TILE ? 0 : within % out->splits;
-      out->slot = slots + __builtin_amdgcn_readlane(ip - part, src) + out->tile * out->splits;
+      out->slot = slots + lane_value(ip - part, src) + out->tile * out->splits;
       return true;
     }
-    base += __builtin_amdgcn_readlane(ic, 63);
-    slots += __builtin_amdgcn_readlane(ip, 63);
+    base += lane_value(ic, 63);
+    slots += lane_value(ip, 63);
   }
   return false;
+}
+
+// Item `index` (BY_TILE: all splits of tile `index`); false past the last.  One whole wave.
+template <bool BY_TILE>
+__device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSchedule& s, int index, KvItem* out) {
+  const int lane = threadIdx.x & 63;
+  KvRequest q{};
+  long long work = 0;
+  for (int r0 = 0; r0 < a.R; r0 += 64) {
+    q = KvRequest{};
+    if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
+    work += (long long)q.tiles * q.units;
+  }
+  if (a.R <= 64 && !__any(work >= (1 << 24)))
+    return kv_find_in<BY_TILE, int>(a, s, index, q, lane_value(wave_scan((int)work), 63), out);
+  return kv_find_in<BY_TILE, long long>(a, s, index, q, wave_sum_i64(work), out);
 }
 
 }  // namespace
