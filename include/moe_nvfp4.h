@@ -533,12 +533,15 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, c
  * window.  out [T][Hq][D] bf16 = softmax(scale * q.k) v over the positions seen; lse [T][Hq] fp32 (or
  * NULL) the natural logarithm of the sum of exponentials.  A row that sees nothing gets zeros and
  * lse = -inf.  Rows outside every request are left as they were.  A row that sees a position whose
- * block table entry is outside [0, num_pages), or beyond the table, becomes NaN.
+ * block table entry is outside [0, num_pages), or beyond the table, becomes NaN.  Tokens at T and beyond
+ * (query_offsets[R] > T, which moe_kv_plan reports) have no row; the others keep their positions.
  * Products are exact (q re-encoded as fp16 under a power of two per row, keys and values as fp16) and
  * sums fp32; the probabilities are rounded to fp16 (11 bits) for the value product only.
  * Deterministic; a row's result depends on the other requests of the call only through the order in
  * which its partial sums are added.
- * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; scale finite and positive; window >= 0.
+ * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; R * table_width < 2^31; scale finite and
+ * positive, scale * k_gscale within [2^-126, 2^100]; window >= 0; query_offsets ascending; seq_lens <= 2^31 - 4096
+ * (a greater one counts as that); out overlaps no input.
  * workspace: moe_nvfp4_kv_attention_workspace_size bytes, 16-byte aligned. */
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);
 moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q, int64_t q_stride,

@@ -95,7 +95,7 @@ moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache, const uin
   if ((int64_t)R * table_width >= ((int64_t)1 << 31)) return MOE_ERR_INVALID_ARGUMENT;
   if (!(std::isfinite(scale) && scale > 0.f) || window < 0) return MOE_ERR_INVALID_ARGUMENT;
   const float s = scale * cache->k_gscale;
-  if (!std::isnormal(s)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(s >= 0x1p-126f && s <= 0x1p100f)) return MOE_ERR_INVALID_ARGUMENT;
   if (T > 1 && (q_stride < (int64_t)Hq * cache->head_dim || q_stride % 8 != 0)) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0 || R == 0) return MOE_OK;
   if (!q || !out || !query_offsets || !seq_lens || !al16(q) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;

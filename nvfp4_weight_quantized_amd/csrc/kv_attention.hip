@@ -509,8 +509,8 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
 // instruction (32 exponentials, 32 fused multiply-adds, 37 additions, 16 conversions, 16 maxima and the
 // wave's eighth of the dequantization per 32 of them).
 template <int D, int NW, int NU, int RS>
-__global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttentionProblem a,
-                                                                                      KvSchedule s, KvPartials part) {
+__global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttentionProblem a, KvSchedule s,
+                                                                        KvPartials part) {
   using U = KvUnit<D>;
   constexpr int NS = D / 32, NT = D / 16, BM = RS * NW, THREADS = 64 * NW;
   constexpr bool kWide = RS == 32;

@@ -47,10 +47,12 @@ struct KvSchedule {
 
 __device__ __forceinline__ KvRequest kv_request(const KvAttentionProblem& a, const KvSchedule& s, int r) {
   KvRequest q{};
-  const int b0 = min(max(a.offsets[r], 0), a.T), b1 = min(max(a.offsets[r + 1], b0), a.T);
+  const int b0 = min(max(a.offsets[r], 0), a.T), end = max(a.offsets[r + 1], b0), b1 = min(end, a.T);
   q.row0 = b0;
   q.n = b1 - b0;
-  q.len = max(a.lens[r], 0);
+  // Tokens past the last row have no row, and the positions from theirs on are seen by none.  Below 2^31 by
+  // more than any unit that a kernel looks at ahead.
+  q.len = (int)max(min((long long)a.lens[r], 0x7FFFF000ll) - (end - b1), 0ll);
   const int rows = q.n * a.G;
   if (rows <= s.min_rows || rows > s.max_rows) return q;
   q.tiles = (rows + s.bm - 1) / s.bm;

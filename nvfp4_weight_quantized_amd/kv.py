@@ -28,6 +28,7 @@ HEAD_DIMS = (64, 128, 256)
 _I32, _BF16 = torch.int32, torch.bfloat16
 _raw_stream = torch._C._cuda_getCurrentRawStream      # device index -> hipStream_t
 _NOTHING = contextlib.nullcontext()
+_I32_END = 2 ** 31
 
 
 def _on(index: int):
@@ -51,9 +52,9 @@ class NvFp4KvCache:
     ``pages`` uint8 [num_pages, kv_heads, page_size / 32, 36 * head_dim], contiguous; ``page_size``
     positions per page (a multiple of 32); ``k_gscale`` and ``v_gscale`` the dequant global scales
     (a cached element is e2m1 * e4m3 * gscale).  The content of new pages does not matter: positions
-    past a request's length are never used.
+    past a request's length are never used.  All of them are fixed for the life of the object.
     """
-    __slots__ = ("pages", "page_size", "k_gscale", "v_gscale", "_struct", "_dev")
+    __slots__ = ("_pages", "_struct", "_dev")
 
     def __init__(self, pages: torch.Tensor, page_size: int, k_gscale: float = 1.0, v_gscale: float = 1.0):
         _need(pages, "pages", torch.uint8, 4)
@@ -67,7 +68,7 @@ class NvFp4KvCache:
         for name, d in (("k_gscale", k_gscale), ("v_gscale", v_gscale)):
             if not 2.0 ** -64 <= d <= 2.0 ** 64:      # also refuses NaN
                 raise ValueError(f"{name}: a dequant global scale lies in [2^-64, 2^64], got {d!r}")
-        self.pages, self.page_size, self.k_gscale, self.v_gscale = pages, page_size, float(k_gscale), float(v_gscale)
+        self._pages = pages
         self._struct = L.KvCache(p, page_size, h, b // 36, k_gscale, v_gscale, pages.data_ptr())
         self._dev = pages.device
 
@@ -79,6 +80,22 @@ class NvFp4KvCache:
             raise ValueError(f"head_dim in {HEAD_DIMS} and page_size a multiple of {_UNIT} expected")
         return cls(torch.zeros(num_pages, kv_heads, page_size // _UNIT, 36 * head_dim, dtype=torch.uint8,
                                device=device), page_size, k_gscale, v_gscale)
+
+    @property
+    def pages(self) -> torch.Tensor:
+        return self._pages
+
+    @property
+    def page_size(self) -> int:
+        return self._struct.page_size
+
+    @property
+    def k_gscale(self) -> float:
+        return self._struct.k_gscale
+
+    @property
+    def v_gscale(self) -> float:
+        return self._struct.v_gscale
 
     @property
     def num_pages(self) -> int:
@@ -122,8 +139,10 @@ def kv_plan(kv_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
         _shape(new_lens, "new_lens", (r,))
     if rows != r:
         raise ValueError(f"block_table: {rows} rows for {r} requests")
-    if num_tokens < 0:
+    if not 0 <= num_tokens < _I32_END:
         raise ValueError(f"num_tokens {num_tokens}")
+    if page_size <= 0 or num_pages <= 0 or page_size * num_pages >= _I32_END:
+        raise ValueError(f"{num_pages} pages of {page_size} positions")
     # one allocation for the outputs
     sizes = (r + 1, r, num_tokens, num_tokens, 1)
     buf = torch.empty(2 * r + 2 * num_tokens + 2, dtype=_I32, device=dev)
@@ -234,14 +253,14 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
         scale = dim ** -0.5
     if not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError(f"scale must be finite and positive, got {scale!r}")
-    if window < 0:
+    if not 0 <= window < _I32_END:
         raise ValueError(f"window {window}")
     if out is None:
         out = torch.empty((t, heads, dim), dtype=_BF16, device=dev)
     else:
         _need(out, "out", _BF16, 3)
         _shape(out, "out", (t, heads, dim))
-        _same_device(cache.pages, ("out", out))
+        _same_device(cache._pages, ("out", out))
     lse = torch.empty((t, heads), dtype=torch.float32, device=dev) if return_lse else None
     lib = L.lib()
     if workspace is None:
@@ -249,7 +268,7 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
                                 dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8)
-        _same_device(cache.pages, ("workspace", workspace))
+        _same_device(cache._pages, ("workspace", workspace))
     with _on(dev.index):
         st = lib.moe_nvfp4_kv_attention(
             c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,

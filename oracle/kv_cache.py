@@ -138,7 +138,7 @@ def attention(q, pages, page_size, k_gscale, v_gscale, offsets, lens, table, sca
         slots = slots_of(table[r], page_size, 0, length)
         k = decode(pages, page_size, slots, k_gscale, False)
         v = decode(pages, page_size, slots, v_gscale, True)
-        for t in range(a, b):
+        for t in range(a, min(b, t_n)):
             pos = length - (b - a) + (t - a)
             lo = max(0, pos - window + 1) if window else 0
             if pos < 0:

@@ -220,6 +220,7 @@ def test_attention_wrappers_refuse_before_any_launch():
     ok = dict(q=q, query_offsets=off, seq_lens=lens, block_table=table)
     for bad in (dict(q=q[:, :5]), dict(q=q[..., :32]), dict(q=q.transpose(0, 1)), dict(query_offsets=off[:2]),
                 dict(block_table=table[:1]), dict(scale=0.0), dict(scale=float("nan")), dict(window=-1),
+                dict(window=2 ** 32 + 5),
                 dict(out=torch.empty_like(q[:1])), dict(seq_lens=lens.cpu()),
                 dict(block_table=table.t().contiguous().t())):
         with pytest.raises(ValueError):
@@ -239,3 +240,120 @@ def test_no_rows_and_no_requests():
     out = torch.full_like(q, 3.0)
     kv.kv_attention(case.cache(), q, z, z[:0], torch.zeros(0, 4, dtype=torch.int32, device=DEV), out=out)
     assert (out == 3.0).all()
+
+
+# The host knows the width of the block table only: a narrow one lets few rows be taken tile by tile and
+# many in 16-row waves, a wide one makes the call cut every row's positions into shares and take 32-row waves.
+WIDE = 40000
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,reqs,window,pad", [
+    (8, DECODE, 0, 0),
+    (17, DECODE, 40, 3),
+    (64, [(1, 3), (2, 700), (1, 0)], 0, 0),
+    (4, MIXED, 0, 5),
+    (16, MIXED, 64, 0),
+    (1, [(300, 0)], 0, 2),
+    (1, [(270, 1500)], 333, 0),                      # every tile's window is cut
+    (4, [(333, 0), (1, 1800), (65, 1)], 0, 0),       # the first tiles see little: splits of theirs are empty
+    (3, [(100, 2000), (96, 0), (0, 50), (2, 31)], 70, 7),
+])
+def test_wide_block_tables(dim, group, reqs, window, pad):
+    case = kh.Case(dim + group, dim, 2, group, 32, reqs, window=window, pad=pad, width_extra=WIDE)
+    kh.check_attention(case, *case.run())
+
+
+@pytest.mark.parametrize("reqs", [[(1, 130), (1, 70)], [(40, 90), (50, 20)]])
+def test_a_bad_page_of_a_wide_table(reqs):
+    case = kh.Case(40, 128, 2, 4, 32, reqs, window=35, width_extra=WIDE)
+    good, good_lse = case.run()
+    for entry in (-1, case.pages.shape[0]):
+        save = case.table[0, 2]
+        case.table[0, 2] = entry                     # positions 64..95 of request 0
+        out, lse = case.run()
+        case.table[0, 2] = save
+        n0 = reqs[0][0]
+        pos = case.lens[0] - n0 + np.arange(n0)
+        hit = np.zeros(case.tokens, bool)
+        hit[:n0] = (pos >= 64) & (pos - 35 < 95)
+        h = torch.from_numpy(hit).to(DEV)
+        assert torch.isnan(out[h]).all() and torch.isnan(lse[h]).all()
+        assert torch.equal(out[~h], good[~h]) and torch.equal(lse[~h], good_lse[~h])
+
+
+@pytest.mark.parametrize("extra", [1, WIDE])
+def test_rows_before_the_first_position_beside_many_rows(extra):
+    case = kh.Case(41, 64, 2, 3, 32, [(90, 0), (4, 40), (70, 0)], width_extra=extra)
+    case.lens = np.array([31, 44, 0], np.int32)
+    out, lse = case.run()
+    kh.check_attention(case, out, lse)
+    assert torch.isneginf(lse[:59]).all() and (out[:59] == 0).all() and torch.isneginf(lse[94:]).all()
+
+
+@pytest.mark.parametrize("requests,most_new,most_old,extra", [
+    (65, 1, 90, 1), (130, 1, 300, 1), (600, 1, 3, 1), (600, 2, 3, 1), (70, 130, 40, 1), (70, 130, 40, 200), (200, 1, 0, 1)])
+def test_many_requests(requests, most_new, most_old, extra):
+    """More requests than lanes; shares that hold many short tiles; idle requests among them."""
+    rng = np.random.default_rng(requests + most_new)
+    reqs = [(int(rng.integers(0, most_new + 1)), int(rng.integers(0, most_old + 1))) for _ in range(requests)]
+    case = kh.Case(42, 64, 4, 2, 32, reqs, width_extra=extra)
+    kh.check_attention(case, *case.run())
+
+
+@pytest.mark.parametrize("reqs", [[(3, 60), (5, 20), (4, 9)], [(40, 60), (50, 20), (90, 3)]])
+@pytest.mark.parametrize("tokens", [1, 2, 6, 8, 60, 97])
+def test_fewer_rows_than_tokens(reqs, tokens):
+    """Tokens past the last row have no row; the others keep their positions."""
+    case = kh.Case(43, 64, 2, 4, 32, reqs)
+    tokens = min(tokens, case.tokens)
+    full, full_lse = case.run()
+    case.q = case.q[:tokens]
+    out, lse = case.run()
+    kh.check_attention(case, out, lse, rows=slice(0, tokens))
+    # the same rows of the whole step, within the bounds of both
+    ref, ref_lse, mags = case.reference()
+    tol, _ = kh.bounds(ref, ref_lse, mags, slice(0, tokens), int(case.lens.max()), 64)
+    assert np.all(np.abs((full[:tokens].double() - out.double()).cpu().numpy()) <= 2 * tol)
+
+
+@pytest.mark.parametrize("scale,d_k", [(2.0 ** -62, 2.0 ** -64), (2.0 ** -60, 2.0 ** -60), (2.0 ** 36, 2.0 ** 64)])
+@pytest.mark.parametrize("n", [2, 80])
+def test_zero_rows_at_the_ends_of_the_scales(scale, d_k, n):
+    """The factor of the scores at both ends of its range, rows of zeros and (below) of small elements
+    beside masked positions: no 0 * inf."""
+    case = kh.Case(44, 64, 1, 2, 32, [(n, 45), (1, 0)], d_k=d_k, sigma_k=d_k)
+    case.scale = scale
+    case.q[:] = 0.0
+    if scale < 1:
+        case.q[::2] = kh.bf16(np.random.default_rng(1), case.q[::2].shape, 2.0 ** -100)
+    out, lse = case.run()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    kh.check_attention(case, out, lse)
+
+
+def test_two_graphs_replayed_on_two_streams():
+    """Two captured calls have workspaces of their own: replayed at once, each gives the eager result."""
+    cases = [kh.Case(45, 128, 2, 8, 64, [(1, 2500), (1, 300)], width_extra=300), kh.Case(46, 128, 2, 4, 32, [(80, 900)])]
+    sets = [(c.cache(), kh.to_bf16(c.q), c.args()) for c in cases]
+    eager = [kv.kv_attention(c, q, *a, return_lse=True) for c, q, a in sets]
+    graphs, outs = [], []
+    for c, q, a in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(kv.kv_attention(c, q, *a, return_lse=True))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for out in outs:
+            out[0].zero_()
+            out[1].zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(outs, eager):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for c, got in zip(cases, eager):
+        kh.check_attention(c, *got)

@@ -246,3 +246,9 @@ def test_wrappers_refuse_before_any_launch():
     from nvfp4_weight_quantized_amd import MoeError
     with pytest.raises(MoeError):
         kv.kv_plan(z, z, t, z, 33, 2, 2)
+    for args in ((z, z, t, z, 32, 2, 2 ** 31), (z, z, t, z, 2 ** 32 + 32, 2, 2), (z, z, t, z, 32, 2 ** 32 + 2, 2)):
+        with pytest.raises(ValueError):
+            kv.kv_plan(*args)
+    for name in ("pages", "page_size", "k_gscale", "v_gscale"):      # the launches would not see a change
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))

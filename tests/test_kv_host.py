@@ -152,7 +152,7 @@ def _attend(cache, q=0x2000, stride=512, t=3, heads=4, off=0x3000, lens=0x3100, 
                                  dict(t=-1), dict(heads=0), dict(heads=3), dict(heads=2 * 65), dict(off=None),
                                  dict(lens=None), dict(r=-1), dict(r=4097), dict(table=None), dict(width=-1),
                                  dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-                                 dict(scale=1e-39), dict(window=-1), dict(out=None), dict(out=0x4008),
+                                 dict(scale=1e-39), dict(scale=2.0 ** 101), dict(window=-1), dict(out=None), dict(out=0x4008),
                                  dict(t=1 << 30), dict(r=4096, width=1 << 20)])
 def test_attention_refusals(bad):
     assert _attend(_cache(), **bad) == INV
