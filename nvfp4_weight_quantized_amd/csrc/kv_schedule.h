@@ -56,9 +56,13 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttentionProblem& a, con
   const int rows = q.n * a.G;
   if (rows <= s.min_rows || rows > s.max_rows) return q;
   q.tiles = (rows + s.bm - 1) / s.bm;
+  const int span = (s.bm - 1) / a.G + 1;      // the last row of a tile is at most so many positions behind the first
   long long units = ((long long)q.len + kKvUnit - 1) / kKvUnit;
-  if (a.window > 0)      // a tile spans at most (bm - 1) / G + 2 tokens, their windows that many less 1 + window positions
-    units = min(units, ((long long)((s.bm - 1) / a.G + 1) + a.window + 2 * kKvUnit - 2) / kKvUnit);
+  if (a.window > 0) units = min(units, ((long long)span + a.window + 2 * kKvUnit - 2) / kKvUnit);
+  // Behind the table every unit is bad, and a row that sees one is NaN: a tile needs none past those that
+  // hold the first position behind the table or the first one seen, whichever is later, of each of its rows.
+  // So a length far beyond the table costs no more than one that fills it.
+  units = min(units, (long long)a.width * (a.cache.page_size / kKvUnit) + span / kKvUnit + 2);
   q.units = (int)units;
   return q;
 }

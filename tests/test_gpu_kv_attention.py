@@ -357,3 +357,33 @@ def test_two_graphs_replayed_on_two_streams():
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for c, got in zip(cases, eager):
         kh.check_attention(c, *got)
+
+
+@pytest.mark.parametrize("group,n", [(1, 3), (1, 200), (4, 90), (8, 5), (8, 150)])
+@pytest.mark.parametrize("window", [0, 1, 40, 10 ** 6])
+def test_rows_behind_the_table_are_nan(group, n, window):
+    """A table of 64 positions: rows before its end are right, the others NaN, however far they lie behind
+    it and whatever their windows reach."""
+    case = kh.Case(47, 64, 2, group, 32, [(n, 20), (2, 5)], window=window)
+    full, case.table = case.table, np.ascontiguousarray(case.table[:, :2])
+    out, lse = case.run()
+    tail = slice(max(0, 64 - 20), n)
+    assert torch.isnan(out[tail]).all() and torch.isnan(lse[tail]).all()
+    case.table = full
+    keep = np.array([t for t in range(case.tokens) if t >= n or t < 64 - 20])
+    kh.check_attention(case, out, lse, rows=keep)
+    case.table = np.ascontiguousarray(full[:, :2])
+    for far in (70000, 2 ** 31 - 1):
+        case.lens[0] = far
+        again, again_lse = case.run()
+        assert torch.isnan(again[:n]).all() and torch.isnan(again_lse[:n]).all()
+        kh.check_attention(_second(case), again[n:], again_lse[n:])
+
+
+def _second(case):
+    """The second request of a case, as a case of its own."""
+    import copy
+    c = copy.copy(case)
+    n = int(case.offsets[1])
+    c.q, c.offsets, c.lens, c.table = case.q[n:], case.offsets[1:] - n, case.lens[1:], case.table[1:]
+    return c
