@@ -1033,7 +1033,7 @@ struct Launch {
 
 constexpr int kCus = 256;              // compute units of the card
 constexpr int kRowsMinChunk = 4;       // units: one per wave
-constexpr int kTilesTarget = 512;
+constexpr int kTilesTarget = kCus;     // one workgroup is resident per compute unit
 constexpr int kTilesMinChunk = 8;      // units: four steps
 constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
 constexpr int kWholeUnits = 64;        // block tables of at most so many units, and

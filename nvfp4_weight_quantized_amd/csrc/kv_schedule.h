@@ -5,8 +5,11 @@
 // A request r with n query tokens has n * G rows per kv head (row = token * G + head of the group), cut
 // into tiles of BM rows, each of which sees at most `units` units (32 positions): all of them, or with a
 // window those that its rows' windows reach.  A tile's units, counted from the first one it sees, are cut
-// into splits of C units, C chosen so that the items of one kv head number about `target`:
+// into equal splits of about C units, C chosen so that the items of one kv head number about `target`:
 //   C = max(min_chunk, ceil(sum_r tiles_r * units_r / target)).
+// What exceeds a multiple of C by less than a quarter of it makes no further split: a tile cut for a few
+// units pays for the partial sums and their joining (2 prompts of 900, 16/8 heads, dimension 64:
+// 43.4 against 28.7 us).
 // Items are ordered by request, tile, split; a tile of a request with one split writes its rows, the
 // others leave partial sums in `slots` numbered the same way, which the combine launch adds in split
 // order.  Every workgroup finds its own item with two passes over the lengths (no host knowledge, no
@@ -231,7 +234,7 @@ __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const Kv
       q = KvRequest{};
       if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
     }
-    const int splits = max(1, (int)(((uint32_t)q.units + chunk - 1) / (uint32_t)chunk));
+    const int splits = (int)((uint32_t)(max(0, q.units - 1 - chunk / 4)) / (uint32_t)chunk) + 1;
     const int items = q.tiles * splits, count = BY_TILE ? q.tiles : items;
     const int part = splits > 1 ? items : 0;
     const int ic = wave_scan(count), ip = wave_scan(part);
@@ -243,7 +246,7 @@ __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const Kv
       out->r = r0 + src;
       out->q = lane_request(q, src);
       out->splits = lane_value(splits, src);
-      out->chunk = chunk;
+      out->chunk = (int)((uint32_t)(out->q.units + out->splits - 1) / (uint32_t)out->splits);
       out->tile = BY_TILE ? within : within / out->splits;
       out->split = BY_TILE ? 0 : within % out->splits;
       out->slot = slots + lane_value(ip - part, src) + out->tile * out->splits;
