@@ -133,6 +133,31 @@ def test_append_writes_the_oracles_bytes(dim, heads, page, t, d_k, d_v):
     assert np.array_equal(p_ref.cpu().numpy(), pk) and np.array_equal(s_ref.cpu().numpy(), sk)
 
 
+@pytest.mark.parametrize("dim,heads", [(64, 64), (128, 33), (256, 16)])
+@pytest.mark.parametrize("runs,page", [([(0, 528)], 96), ([(3, 40), (64, 33), (31, 1), (0, 200), (90, 259)], 64)])
+def test_append_of_runs_writes_the_oracles_bytes(dim, heads, runs, page):
+    """Enough rows for quads of positions: runs that fill units, begin and end inside units and quads, and
+    meet in one window of rows; bytes of other positions stay."""
+    rng = np.random.default_rng(dim + len(runs))
+    slots, at = [], 0
+    for first, n in runs:                          # each run has pages of its own
+        pages_of = rng.permutation(-(-(first + n) // page)) + at
+        at += len(pages_of)
+        pos = first + np.arange(n)
+        slots.append(pages_of[pos // page] * page + pos % page)
+    slots = np.concatenate(slots).astype(np.int32)
+    t = len(slots)
+    assert 2 * t * heads * (dim // 16) >= 1 << 18
+    k, v = _rows(rng, t, heads, dim), _rows(rng, t, heads, dim)
+    pages = rng.integers(0, 256, (at, heads, page // 32, 36 * dim)).astype(np.uint8)
+    want = pages.copy()
+    okv.append(want, page, k, slots, 0.0625, False)
+    okv.append(want, page, v, slots, 0.5, True)
+    cache = kv.NvFp4KvCache(torch.from_numpy(pages).to(DEV), page, 0.0625, 0.5)
+    kv.kv_append(cache, kh.to_bf16(k), kh.to_bf16(v), _i32(slots))
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("d", [1.0, 2.0 ** -64, 2.0 ** 64, 3.3e-4, 0.0371, 1.0 / 2688.0])
 def test_append_of_every_largest_magnitude(d):
     """Groups whose largest element runs over every finite bf16 magnitude, the others random below it or
