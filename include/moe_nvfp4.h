@@ -542,7 +542,8 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, c
  * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; R * table_width < 2^31; scale finite and
  * positive, scale * k_gscale within [2^-126, 2^100]; window >= 0; query_offsets ascending; seq_lens <= 2^31 - 4096
  * (a greater one counts as that); out overlaps no input.
- * workspace: moe_nvfp4_kv_attention_workspace_size bytes, 16-byte aligned. */
+ * workspace: moe_nvfp4_kv_attention_workspace_size bytes, 16-byte aligned, are enough for every table; a
+ * narrow one may need less, down to none (NULL).  MOE_ERR_WORKSPACE_TOO_SMALL otherwise. */
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);
 moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q, int64_t q_stride,
                                     int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens,

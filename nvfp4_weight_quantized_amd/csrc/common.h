@@ -320,7 +320,8 @@ struct KvAttentionProblem {
   uint16_t* out;            // [T][Hq][D]
   float* lse;               // [T][Hq] or NULL
 };
-size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);
+size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim,
+                              int64_t table_units);
 moe_status_t launch_kv_attention(const KvAttentionProblem& p, void* workspace, hipStream_t stream);
 
 }  // namespace moe

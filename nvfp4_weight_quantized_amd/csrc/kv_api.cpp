@@ -81,7 +81,7 @@ size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, i
       Hq / kv_heads > 64 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       (int64_t)T * Hq >= ((int64_t)1 << 31))
     return 0;
-  return moe::kv_attention_workspace(T, R, Hq, kv_heads, head_dim);
+  return moe::kv_attention_workspace(T, R, Hq, kv_heads, head_dim, INT64_MAX);      // any table
 }
 
 moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
@@ -100,7 +100,8 @@ moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache, const uin
   if (T == 0 || R == 0) return MOE_OK;
   if (!q || !out || !query_offsets || !seq_lens || !al16(q) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
   if (table_width > 0 && !block_table) return MOE_ERR_INVALID_ARGUMENT;
-  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim);
+  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim,
+                                                  (int64_t)table_width * (cache->page_size / moe::kKvUnit));
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !al16(workspace)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;

@@ -1112,9 +1112,9 @@ Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, 
 
 }  // namespace
 
-size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int32_t D) {
+size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int32_t D, int64_t table_units) {
   if (T == 0 || R == 0) return 0;
-  const Launches x = plan_launches(T, R, Hq / hkv, hkv, D, INT64_MAX);      // any table
+  const Launches x = plan_launches(T, R, Hq / hkv, hkv, D, table_units);
   size_t bytes = 0;
   for (int i = 0; i < x.n; ++i) bytes = std::max(bytes, x.l[i].bytes);
   return bytes;

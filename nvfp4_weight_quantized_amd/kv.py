@@ -38,11 +38,14 @@ def _on(index: int):
 
 def _ints(t: torch.Tensor, name: str, ndim: int, dev: Optional[torch.device] = None) -> torch.device:
     """A contiguous int32 GPU tensor (on ``dev``, when given); its device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.is_cuda and t.dim() == ndim and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.dim() == ndim and t.is_contiguous()):
         _need(t, name, _I32, ndim)
     d = t.device
-    if dev is not None and d != dev:
-        raise ValueError(f"{name}: on {d}, expected {dev}")
+    if d != dev:
+        if dev is not None:
+            raise ValueError(f"{name}: on {d}, expected {dev}")
+        if d.type != "cuda":
+            raise ValueError(f"{name}: must be a GPU tensor")
     return d
 
 
@@ -63,7 +66,7 @@ class NvFp4KvCache:
             raise ValueError(f"pages: last dimension {b}, expected 36 * head_dim with head_dim in {HEAD_DIMS}")
         if page_size % _UNIT or page_size != u * _UNIT:
             raise ValueError(f"pages: {u} units of {_UNIT} positions do not make a page of {page_size}")
-        if L.lib().moe_nvfp4_kv_cache_bytes(p, page_size, h, b // 36) == 0:
+        if not (0 < page_size <= 65536 and 0 < h <= 1024 and 0 < p * page_size < _I32_END):
             raise ValueError(f"pages: sizes {tuple(pages.shape)} outside the cache's limits")
         for name, d in (("k_gscale", k_gscale), ("v_gscale", v_gscale)):
             if not 2.0 ** -64 <= d <= 2.0 ** 64:      # also refuses NaN
@@ -256,24 +259,28 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
     if not 0 <= window < _I32_END:
         raise ValueError(f"window {window}")
     if out is None:
-        out = torch.empty((t, heads, dim), dtype=_BF16, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty((t, heads, dim), dtype=_BF16, device=dev)
     else:
         _need(out, "out", _BF16, 3)
         _shape(out, "out", (t, heads, dim))
         _same_device(cache._pages, ("out", out))
     lse = torch.empty((t, heads), dtype=torch.float32, device=dev) if return_lse else None
     lib = L.lib()
-    if workspace is None:
-        workspace = torch.empty(lib.moe_nvfp4_kv_attention_workspace_size(t, r, heads, kv_heads, dim),
-                                dtype=torch.uint8, device=dev)
-    else:
+    if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
         _same_device(cache._pages, ("workspace", workspace))
     with _on(dev.index):
-        st = lib.moe_nvfp4_kv_attention(
-            c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
-            block_table.data_ptr(), width, scale, window, out.data_ptr(), lse.data_ptr() if return_lse else None,
-            workspace.data_ptr(), workspace.numel(), _raw_stream(dev.index))
+        while True:
+            st = lib.moe_nvfp4_kv_attention(
+                c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
+                block_table.data_ptr(), width, scale, window, out.data_ptr(), lse.data_ptr() if return_lse else None,
+                workspace.data_ptr() if workspace is not None else None,
+                workspace.numel() if workspace is not None else 0, _raw_stream(dev.index))
+            if st != L.MOE_ERR_WORKSPACE_TOO_SMALL or workspace is not None:
+                break
+            # short tables need none; nothing has been enqueued
+            workspace = torch.empty(lib.moe_nvfp4_kv_attention_workspace_size(t, r, heads, kv_heads, dim),
+                                    dtype=torch.uint8, device=dev)
     if st:
         L.check("moe_nvfp4_kv_attention", st)
     return (out, lse) if return_lse else out

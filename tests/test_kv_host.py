@@ -167,10 +167,13 @@ def test_attention_no_ops_and_sizes():
                 (1, 1, 4, 2, 96), (1 << 30, 1, 4, 2, 128)):
         assert size(*bad) == 0
     need = size(3, 2, 4, 2, 128)
-    if need:
-        assert _attend(_cache(), ws_bytes=need - 1) == SMALL
-        assert _attend(_cache(), ws=None) == SMALL
-        assert _attend(_cache(), ws=0x100008) == INV
+    assert need > 0
+    for wide in (dict(width=1000), dict(width=1000, t=400)):      # a narrow table may need none
+        need = size(wide.get("t", 3), 2, 4, 2, 128)
+        assert _attend(_cache(), ws=None, ws_bytes=0, **wide) == SMALL
+        assert _attend(_cache(), ws=None, **wide) == SMALL
+        assert _attend(_cache(), ws=0x100008, **wide) == INV
+    assert _attend(_cache(), ws_bytes=size(3, 2, 4, 2, 128) - 1, width=1000) == SMALL
     cb = L.lib().moe_nvfp4_kv_cache_bytes
     assert cb(10, 64, 8, 128) == 10 * 64 * 8 * 128 * 2 * 9 // 16
     assert cb(0, 64, 8, 128) == cb(10, 40, 8, 128) == cb(10, 64, 0, 128) == cb(10, 64, 8, 80) == 0
