@@ -1023,7 +1023,7 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
 // Host side of one launch: schedule, grid and workspace.
 struct Launch {
   bool shares;        // few-row kernel (equal shares) or tile kernel (items)
-  bool whole;         // few-row kernel, whole tiles: no partial sums, no combine launch
+  bool whole;         // tiles are not cut: no partial sums, no combine launch
   int rs;             // tile kernel: rows per wave
   KvSchedule s;
   int64_t grid;       // workgroups
@@ -1033,12 +1033,26 @@ struct Launch {
 
 constexpr int kCus = 256;              // compute units of the card
 constexpr int kRowsMinChunk = 4;       // units: one per wave
+// Few rows, block tables of at most so many units and at most so many tiles: a workgroup of 8 waves takes a
+// tile whole.  These are bound by latency, and whole tiles save the combine launch and its gap (one request
+// of 1024 positions, 32/4 heads, dimension 128: 10.5 against 11.1 us on the GPU, 14.8 against 17.4 us with the
+// host's part; 16 waves: 12.4 us on the GPU).
+constexpr int kWholeUnits = 64, kWholeTiles = 256;
 constexpr int kTilesTarget = kCus;     // one workgroup is resident per compute unit
 constexpr int kTilesMinChunk = 8;      // units: four steps
+// Many rows, block tables of at most so many steps: tiles are not cut, for the same reason (3 requests of 243 to
+// 337 tokens, 4/2 heads, dimension 64, 17 units: 13.2 against 16.2 us; 2 requests of 921, 8 heads, 29 units:
+// 20.7 against 24.4 us; but 3 of 140 to 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us).
+constexpr int kTilesWholeSteps = 12;
 constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
-constexpr int kWholeUnits = 64;        // block tables of at most so many units, and
-constexpr int kWholeTiles = 256;       // at most so many tiles: one workgroup of 8 waves takes a tile whole
-constexpr int kRowsSplit = 64;         // requests of more rows go to the tile kernel where both run
+// Requests of more rows go to the tile kernel where both run.  32 requests on 4000 positions, 32/8 heads,
+// dimension 128: 64 rows each 83 us, in the tile kernel 144 us; 128 rows each 153 us, in the few-row kernel
+// 137 us, but then 12 short prompts of up to 32 tokens take 15.1 instead of 9.7 us (two more launches).
+constexpr int kRowsSplit = 64;
+// Requests * heads * units of the table up to which the tile kernel takes requests of few rows too, and two
+// launches are saved (5 prompts of 527 to 763 tokens, 2 heads: 24.5 against 28.9 us).  A request of one row and
+// a long context takes several times longer there.
+constexpr int64_t kAloneWork = 2048;
 
 int rows_resident(int D, int bm) {
   if (D == 64) return bm == 16 ? rows_occupancy<64, 1>() : rows_occupancy<64, 2>();
@@ -1058,9 +1072,6 @@ Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, i
   const int64_t tiles = std::min(with_rows + (int64_t)T * G / bm, with_rows * (((int64_t)max_rows + bm - 1) / bm));
   p.tiles = tiles * hkv;
   size_t slots;
-  // Few short contexts are bound by latency: whole tiles save the combine launch and its gap (one request
-  // of 1024 positions, 32/4 heads, dimension 128: 10.5 us against 11.1 us on the GPU, 14.8 against 17.4 us
-  // with the host's part; 16 waves: 12.4 us on the GPU).
   p.whole = shares && bm == 16 && table_units <= kWholeUnits && p.tiles <= kWholeTiles;
   if (p.whole) {
     p.s = KvSchedule{bm, 1, 1, min_rows, max_rows};
@@ -1073,9 +1084,10 @@ Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, i
     p.grid = std::min((int64_t)p.s.target, p.tiles * ((most + kRowsMinChunk - 1) / kRowsMinChunk));
     slots = 2 * (size_t)p.s.target;
   } else {
-    p.s = KvSchedule{bm, std::max(1, kTilesTarget / hkv), kTilesMinChunk, min_rows, max_rows};
-    p.grid = (tiles + p.s.target) * hkv;
-    slots = 2 * (size_t)p.s.target * hkv;
+    p.whole = table_units <= kTilesWholeSteps * (D == 256 ? 1 : 2);
+    p.s = KvSchedule{bm, std::max(1, kTilesTarget / hkv), p.whole ? 1 << 20 : kTilesMinChunk, min_rows, max_rows};
+    p.grid = (tiles + (p.whole ? 0 : p.s.target)) * hkv;
+    slots = p.whole ? 0 : 2 * (size_t)p.s.target * hkv;
   }
   p.o_bytes = slots * bm * D * 4;
   p.bytes = p.o_bytes + slots * 2 * bm * 4;
@@ -1091,8 +1103,10 @@ struct Launches {
 Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int64_t table_units) {
   Launches x{};
   const int64_t rows = (int64_t)T * G;
+  // Requests of more than kRowsSplit rows are certain, or likely: a step of 1024 rows and more that are not all
+  // of single tokens.
   const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
-  const bool few = !tiles || R > 1;
+  const bool few = !tiles || (R > 1 && (int64_t)R * hkv * std::min(table_units, (int64_t)1 << 32) > kAloneWork);
   if (tiles) {
     // 32 rows per wave (256 per tile) at twice the rate, 16 rows (128) with twice the tiles.  Measured, 32/8
     // heads, dimension 128: prompt of 8192 (264k units over all tiles) 572 against 849 us, 512 tokens on
@@ -1142,7 +1156,7 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
         else
           hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, 8, DD == 256 ? 1 : 2, 16>), grid, dim3(512), 0, stream, a,
                              p.s, part);
-        hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
+        if (!p.whole) hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
       } else {
         if (p.whole)
           hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1, 8>), grid, dim3(512), 0, stream, a, p.s, part);

@@ -242,8 +242,9 @@ def test_no_rows_and_no_requests():
     assert (out == 3.0).all()
 
 
-# The host knows the width of the block table only: a narrow one lets few rows be taken tile by tile and
-# many in 16-row waves, a wide one makes the call cut every row's positions into shares and take 32-row waves.
+# The host knows the width of the block table only: a narrow one lets tiles be taken whole, and few rows by the
+# kernel for many; a wider one makes the call cut positions into shares and splits, and a very wide one take
+# 32-row waves.
 WIDE = 40000
 
 
@@ -259,8 +260,9 @@ WIDE = 40000
     (4, [(333, 0), (1, 1800), (65, 1)], 0, 0),       # the first tiles see little: splits of theirs are empty
     (3, [(100, 2000), (96, 0), (0, 50), (2, 31)], 70, 7),
 ])
-def test_wide_block_tables(dim, group, reqs, window, pad):
-    case = kh.Case(dim + group, dim, 2, group, 32, reqs, window=window, pad=pad, width_extra=WIDE)
+@pytest.mark.parametrize("extra", [400, WIDE])
+def test_wide_block_tables(extra, dim, group, reqs, window, pad):
+    case = kh.Case(dim + group, dim, 2, group, 32, reqs, window=window, pad=pad, width_extra=extra)
     kh.check_attention(case, *case.run())
 
 
