@@ -131,12 +131,16 @@ struct KvPartials {
 };
 
 // ------------------------------------------------------------------------- few rows per request
-// Workgroups of NW waves (4; more where whole tiles are taken) with an equal share of the units each
-// (KvShare); of a segment (one kv head and row tile of 16*MI rows) each wave takes every NW-th unit.  A unit's 36*D contiguous bytes go straight
-// to LDS, into a ring of kRing units of the wave's own (no barrier, no registers held for loads in
-// flight), and from there to registers when their turn comes.  The waves' sums meet in LDS at the
-// end of the segment.
-constexpr int kRing = 2;
+// Workgroups of NW waves (4; 8 where whole tiles are taken) with an equal share of the units each (KvShare);
+// of a segment (one kv head and row tile of 16*MI rows) each wave takes every NW-th unit.  A unit's 36*D
+// contiguous bytes go straight to LDS, into a ring of kRing units of the wave's own (no barrier, no registers
+// held for loads in flight), and from there to registers when their turn comes.  The waves' sums meet in LDS
+// at the end of the segment.  MI = 2 where a request may have more than 16 rows per kv head.
+// Bound by memory and the vector unit together: a unit of dimension 128 takes about 300 vector instructions of
+// a wave, 1200 cycles, in which a quarter of a compute unit's share of the memory brings 4.6 KB.  64 requests
+// of 90 to 8100 positions (64/8 heads, 313 MB): 62 us and 7 us for the combine launch, 4.5 TB/s over both; 3
+// contexts of 70 to 131 thousand positions (32/8 heads, 372 MB): 5.0 TB/s; a plain read reaches 7.1 TB/s.
+constexpr int kRing = 2;      // 147 of a compute unit's 160 KB for four workgroups of dimension 128
 
 // Waves per SIMD the kernel is built for (registers, ring), and so its resident workgroups per compute unit.
 template <int D, int MI, int NW = 4>
@@ -505,7 +509,7 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
 //   for head dimension 256, whose 32-row outputs and queries (128 + 64 of 256 registers) leave none to
 //   overlap anything: 249 us against 263 us for the chunks of 5 requests (16/2 heads, window 1024).
 // Bound by the vector unit and LDS beside the matrix unit: a prompt of 8192 (32/8 heads, dimension 128)
-// runs at 955-993 TFLOP/s, the matrix unit 45% busy, 7.6 vector instructions per 32-cycle matrix
+// runs at 963-996 TFLOP/s, the matrix unit 45% busy, 7.6 vector instructions per 32-cycle matrix
 // instruction (32 exponentials, 32 fused multiply-adds, 37 additions, 16 conversions, 16 maxima and the
 // wave's eighth of the dequantization per 32 of them).
 template <int D, int NW, int NU, int RS>
@@ -925,7 +929,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
 // ------------------------------------------------------------------------- combine
 // One wave per row of a cut tile: lane i reads the maximum and sum of partial i, then D / 4 lanes take four
 // elements each, 256 / D partials at a time, added in a fixed order.  Offsets into the partials fit 32 bits:
-// there are at most 2 * 1024 of 16 rows or 2 * 512 of 256.
+// there are at most 2 * 1024 of 16 rows or 2 * 1024 of 256.  Bound by latency (the schedule, the weights, the
+// rows, one after the other): 7 us for 512 tiles of 8 rows with up to 9 partials each.
 template <int D, bool SHARES>
 __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a, KvSchedule s, KvPartials part) {
   const int hkv = a.cache.kv_heads, lane = threadIdx.x & 63;

@@ -15,7 +15,10 @@ __device__ __forceinline__ int sat31(long long v) { return (int)min(v, 0x7FFFFFF
 // Every workgroup forms the two prefix sums over the requests (tokens, pages opened) in LDS and then
 // places its own 1024 tokens; workgroup 0 also writes the per-request outputs.  A page is opened by
 // exactly one token, the one at its first position, so no two workgroups write the same entry, and
-// the entries read (pages held) are never written.
+// the entries read (pages held) are never written.  Bound by latency: two rounds of memory, a scan over 16
+// waves and a search of log2 R steps, 5.7 us for 64 requests, 6.7 us for 512 with 25000 tokens (a launch alone
+// takes about 3 us); one launch, because a second one for the tokens would cost more than the prefix sums
+// that every workgroup repeats.
 __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
     const int32_t* __restrict__ kv_lens, const int32_t* __restrict__ new_lens, int R, int ps, int num_pages,
     const int32_t* __restrict__ free_pages, int num_free, int32_t* block_table, int width, int T,
@@ -120,6 +123,12 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
 // takes every quad that begins among its W rows (a row whose slot is a multiple of 4 or does not follow
 // the row before it), with the rows after it that continue it, also those of the next window.  W = 1
 // stores bytes, row by row: for steps of few rows, where the threads of the quads would not fill the card.
+// Measured with 8 heads of 128 and a gather of the same rows after it: 1024 rows 13.4 (W = 4) against 10.3 us
+// (W = 1), 2048 rows 15.1 against 14.4, 4096 rows 18.6 against 19.8, 8192 rows 26.2 against 31.1 us.
+// Bound by the vector unit: about 320 instructions per group (two fp32 quotients per element step to be
+// exact to the bit), 16.2 us for 8192 rows of 8 heads of 128, whose 43 MB pass in 8.3 us at the rate of a
+// copy.  Putting whole units together in LDS and writing them in order took 20.8 us: the scattered stores
+// are not what it waits for.
 constexpr long long kAppendQuadThreads = 1 << 18;      // rows * groups from which quads are taken
 
 __device__ __forceinline__ void load_group16(const uint16_t* __restrict__ row, float (&x)[16]) {
@@ -216,7 +225,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(moe_nvfp4_kv_cache_t c, 
 // A workgroup takes 32 rows of the list for one head.  Where they lie in at most two units (consecutive
 // positions, whatever their alignment), both units come to LDS whole and in order and every thread
 // assembles 16-byte pieces of the output rows from there; otherwise the pieces are assembled from global
-// memory.
+// memory.  Bound by memory: 32768 rows of 8 heads of 128 (172 MB) in 36.2 us, 4.75 TB/s against the 5.17 TB/s
+// of a copy.
 constexpr int kGatherRows = 32;
 
 template <int D>
