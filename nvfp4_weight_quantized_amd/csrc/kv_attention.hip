@@ -149,14 +149,12 @@ constexpr int rows_occupancy() {
   return D == 256 ? (MI == 2 ? 1 : 2) : D == 128 ? (MI == 2 ? 2 : 4) : (MI == 2 ? 3 : 4);
 }
 
-// Waits until at most n units' loads (PER instructions each) of this wave are in flight.
+// Waits until at most n units' loads (PER instructions each) of this wave are in flight, n < kRing.
 template <int PER>
 __device__ __forceinline__ void wait_units(int n) {
-  static_assert(3 * PER <= 63, "the counter of loads in flight");
-  if (n <= 0) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-  else if (n == 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(PER) : "memory");
-  else if (n == 2) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * PER) : "memory");
-  else asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * PER) : "memory");
+  static_assert(kRing == 2 && PER <= 63, "the counter of loads in flight");
+  if (n == 0) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0)" : : "n"(PER) : "memory");
 }
 
 template <int D, int MI, int NW>

@@ -126,7 +126,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
 // Measured with 8 heads of 128 and a gather of the same rows after it: 1024 rows 13.4 (W = 4) against 10.3 us
 // (W = 1), 2048 rows 15.1 against 14.4, 4096 rows 18.6 against 19.8, 8192 rows 26.2 against 31.1 us.
 // Bound by the vector unit: about 320 instructions per group (two fp32 quotients per element step to be
-// exact to the bit), 16.2 us for 8192 rows of 8 heads of 128, whose 43 MB pass in 8.3 us at the rate of a
+// exact to the bit), 16.0 us for 8192 rows of 8 heads of 128, whose 43 MB pass in 8.3 us at the rate of a
 // copy.  Putting whole units together in LDS and writing them in order took 20.8 us: the scattered stores
 // are not what it waits for.
 constexpr long long kAppendQuadThreads = 1 << 18;      // rows * groups from which quads are taken
@@ -225,9 +225,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(moe_nvfp4_kv_cache_t c, 
 // A workgroup takes 32 rows of the list for one head.  Where they lie in at most two units (consecutive
 // positions, whatever their alignment), both units come to LDS whole and in order and every thread
 // assembles 16-byte pieces of the output rows from there; otherwise the pieces are assembled from global
-// memory.  Bound by memory: 32768 rows of 8 heads of 128 (172 MB) in 36.2 us, 4.75 TB/s against the 5.17 TB/s
-// of a copy.
+// memory.  Bound by memory: 32768 rows of 8 heads of 128 (172 MB) in 33.4 us, 5.16 TB/s, the rate of a copy
+// (with stores that stay in the caches 36.1 us).
 constexpr int kGatherRows = 32;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int D>
 __global__ __launch_bounds__(256) void kv_gather_kernel(moe_nvfp4_kv_cache_t c, const int32_t* __restrict__ slots,
@@ -287,8 +288,8 @@ __global__ __launch_bounds__(256) void kv_gather_kernel(moe_nvfp4_kv_cache_t c, 
 #pragma unroll
       for (int b = 0; b < 4; ++b) w[b] = f32x2_to_bf16x2(e[b][0] * sc * d, e[b][1] * sc * d);
     }
-    *reinterpret_cast<uint4*>((is_v ? v : k) + ((size_t)(t0 + r) * c.kv_heads + h) * D + 8 * g8) =
-        uint4{w[0], w[1], w[2], w[3]};
+    uint16_t* dst = (is_v ? v : k) + ((size_t)(t0 + r) * c.kv_heads + h) * D + 8 * g8;
+    __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4*>(dst));
   }
 }
 
