@@ -236,7 +236,7 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
     ``return_lse``: also the natural log-sum-exp of each row's scores, fp32 [T, heads] (-inf for a row
     that sees nothing, whose output is zero).  Rows outside every request (a padded batch) are left as
     they were in ``out``.  q may be a slice of a fused projection's output.  Without ``workspace`` the
-    call takes one from torch's allocator, so calls on several streams do not share it.
+    call takes one from torch's allocator where it needs one, so calls on several streams do not share it.
     """
     c, dev = cache._struct, cache._dev
     dim, kv_heads = c.head_dim, c.kv_heads
