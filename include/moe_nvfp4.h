@@ -537,6 +537,7 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, c
  * (query_offsets[R] > T, which moe_kv_plan reports) have no row; the others keep their positions.
  * Products are exact (q re-encoded as fp16 under a power of two per row, keys and values as fp16) and
  * sums fp32; the probabilities are rounded to fp16 (11 bits) for the value product only.
+ * Scores are fp32 numbers of magnitude below 2^126: of larger ones a row gets some mean of the values it sees.
  * Deterministic; a row's result depends on the other requests of the call only through the order in
  * which its partial sums are added.
  * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; R * table_width < 2^31; scale finite and

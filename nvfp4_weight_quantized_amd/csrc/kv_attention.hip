@@ -17,6 +17,11 @@
 // powers of two): p_j <= 2^8 relative to it, so the sums stay in range and exact in the same way, and
 // the usual unit needs no exchange between lanes and no rescale.  p carries another factor 2^7, which
 // cancels in out, so that fp16 p reaches down to 2^-31 of the largest.
+//
+// Exponents are fma(s, c, 7 - m), s the raw score of the product, c its factor and m = fl(max s * c): they differ
+// from those relative to the exact maximum by the rounding of m, one number for the whole row, which cancels in
+// out.  It must not reach a power of two, let alone the range of fp16: from |m| = 2^16 on (rounding 2^-8) a row is
+// "far", its m is held as a raw score and its exponents are fma(s - m, c, 7), exactly 7 at the largest score.
 #include <cfloat>
 
 #include "kv_layout.h"
@@ -37,6 +42,7 @@ constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kSlack = 8.f;     // how far a score may exceed the reference maximum
 constexpr float kPExp = 7.f;      // power of two carried by p
 constexpr float kNone = -FLT_MAX; // reference maximum of a row that has seen nothing
+constexpr float kFar = 0x1p16f;   // reference maximum from which it is held as a raw score
 
 // Eight codes (one dword) of one position times their scale.
 __device__ __forceinline__ f16x8 k_operand(uint32_t codes, _Float16 s) {
@@ -118,6 +124,35 @@ __device__ __forceinline__ f16x2 bf16x2_to_f16(uint32_t w, int sh) {
 __device__ __forceinline__ int row_shift(int e, float c0) { return min(141 - e, ilogbf(c0) + 120); }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The reference maximum m of a row moved to the largest of it and of the raw score mx (-inf: none seen); the
+// factor for its sums.  c: the scores' factor.  A row that was far stays so.
+__device__ __forceinline__ float kv_move(float mx, float c, float& m, bool& far) {
+  float f = 1.f;
+  if (!far) {
+    const float top = fmaxf(mx * c, m);
+    if (fabsf(top) < kFar || mx == -INFINITY) {
+      f = exp2_hw(m - top);
+      m = top;
+      return f;
+    }
+    far = true;
+    if (m != kNone) {      // from log2 units to the nearest raw score, the sums corrected by what that rounds
+      const float raw = m / c;
+      f = exp2_hw(__fmaf_rn(-raw, c, m));
+      m = raw;
+    }
+  }
+  const float top = fmaxf(mx, m);
+  f *= exp2_hw((m - top) * c);
+  m = top;
+  return f;
+}
+
+// A far row's reference maximum in log2 units, where those of a row's partial sums are compared.
+__device__ __forceinline__ float kv_reference(float m, float c, bool far) {
+  return far ? fmaxf(fminf(m * c, FLT_MAX), -FLT_MAX) : m;
+}
 
 // Keys of dword `first`.. of a unit that lie before position len: byte mask of four scale bytes.
 __device__ __forceinline__ uint32_t keep_bytes(int first, int len) {
@@ -261,13 +296,15 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
         const f16x2 p2 = bf16x2_to_f16(w[k][2], shift), p3 = bf16x2_to_f16(w[k][3], shift);
         qf[mi][k] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
       }
-      c[mi] = ldexpf(a.scale * kLog2e, -shift);
+      c[mi] = fminf(ldexpf(a.scale * kLog2e, -shift), FLT_MAX);      // a score of 0 stays 0
     }
 
     f32x4 o[MI][NS][2];
     float m[MI], l[MI];
+    bool far[MI], any_far = false;
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
+      far[mi] = false;
       m[mi] = kNone;
       l[mi] = 0.f;
 #pragma unroll
@@ -335,6 +372,11 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
           const float ref = m[mi] - kPExp;
 #pragma unroll
           for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(sc[mi][k >> 2][k & 3], c[mi], -ref);
+          if (__builtin_expect(any_far, 0)) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              t[k] = far[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
+          }
         };
         exponents();
         const float most =
@@ -343,9 +385,8 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
           float mx = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sc[mi][k >> 2][k & 3]);
-          mx = fmaxf(quarter_max(mx) * c[mi], m[mi]);
-          const float f = exp2_hw(m[mi] - mx);
-          m[mi] = mx;
+          const float f = kv_move(quarter_max(mx), c[mi], m[mi], far[mi]);
+          any_far |= __any(far[mi]);
           l[mi] *= f;
 #pragma unroll
           for (int r = 0; r < NS; ++r)
@@ -405,6 +446,7 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const float ls = quarter_sum(l[mi]);
+      m[mi] = kv_reference(m[mi], c[mi], far[mi]);
       if (eq == 0) {
         m_lds[wave][16 * mi + en] = m[mi];
         l_lds[wave][16 * mi + en] = ls;
@@ -587,7 +629,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
       const f16x2 p2 = bf16x2_to_f16(w[t][2], sh), p3 = bf16x2_to_f16(w[t][3], sh);
       qf[t] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
     }
-    c = ldexpf(a.scale * kLog2e, -sh);
+    c = fminf(ldexpf(a.scale * kLog2e, -sh), FLT_MAX);      // a score of 0 stays 0
   }
   const int wrow = row_base + RS * wave;
   reach(min(wrow, rows - 1), wrow + RS, &pos_min, &pos_max, &see_all, &see_any);
@@ -602,6 +644,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
   constexpr int NO = kWide ? NS : 2 * NS, NA = kWide ? 16 : 4;
   Acc o[NO];
   float m = kNone, l = 0.f;
+  bool far = false, any_far = false;
 #pragma unroll
   for (int r = 0; r < NO; ++r)
 #pragma unroll
@@ -763,6 +806,19 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
   auto exponents = [&]() __attribute__((always_inline)) {
     const float ref = m - kPExp;
     float mx = -INFINITY;
+    if (__builtin_expect(any_far, 0)) {
+#pragma unroll
+      for (int b = 0; b < NU; ++b)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int i = 0; i < NA; ++i) {
+            const float x = sacc[b][k][i];
+            sacc[b][k][i] = far ? __fmaf_rn(x - m, c, kPExp) : __fmaf_rn(x, c, -ref);
+            mx = fmaxf(mx, sacc[b][k][i]);
+          }
+      return mx;
+    }
 #pragma unroll
     for (int b = 0; b < NU; ++b)
 #pragma unroll
@@ -785,9 +841,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
       for (int k = 0; k < NK; ++k)
 #pragma unroll
         for (int i = 0; i < NA; ++i) mx = fmaxf(mx, sacc[b][k][i]);
-    mx = fmaxf(row_max(mx) * c, m);
-    const float f = exp2_hw(m - mx);
-    m = mx;
+    const float f = kv_move(row_max(mx), c, m, far);
+    any_far |= __any(far);
     l *= f;
 #pragma unroll
     for (int r = 0; r < NO; ++r)
@@ -893,6 +948,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
   }
 
   l = kWide ? half_sum(l) : quarter_sum(l);
+  m = kv_reference(m, c, far);
   if (!valid) return;
   const size_t at = (size_t)(it.q.row0 + tok) * a.Hq + h * a.G + g;
   // groups of four elements of the lane's row, and where they begin
