@@ -537,7 +537,7 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, c
  * (query_offsets[R] > T, which moe_kv_plan reports) have no row; the others keep their positions.
  * Products are exact (q re-encoded as fp16 under a power of two per row, keys and values as fp16) and
  * sums fp32; the probabilities are rounded to fp16 (11 bits) for the value product only.
- * Scores are fp32 numbers of magnitude below 2^126: of larger ones a row gets some mean of the values it sees.
+ * Scores are fp32 numbers of magnitude below 2^126; a row with larger ones has no specified result.
  * Deterministic; a row's result depends on the other requests of the call only through the order in
  * which its partial sums are added.
  * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; R * table_width < 2^31; scale finite and
@@ -551,6 +551,12 @@ moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache /* host */
                                     int32_t R, const int32_t* block_table, int32_t table_width, float scale,
                                     int32_t window, uint16_t* out, float* lse, void* workspace,
                                     size_t workspace_bytes, void* stream);
+/* The same for out and lse without content yet: rows outside every request get zeros and lse = -inf. */
+moe_status_t moe_nvfp4_kv_attention_fill(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q, int64_t q_stride,
+                                         int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens,
+                                         int32_t R, const int32_t* block_table, int32_t table_width, float scale,
+                                         int32_t window, uint16_t* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- measurement helper
  * Not a step of the layer: reads `bytes` bytes of device memory at `buf` once with a plain

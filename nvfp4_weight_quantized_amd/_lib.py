@@ -116,6 +116,7 @@ SIGNATURES = {
                                      c_void_p, i32, ctypes.c_float, i32, c_void_p, c_void_p, c_void_p, size_t,
                                      c_void_p]),
 }
+SIGNATURES["moe_nvfp4_kv_attention_fill"] = SIGNATURES["moe_nvfp4_kv_attention"]
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 

@@ -319,6 +319,8 @@ struct KvAttentionProblem {
   int32_t window;           // 0: none
   uint16_t* out;            // [T][Hq][D]
   float* lse;               // [T][Hq] or NULL
+  bool fill;                // rows outside every request: zeros and -inf, else left
+  uint32_t work_groups;     // of the launch; the workgroups from here on fill
 };
 size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim,
                               int64_t table_units);

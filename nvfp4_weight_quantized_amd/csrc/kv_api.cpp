@@ -27,6 +27,48 @@ bool valid_cache(const moe_nvfp4_kv_cache_t* c) {
 
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
+moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
+                          int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                          const int32_t* block_table, int32_t table_width, float scale, int32_t window, uint16_t* out,
+                          float* lse, bool fill, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_cache(cache) || T < 0 || R < 0 || R > moe::kKvMaxRequests || table_width < 0)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (Hq < 1 || Hq % cache->kv_heads != 0 || Hq / cache->kv_heads > 64 || (int64_t)T * Hq >= ((int64_t)1 << 31))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((int64_t)R * table_width >= ((int64_t)1 << 31)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(std::isfinite(scale) && scale > 0.f) || window < 0) return MOE_ERR_INVALID_ARGUMENT;
+  const float s = scale * cache->k_gscale;
+  if (!(s >= 0x1p-126f && s <= 0x1p100f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (T > 1 && (q_stride < (int64_t)Hq * cache->head_dim || q_stride % 8 != 0)) return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0 || (R == 0 && !fill)) return MOE_OK;
+  if (!out || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  if (R > 0 && (!q || !query_offsets || !seq_lens || !al16(q))) return MOE_ERR_INVALID_ARGUMENT;
+  if (R > 0 && table_width > 0 && !block_table) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim,
+                                                  (int64_t)table_width * (cache->page_size / moe::kKvUnit));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && !al16(workspace)) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  moe::KvAttentionProblem p{};
+  p.cache = *cache;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.T = T;
+  p.Hq = Hq;
+  p.G = Hq / cache->kv_heads;
+  p.offsets = query_offsets;
+  p.lens = seq_lens;
+  p.R = R;
+  p.table = block_table;
+  p.width = table_width;
+  p.scale = s;
+  p.window = window;
+  p.out = out;
+  p.lse = lse;
+  p.fill = fill;
+  return moe::launch_kv_attention(p, workspace, static_cast<hipStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -88,40 +130,16 @@ moe_status_t moe_nvfp4_kv_attention(const moe_nvfp4_kv_cache_t* cache, const uin
                                     int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
                                     const int32_t* block_table, int32_t table_width, float scale, int32_t window,
                                     uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!valid_cache(cache) || T < 0 || R < 0 || R > moe::kKvMaxRequests || table_width < 0)
-    return MOE_ERR_INVALID_ARGUMENT;
-  if (Hq < 1 || Hq % cache->kv_heads != 0 || Hq / cache->kv_heads > 64 || (int64_t)T * Hq >= ((int64_t)1 << 31))
-    return MOE_ERR_INVALID_ARGUMENT;
-  if ((int64_t)R * table_width >= ((int64_t)1 << 31)) return MOE_ERR_INVALID_ARGUMENT;
-  if (!(std::isfinite(scale) && scale > 0.f) || window < 0) return MOE_ERR_INVALID_ARGUMENT;
-  const float s = scale * cache->k_gscale;
-  if (!(s >= 0x1p-126f && s <= 0x1p100f)) return MOE_ERR_INVALID_ARGUMENT;
-  if (T > 1 && (q_stride < (int64_t)Hq * cache->head_dim || q_stride % 8 != 0)) return MOE_ERR_INVALID_ARGUMENT;
-  if (T == 0 || R == 0) return MOE_OK;
-  if (!q || !out || !query_offsets || !seq_lens || !al16(q) || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
-  if (table_width > 0 && !block_table) return MOE_ERR_INVALID_ARGUMENT;
-  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim,
-                                                  (int64_t)table_width * (cache->page_size / moe::kKvUnit));
-  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (need > 0 && !al16(workspace)) return MOE_ERR_INVALID_ARGUMENT;
-  if (moe_status_t st = check_arch(nullptr)) return st;
-  moe::KvAttentionProblem p{};
-  p.cache = *cache;
-  p.q = q;
-  p.q_stride = q_stride;
-  p.T = T;
-  p.Hq = Hq;
-  p.G = Hq / cache->kv_heads;
-  p.offsets = query_offsets;
-  p.lens = seq_lens;
-  p.R = R;
-  p.table = block_table;
-  p.width = table_width;
-  p.scale = s;
-  p.window = window;
-  p.out = out;
-  p.lse = lse;
-  return moe::launch_kv_attention(p, workspace, static_cast<hipStream_t>(stream));
+  return kv_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, scale, window, out,
+                      lse, false, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_nvfp4_kv_attention_fill(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
+                                         int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                                         const int32_t* block_table, int32_t table_width, float scale, int32_t window,
+                                         uint16_t* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return kv_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, scale, window, out,
+                      lse, true, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -160,6 +160,29 @@ __device__ __forceinline__ uint32_t keep_bytes(int first, int len) {
   return v >= 4 ? 0xFFFFFFFFu : v <= 0 ? 0u : (1u << (8 * v)) - 1u;
 }
 
+// Zeros (lse: -inf) for the rows of no request, [0, offsets[0]) and [offsets[R], T): workgroup `index` of `count`.
+// Workgroups of their own behind those of the launch, so the others neither wait for the offsets nor carry the stores.
+// Inlined: a call gives the tile kernel a stack and spills (prompt of 8192 564 -> 632 us).
+constexpr int64_t kFillGroups = 32;
+template <int D>
+__device__ __forceinline__ void kv_fill_rows(const KvAttentionProblem& a, int index, int count) {
+  const int before = a.R > 0 ? min(max(a.offsets[0], 0), a.T) : a.T;
+  const int after = a.R > 0 ? min(max(a.offsets[a.R], before), a.T) : a.T;
+  for (int i = index; i < before + a.T - after; i += count) {
+    const size_t row = (size_t)(i < before ? i : i - before + after) * a.Hq;
+    u32x4* out = reinterpret_cast<u32x4*>(a.out + row * D);
+    for (int j = threadIdx.x; j < a.Hq * (D / 8); j += blockDim.x) out[j] = u32x4{0, 0, 0, 0};
+    if (a.lse)
+      for (int j = threadIdx.x; j < a.Hq; j += blockDim.x) a.lse[row + j] = -INFINITY;
+  }
+}
+
+// For a step without requests.
+template <int D>
+__global__ __launch_bounds__(256) void kv_fill_kernel(KvAttentionProblem a) {
+  kv_fill_rows<D>(a, blockIdx.x, gridDim.x);
+}
+
 struct KvPartials {
   float* o;    // [slot][BM][D], unnormalised
   float* ml;   // [slot][2][BM]: reference maximum, sum
@@ -202,6 +225,7 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
   // the waves' rings; at the end of a segment one 32-element range of the sums (rows padded to 36 floats)
   __shared__ __align__(16) uint8_t lds[kOut > kRings ? kOut : kRings];
   __shared__ float m_lds[NW][BM], l_lds[NW][BM];
+  if (blockIdx.x >= a.work_groups) return kv_fill_rows<D>(a, blockIdx.x - a.work_groups, gridDim.x - a.work_groups);
   using lds_bytes = __attribute__((address_space(3))) uint8_t*;
   float(*o_lds)[BM][36] = reinterpret_cast<float(*)[BM][36]>(lds);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -563,6 +587,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
   constexpr int kHalf = 2 * D * NU;                   // 8-byte code pieces of the keys (and of the values) of a step
   constexpr int kKeys = 64 * D * NU;                  // bytes of the keys' (and of the values') operands
   __shared__ __align__(16) uint8_t key_lds0[kKeys], key_lds1[kKeys], value_lds0[kKeys], value_lds1[kKeys];
+  if (blockIdx.x >= a.work_groups) return kv_fill_rows<D>(a, blockIdx.x - a.work_groups, gridDim.x - a.work_groups);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int z = lane / RS, nrow = lane & (RS - 1);     // part of the contraction, row
   const int hkv = a.cache.kv_heads;
@@ -1193,11 +1218,20 @@ size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int
   return bytes;
 }
 
-moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, hipStream_t stream) {
+moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* workspace, hipStream_t stream) {
+  KvAttentionProblem a = problem;
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
+  const int64_t fill = a.fill ? std::min((int64_t)a.T, kFillGroups) : 0;
+  if (a.T == 0 || (a.R == 0 && !a.fill)) return MOE_OK;
+  if (a.R == 0) {
+    with_head_dim(D, [&](auto tag) {
+      hipLaunchKernelGGL(kv_fill_kernel<decltype(tag)::value>, dim3((unsigned)fill), dim3(256), 0, stream, a);
+    });
+    return launch_status();
+  }
   const Launches x = plan_launches(a.T, a.R, a.G, hkv, D, (int64_t)a.width * (a.cache.page_size / kKvUnit));
   for (int i = 0; i < x.n; ++i)
-    if (x.l[i].grid > 0x7FFFFFFFLL || x.l[i].tiles > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
+    if (x.l[i].grid + fill > 0x7FFFFFFFLL || x.l[i].tiles > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < x.n; ++i) {
     const Launch& p = x.l[i];
     KvPartials part{static_cast<float*>(workspace), nullptr};
@@ -1207,7 +1241,8 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& a, void* workspace, h
       // few tiles: a wave per two rows, many: per eight, as most are found whole (5 prompts of 527 to 763
       // tokens, 2 heads: 28.8 against 35.8 us; a prompt of 2000, 32 heads: 73 against 70 us with twice as many)
       const int64_t most = p.s.bm / 8, per_tile = std::max(std::min(most, (int64_t)4), std::min(most, 2048 / p.tiles));
-      const dim3 grid((unsigned)p.grid), rows((unsigned)p.tiles, (unsigned)per_tile);
+      a.work_groups = (uint32_t)p.grid;
+      const dim3 grid((unsigned)(p.grid + (i == 0 ? fill : 0))), rows((unsigned)p.tiles, (unsigned)per_tile);
       if (!p.shares) {
         if (DD != 256 && p.rs == 32)
           hipLaunchKernelGGL((kv_attention_tiles_kernel<DD == 256 ? 128 : DD, 8, 2, 32>), grid, dim3(512), 0, stream, a,

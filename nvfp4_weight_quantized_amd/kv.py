@@ -235,8 +235,9 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
     own, with ``window`` > 0 only the last ``window`` of them.  ``scale`` defaults to head_dim^-0.5.
     ``return_lse``: also the natural log-sum-exp of each row's scores, fp32 [T, heads] (-inf for a row
     that sees nothing, whose output is zero).  Rows outside every request (a padded batch) are left as
-    they were in ``out``.  q may be a slice of a fused projection's output.  Without ``workspace`` the
-    call takes one from torch's allocator where it needs one, so calls on several streams do not share it.
+    they were in a given ``out`` and zeros without it; their ``lse`` is -inf.  q may be a slice of a fused
+    projection's output.  Without ``workspace`` the call takes one from torch's allocator where it needs
+    one, so calls on several streams do not share it.
     """
     c, dev = cache._struct, cache._dev
     dim, kv_heads = c.head_dim, c.kv_heads
@@ -258,20 +259,25 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
         raise ValueError(f"scale must be finite and positive, got {scale!r}")
     if not 0 <= window < _I32_END:
         raise ValueError(f"window {window}")
+    lib, lse = L.lib(), None
     if out is None:
+        attend = lib.moe_nvfp4_kv_attention_fill
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty((t, heads, dim), dtype=_BF16, device=dev)
+        if return_lse:
+            lse = torch.empty((t, heads), dtype=torch.float32, device=dev)
     else:
+        attend = lib.moe_nvfp4_kv_attention
         _need(out, "out", _BF16, 3)
         _shape(out, "out", (t, heads, dim))
         _same_device(cache._pages, ("out", out))
-    lse = torch.empty((t, heads), dtype=torch.float32, device=dev) if return_lse else None
-    lib = L.lib()
+        if return_lse:
+            lse = torch.full((t, heads), -math.inf, dtype=torch.float32, device=dev)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
         _same_device(cache._pages, ("workspace", workspace))
     with _on(dev.index):
         while True:
-            st = lib.moe_nvfp4_kv_attention(
+            st = attend(
                 c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
                 block_table.data_ptr(), width, scale, window, out.data_ptr(), lse.data_ptr() if return_lse else None,
                 workspace.data_ptr() if workspace is not None else None,

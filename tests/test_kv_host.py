@@ -158,6 +158,18 @@ def test_attention_refusals(bad):
     assert _attend(_cache(), **bad) == INV
 
 
+@pytest.mark.parametrize("bad", [dict(q=None), dict(q=0x2008), dict(stride=511), dict(t=-1), dict(heads=3), dict(off=None),
+                                 dict(lens=None), dict(r=4097), dict(table=None), dict(scale=0.0), dict(window=-1),
+                                 dict(out=None), dict(out=0x4008), dict(out=None, r=0), dict(out=0x4008, r=0),
+                                 dict(ws=0x100008, width=1000)])
+def test_attention_fill_refusals(bad, monkeypatch):
+    """The entry that also fills the rows of no request refuses what the other one does, and without requests
+    (where every row is filled) outputs that cannot be written."""
+    monkeypatch.setattr(L.lib(), "moe_nvfp4_kv_attention", L.lib().moe_nvfp4_kv_attention_fill)
+    assert _attend(_cache(), **bad) == INV
+    assert _attend(_cache(), t=0) == L.MOE_OK
+
+
 def test_attention_no_ops_and_sizes():
     assert _attend(None) == INV
     assert _attend(_cache(), t=0) == L.MOE_OK
