@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "../../include/moe_nvfp4.h"
+#include "kv_limits.h"
 
 namespace moe {
 
@@ -293,9 +294,6 @@ moe_status_t launch_quantize_act_nv(const uint16_t* a, int64_t rows, int32_t col
                                     uint8_t* scales, uint16_t* values, hipStream_t stream);
 
 // Paged NVFP4 key/value cache ------------------------------------------------------------------
-constexpr int kKvMaxRequests = 4096;
-constexpr int kKvUnit = 32;   // positions per unit of a page (36 * head_dim bytes)
-
 moe_status_t launch_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int32_t R, int32_t page_size,
                             int32_t num_pages, const int32_t* free_pages, int32_t num_free, int32_t* block_table,
                             int32_t table_width, int32_t num_tokens, int32_t* query_offsets, int32_t* seq_lens,

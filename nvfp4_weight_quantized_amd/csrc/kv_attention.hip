@@ -24,6 +24,7 @@
 // "far", its m is held as a raw score and its exponents are fma(s - m, c, 7), exactly 7 at the largest score.
 #include <cfloat>
 
+#include "kv_launch.h"
 #include "kv_layout.h"
 #include "kv_schedule.h"
 
@@ -199,13 +200,6 @@ struct KvPartials {
 // of 90 to 8100 positions (64/8 heads, 313 MB): 62 us and 7 us for the combine launch, 4.5 TB/s over both; 3
 // contexts of 70 to 131 thousand positions (32/8 heads, 372 MB): 5.0 TB/s; a plain read reaches 7.1 TB/s.
 constexpr int kRing = 2;      // 147 of a compute unit's 160 KB for four workgroups of dimension 128
-
-// Waves per SIMD the kernel is built for (registers, ring), and so its resident workgroups per compute unit.
-template <int D, int MI, int NW = 4>
-constexpr int rows_occupancy() {
-  if (NW > 4) return NW / 4;      // one workgroup
-  return D == 256 ? (MI == 2 ? 1 : 2) : D == 128 ? (MI == 2 ? 2 : 4) : (MI == 2 ? 3 : 4);
-}
 
 // Waits until at most n units' loads (PER instructions each) of this wave are in flight, n < kRing.
 template <int PER>
@@ -1102,110 +1096,6 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
           u32x2{f32x2_to_bf16x2(v[0] * norm, v[1] * norm), f32x2_to_bf16x2(v[2] * norm, v[3] * norm)};
     if (a.lse && lane == 0) a.lse[dst] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
   }
-}
-
-// Host side of one launch: schedule, grid and workspace.
-struct Launch {
-  bool shares;        // few-row kernel (equal shares) or tile kernel (items)
-  bool whole;         // tiles are not cut: no partial sums, no combine launch
-  int rs;             // tile kernel: rows per wave
-  KvSchedule s;
-  int64_t grid;       // workgroups
-  int64_t tiles;      // bound on the row tiles over all heads
-  size_t o_bytes, bytes;
-};
-
-constexpr int kCus = 256;              // compute units of the card
-constexpr int kRowsMinChunk = 4;       // units: one per wave
-// Few rows, block tables of at most so many units and at most so many tiles: a workgroup of 8 waves takes a
-// tile whole.  These are bound by latency, and whole tiles save the combine launch and its gap (one request
-// of 1024 positions, 32/4 heads, dimension 128: 10.5 against 11.1 us on the GPU, 14.8 against 17.4 us with the
-// host's part; 16 waves: 12.4 us on the GPU).
-constexpr int kWholeUnits = 64, kWholeTiles = 256;
-constexpr int kTilesTarget = kCus;     // one workgroup is resident per compute unit
-constexpr int kTilesMinChunk = 8;      // units: four steps
-// Many rows, block tables of at most so many steps: tiles are not cut, for the same reason (3 requests of 243 to
-// 337 tokens, 4/2 heads, dimension 64, 17 units: 13.2 against 16.2 us; 2 requests of 921, 8 heads, 29 units:
-// 20.7 against 24.4 us; but 3 of 140 to 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us).
-constexpr int kTilesWholeSteps = 12;
-constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
-// Requests of more rows go to the tile kernel where both run.  32 requests on 4000 positions, 32/8 heads,
-// dimension 128: 64 rows each 83 us, in the tile kernel 144 us; 128 rows each 153 us, in the few-row kernel
-// 137 us, but then 12 short prompts of up to 32 tokens take 15.1 instead of 9.7 us (two more launches).
-constexpr int kRowsSplit = 64;
-// Requests * heads * units of the table up to which the tile kernel takes requests of few rows too, and two
-// launches are saved (5 prompts of 527 to 763 tokens, 2 heads: 24.5 against 28.9 us).  A request of one row and
-// a long context takes several times longer there.
-constexpr int64_t kAloneWork = 2048;
-
-int rows_resident(int D, int bm) {
-  if (D == 64) return bm == 16 ? rows_occupancy<64, 1>() : rows_occupancy<64, 2>();
-  if (D == 128) return bm == 16 ? rows_occupancy<128, 1>() : rows_occupancy<128, 2>();
-  return bm == 16 ? rows_occupancy<256, 1>() : rows_occupancy<256, 2>();
-}
-
-// Requests with min_rows < rows <= max_rows in tiles of bm rows.  Few rows: as many shares as workgroups
-// are resident at once.  Many rows: with chunk >= sum(tiles * units) / target the items are
-// sum tiles * ceil(units / chunk) <= tiles + target per kv head; those of requests with two splits or
-// more number at most twice target.
-Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, int32_t R, int32_t G, int32_t hkv,
-                   int32_t D, int64_t table_units) {
-  Launch p{};
-  p.shares = shares;
-  const int64_t with_rows = std::min((int64_t)R, (int64_t)T);
-  const int64_t tiles = std::min(with_rows + (int64_t)T * G / bm, with_rows * (((int64_t)max_rows + bm - 1) / bm));
-  p.tiles = tiles * hkv;
-  size_t slots;
-  p.whole = shares && bm == 16 && table_units <= kWholeUnits && p.tiles <= kWholeTiles;
-  if (p.whole) {
-    p.s = KvSchedule{bm, 1, 1, min_rows, max_rows};
-    p.grid = p.tiles;
-    slots = 0;
-  } else if (shares) {
-    p.s = KvSchedule{bm, kCus * rows_resident(D, bm), kRowsMinChunk, min_rows, max_rows};
-    // no more than the shares of least length that the table's units make (kv_request)
-    const int64_t most = std::min(table_units, (int64_t)1 << 32) + (bm + kKvUnit) / kKvUnit + 2 + kSwitch;
-    p.grid = std::min((int64_t)p.s.target, p.tiles * ((most + kRowsMinChunk - 1) / kRowsMinChunk));
-    slots = 2 * (size_t)p.s.target;
-  } else {
-    p.whole = table_units <= kTilesWholeSteps * (D == 256 ? 1 : 2);
-    p.s = KvSchedule{bm, std::max(1, kTilesTarget / hkv), p.whole ? 1 << 20 : kTilesMinChunk, min_rows, max_rows};
-    p.grid = (tiles + (p.whole ? 0 : p.s.target)) * hkv;
-    slots = p.whole ? 0 : 2 * (size_t)p.s.target * hkv;
-  }
-  p.o_bytes = slots * bm * D * 4;
-  p.bytes = p.o_bytes + slots * 2 * bm * 4;
-  return p;
-}
-
-// The launches of a call: the few-row kernel, the tile kernel, or both, each on its requests.
-struct Launches {
-  int n;
-  Launch l[2];
-};
-
-Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int64_t table_units) {
-  Launches x{};
-  const int64_t rows = (int64_t)T * G;
-  // Requests of more than kRowsSplit rows are certain, or likely: a step of 1024 rows and more that are not all
-  // of single tokens.
-  const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
-  const bool few = !tiles || (R > 1 && (int64_t)R * hkv * std::min(table_units, (int64_t)1 << 32) > kAloneWork);
-  if (tiles) {
-    // 32 rows per wave (256 per tile) at twice the rate, 16 rows (128) with twice the tiles.  Measured, 32/8
-    // heads, dimension 128: prompt of 8192 (264k units over all tiles) 572 against 849 us, 512 tokens on
-    // 20000 positions (46k) 211 against 275 us, prompt of 2000 (17k) 105 against 75 us.  The host knows the
-    // table's width, not the lengths; a wide table only means the slower of the two for a short step.
-    const int64_t wide = std::min((int64_t)R, (int64_t)T) + rows / 256;
-    const int rs = D != 256 && wide * hkv * std::min(table_units, (int64_t)1 << 26) >= kWideWork ? 32 : 16;
-    x.l[x.n] = plan_launch(false, 8 * rs, few ? kRowsSplit : 0, 0x7FFFFFFF, T, R, G, hkv, D, table_units);
-    x.l[x.n++].rs = rs;
-  }
-  if (few) {
-    const int bm = tiles || rows > 16 * (int64_t)R ? 32 : 16;
-    x.l[x.n++] = plan_launch(true, bm, 0, tiles ? kRowsSplit : 0x7FFFFFFF, T, R, G, hkv, D, table_units);
-  }
-  return x;
 }
 
 }  // namespace

@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "device_util.h"
+#include "kv_launch.h"
 
 namespace moe {
 namespace {
@@ -39,13 +40,6 @@ struct KvItem {
   int splits;
   int chunk;    // units per split
   int slot;     // partial slot of this tile's split 0
-};
-
-struct KvSchedule {
-  int bm;          // rows per tile
-  int target;      // items aimed at, per kv head
-  int min_chunk;   // units
-  int min_rows, max_rows;   // requests of this launch: min_rows < rows <= max_rows
 };
 
 __device__ __forceinline__ KvRequest kv_request(const KvAttentionProblem& a, const KvSchedule& s, int r) {
@@ -119,7 +113,6 @@ struct KvWhere {
   KvRequest q;
   long long base;    // order position of the request's first unit
 };
-constexpr int kSwitch = 8;
 // units of a tile, its length in the order, and a request's per kv head
 __device__ __forceinline__ long long kv_step(const KvRequest& q, const KvShare& sh) {
   const int units = max(1, q.units);
