@@ -163,8 +163,8 @@ __device__ __forceinline__ uint32_t keep_bytes(int first, int len) {
 
 // Zeros (lse: -inf) for the rows of no request, [0, offsets[0]) and [offsets[R], T): workgroup `index` of `count`.
 // Workgroups of their own behind those of the launch, so the others neither wait for the offsets nor carry the stores.
-// Inlined: a call gives the tile kernel a stack and spills (prompt of 8192 564 -> 632 us).
-constexpr int64_t kFillGroups = 32;
+// One per four rows, up to the card's compute units (1100 padded rows of 32 heads of 128, 9 MB: 32 workgroups take 7 us
+// longer).  Inlined: a call gives the tile kernel a stack and spills (prompt of 8192 564 -> 632 us).
 template <int D>
 __device__ __forceinline__ void kv_fill_rows(const KvAttentionProblem& a, int index, int count) {
   const int before = a.R > 0 ? min(max(a.offsets[0], 0), a.T) : a.T;
@@ -1111,7 +1111,7 @@ size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int
 moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* workspace, hipStream_t stream) {
   KvAttentionProblem a = problem;
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
-  const int64_t fill = a.fill ? std::min((int64_t)a.T, kFillGroups) : 0;
+  const int64_t fill = a.fill ? std::min(((int64_t)a.T + 3) / 4, (int64_t)kCus) : 0;
   if (a.T == 0 || (a.R == 0 && !a.fill)) return MOE_OK;
   if (a.R == 0) {
     with_head_dim(D, [&](auto tag) {
