@@ -1000,28 +1000,37 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttent
 }
 
 // ------------------------------------------------------------------------- combine
+// Workgroup x joins, of shares, the tile x or the tile that share x leaves cut (one at most; it is another share's if it
+// began before x), whichever are fewer, of items the x-th cut tile of its head: the launch is of the size of what can be
+// cut, not of the step.  4096 requests of 40 positions, 32/8 heads, dimension 128: 443 us with the attention; a
+// workgroup for each of their tiles, to find nearly all whole after a search of all lengths, 4140 us.  (64 of 40
+// positions: 13.2 us by tiles, 14.6 us by shares.)
 // One wave per row of a cut tile: lane i reads the maximum and sum of partial i, then D / 4 lanes take four
 // elements each, 256 / D partials at a time, added in a fixed order.  Offsets into the partials fit 32 bits:
 // there are at most 2 * 1024 of 16 rows or 2 * 1024 of 256.  Bound by latency (the schedule, the weights, the
 // rows, one after the other): 7 us for 512 tiles of 8 rows with up to 9 partials each.
-template <int D, bool SHARES>
+enum KvJoin { kItems, kTiles, kShares };
+template <int D, KvJoin BY>
 __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a, KvSchedule s, KvPartials part) {
   const int hkv = a.cache.kv_heads, lane = threadIdx.x & 63;
   KvRequest q;
   int h, tile, count;
   uint32_t first, step, odd;      // slots: first, then first + step*i - odd
-  if (SHARES) {
+  if (BY != kItems) {
     KvShare sh;
     KvWhere at;
     long long within;
-    if (!kv_locate<true>(a, s, blockIdx.x, &sh, &at, &within)) return;
+    if (!kv_locate<BY == kTiles>(a, s, blockIdx.x + (BY == kShares ? 1 : 0), &sh, &at, &within)) return;
     q = at.q;
-    h = (int)within / q.tiles;
-    tile = (int)within - h * q.tiles;
-    const int units = max(1, q.units);
-    const long long begin = at.base + within * kv_step(q, sh) + (sh.aligned ? 0 : kSwitch), i0 = div_i64(begin, sh.chunk),
-                    i1 = div_i64(begin + units - 1, sh.chunk);
-    if (i0 == i1) return;
+    // shares: the tile that holds the next share's first place.  Places of its first unit and its last.
+    const long long step_length = kv_step(q, sh), nth = BY == kTiles ? within : div_i64(within, step_length);
+    const long long start = BY == kTiles ? at.base + nth * step_length
+                                         : (blockIdx.x + 1ll) * sh.chunk - (within - nth * step_length);
+    const long long begin = start + (sh.aligned ? 0 : kSwitch);
+    const long long i0 = div_i64(begin, sh.chunk), i1 = div_i64(begin + max(1, q.units) - 1, sh.chunk);
+    if (i0 == i1 || (BY == kShares && i0 != blockIdx.x)) return;
+    h = (int)div_i64(nth, q.tiles);
+    tile = (int)(nth - (long long)h * q.tiles);
     count = (int)(i1 - i0) + 1;
     first = 2 * (uint32_t)i0 + 1;     // the share it begins in ends with it; the later ones begin with it
     step = 2;
@@ -1029,7 +1038,6 @@ __global__ __launch_bounds__(256, 5) void kv_combine_kernel(KvAttentionProblem a
   } else {
     KvItem it;
     if (!kv_find<true>(a, s, blockIdx.x / hkv, &it)) return;
-    if (it.splits == 1) return;
     q = it.q;
     h = blockIdx.x % hkv;
     tile = it.tile;
@@ -1130,9 +1138,10 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* worksp
       constexpr int DD = decltype(tag)::value;
       // few tiles: a wave per two rows, many: per eight, as most are found whole (5 prompts of 527 to 763
       // tokens, 2 heads: 28.8 against 35.8 us; a prompt of 2000, 32 heads: 73 against 70 us with twice as many)
-      const int64_t most = p.s.bm / 8, per_tile = std::max(std::min(most, (int64_t)4), std::min(most, 2048 / p.tiles));
+      const int64_t most = p.s.bm / 8, join = std::max(p.join, (int64_t)1);
+      const int64_t per_tile = std::max(std::min(most, (int64_t)4), std::min(most, 2048 / join));
       a.work_groups = (uint32_t)p.grid;
-      const dim3 grid((unsigned)(p.grid + (i == 0 ? fill : 0))), rows((unsigned)p.tiles, (unsigned)per_tile);
+      const dim3 grid((unsigned)(p.grid + (i == 0 ? fill : 0))), rows((unsigned)join, (unsigned)per_tile);
       if (!p.shares) {
         if (DD != 256 && p.rs == 32)
           hipLaunchKernelGGL((kv_attention_tiles_kernel<DD == 256 ? 128 : DD, 8, 2, 32>), grid, dim3(512), 0, stream, a,
@@ -1140,7 +1149,7 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* worksp
         else
           hipLaunchKernelGGL((kv_attention_tiles_kernel<DD, 8, DD == 256 ? 1 : 2, 16>), grid, dim3(512), 0, stream, a,
                              p.s, part);
-        if (!p.whole) hipLaunchKernelGGL((kv_combine_kernel<DD, false>), rows, dim3(256), 0, stream, a, p.s, part);
+        if (p.join > 0) hipLaunchKernelGGL((kv_combine_kernel<DD, kItems>), rows, dim3(256), 0, stream, a, p.s, part);
       } else {
         if (p.whole)
           hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1, 8>), grid, dim3(512), 0, stream, a, p.s, part);
@@ -1148,7 +1157,10 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* worksp
           hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 1, 4>), grid, dim3(256), 0, stream, a, p.s, part);
         else
           hipLaunchKernelGGL((kv_attention_rows_kernel<DD, 2, 4>), grid, dim3(256), 0, stream, a, p.s, part);
-        if (!p.whole) hipLaunchKernelGGL((kv_combine_kernel<DD, true>), rows, dim3(256), 0, stream, a, p.s, part);
+        if (p.join > 0 && p.join == p.tiles)
+          hipLaunchKernelGGL((kv_combine_kernel<DD, kTiles>), rows, dim3(256), 0, stream, a, p.s, part);
+        else if (p.join > 0)
+          hipLaunchKernelGGL((kv_combine_kernel<DD, kShares>), rows, dim3(256), 0, stream, a, p.s, part);
       }
     });
     if (moe_status_t st = launch_status()) return st;

@@ -34,6 +34,8 @@ struct Launch {
   KvSchedule s;
   int64_t grid;       // workgroups
   int64_t tiles;      // bound on the row tiles over all heads
+  int64_t join;       // tiles to join: of shares, all (== tiles) or those cut at the end of each but the last; of items,
+                      // the cut ones over all heads
   size_t o_bytes, bytes;
 };
 
@@ -77,7 +79,7 @@ int64_t requests_of(int min_rows, int32_t T, int32_t R, int32_t G) {
 // Requests with min_rows < rows <= max_rows in tiles of bm rows.  Few rows: as many shares as workgroups
 // are resident at once.  Many rows: with chunk >= sum(tiles * units) / target the items are
 // sum tiles * ceil(units / chunk) <= tiles + target per kv head; those of requests with two splits or
-// more number at most twice target.
+// more number at most twice target, and so their tiles at most target.
 Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, int32_t R, int32_t G, int32_t hkv,
                    int32_t D, int64_t table_units) {
   Launch p{};
@@ -96,11 +98,13 @@ Launch plan_launch(bool shares, int bm, int min_rows, int max_rows, int32_t T, i
     // no more than the shares of least length that the table's units make (kv_request)
     const int64_t most = std::min(table_units, (int64_t)1 << 32) + (bm + kKvUnit) / kKvUnit + 2 + kSwitch;
     p.grid = std::min((int64_t)p.s.target, p.tiles * ((most + kRowsMinChunk - 1) / kRowsMinChunk));
+    p.join = std::min(p.tiles, p.grid - 1);
     slots = 2 * (size_t)p.s.target;
   } else {
     p.whole = table_units <= kTilesWholeSteps * (D == 256 ? 1 : 2);
     p.s = KvSchedule{bm, std::max(1, kTilesTarget / hkv), p.whole ? 1 << 20 : kTilesMinChunk, min_rows, max_rows};
     p.grid = (tiles + (p.whole ? 0 : p.s.target)) * hkv;
+    p.join = p.whole ? 0 : std::min(tiles, (int64_t)p.s.target) * hkv;      // a cut tile has two items or more
     slots = p.whole ? 0 : 2 * (size_t)p.s.target * hkv;
   }
   p.o_bytes = slots * bm * D * 4;

@@ -215,7 +215,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionProblem& a, const KvS
 }
 
 // kv_find in integers of type I, which hold the whole work; `q` is lane r's request when R <= 64.
-template <bool BY_TILE, typename I>
+template <bool CUT_TILE, typename I>
 __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const KvSchedule& s, int index, KvRequest q,
                                            I work, KvItem* out) {
   const int lane = threadIdx.x & 63;
@@ -228,7 +228,7 @@ __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const Kv
       if (r0 + lane < a.R) q = kv_request(a, s, r0 + lane);
     }
     const int splits = (int)((uint32_t)(max(0, q.units - 1 - chunk / 4)) / (uint32_t)chunk) + 1;
-    const int items = q.tiles * splits, count = BY_TILE ? q.tiles : items;
+    const int items = q.tiles * splits, count = CUT_TILE ? (splits > 1 ? q.tiles : 0) : items;
     const int part = splits > 1 ? items : 0;
     const int ic = wave_scan(count), ip = wave_scan(part);
     const int excl = base + ic - count;
@@ -240,8 +240,8 @@ __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const Kv
       out->q = lane_request(q, src);
       out->splits = lane_value(splits, src);
       out->chunk = (int)((uint32_t)(out->q.units + out->splits - 1) / (uint32_t)out->splits);
-      out->tile = BY_TILE ? within : within / out->splits;
-      out->split = BY_TILE ? 0 : within % out->splits;
+      out->tile = CUT_TILE ? within : within / out->splits;
+      out->split = CUT_TILE ? 0 : within % out->splits;
       out->slot = slots + lane_value(ip - part, src) + out->tile * out->splits;
       return true;
     }
@@ -251,8 +251,9 @@ __device__ __forceinline__ bool kv_find_in(const KvAttentionProblem& a, const Kv
   return false;
 }
 
-// Item `index` (BY_TILE: all splits of tile `index`); false past the last.  One whole wave.
-template <bool BY_TILE>
+// Item `index` (CUT_TILE: all splits of the tile `index`, counted over those of two splits or more); false past the
+// last.  One whole wave.
+template <bool CUT_TILE>
 __device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSchedule& s, int index, KvItem* out) {
   const int lane = threadIdx.x & 63;
   KvRequest q{};
@@ -263,8 +264,8 @@ __device__ __forceinline__ bool kv_find(const KvAttentionProblem& a, const KvSch
     work += (long long)q.tiles * q.units;
   }
   if (a.R <= 64 && !__any(work >= (1 << 24)))
-    return kv_find_in<BY_TILE, int>(a, s, index, q, lane_value(wave_scan((int)work), 63), out);
-  return kv_find_in<BY_TILE, long long>(a, s, index, q, wave_sum_i64(work), out);
+    return kv_find_in<CUT_TILE, int>(a, s, index, q, lane_value(wave_scan((int)work), 63), out);
+  return kv_find_in<CUT_TILE, long long>(a, s, index, q, wave_sum_i64(work), out);
 }
 
 }  // namespace

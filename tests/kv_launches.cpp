@@ -10,9 +10,9 @@ int main() {
     for (int i = 0; i < x.n; ++i) {
       const moe::Launch& p = x.l[i];
       std::printf("{\"shares\": %d, \"whole\": %d, \"rs\": %d, \"bm\": %d, \"target\": %d, \"min_rows\": %d, \"max_rows\": %d, "
-                  "\"grid\": %lld, \"tiles\": %lld, \"bytes\": %zu}%s",
+                  "\"grid\": %lld, \"tiles\": %lld, \"join\": %lld, \"bytes\": %zu}%s",
                   p.shares, p.whole, p.rs, p.s.bm, p.s.target, p.s.min_rows, p.s.max_rows, (long long)p.grid,
-                  (long long)p.tiles, p.bytes, i + 1 < x.n ? ", " : "");
+                  (long long)p.tiles, (long long)p.join, p.bytes, i + 1 < x.n ? ", " : "");
     }
     std::printf("\n");
   }

@@ -82,3 +82,20 @@ def test_launches_are_of_the_steps_size(launches):
         for p in plan:
             most = t * g // (p["min_rows"] + 1)
             assert p["tiles"] <= hkv * (min(r, t, most) + t * g // p["bm"]), call
+
+
+def test_the_joining_launch_is_of_the_size_of_what_is_cut(launches):
+    """Partial sums number at most two per share or item aimed at, and the tiles to join half of that, however many
+    requests or rows a step has."""
+    calls = _calls(400, 4) + [(r, r, 4, 8, 128, 40) for r in (64, 1024, 4096)] + [(1 << 18, 4096, 4, 8, 128, 4096)]
+    for call, plan in zip(calls, launches(calls)):
+        hkv, dim = call[3], call[4]
+        for p in plan:
+            slots = p["bytes"] // (p["bm"] * (dim + 2) * 4)
+            assert p["join"] <= slots / 2
+            if p["whole"]:
+                assert p["join"] == slots == 0
+            elif p["shares"]:
+                assert p["join"] == min(p["tiles"], p["grid"] - 1)      # a boundary between shares each
+            else:
+                assert p["join"] <= p["target"] * hkv
