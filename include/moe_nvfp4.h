@@ -515,13 +515,14 @@ moe_status_t moe_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int32_
  * the rule of moe_nvfp4_quantize_act with k_gscale / v_gscale).  k_stride, v_stride: elements from one
  * token's row to the next (at least Hkv*D, multiples of 8; heads are contiguous).  A slot outside
  * [0, num_pages * page_size) is skipped.  Slots of one call must be distinct.  The cache holds finite
- * values only: infinities saturate, a NaN is stored as the largest code of its group. */
+ * values only: infinities saturate, a NaN is stored as the largest code of its group.
+ * Limit: T * kv_heads * head_dim <= 2^36. */
 moe_status_t moe_nvfp4_kv_append(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* k, const uint16_t* v,
                                  int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T, void* stream);
 
 /* Dequantizes the rows at slots [n] (any order, repeats allowed): k, v [n][Hkv][D] bf16 of
  * e2m1 * e4m3 * global scale (one fp32 product, rounded to bf16).  A slot outside the cache gives a
- * NaN row. */
+ * NaN row.  Limit: n <= 2^29 - 32. */
 moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, const int32_t* slots, int32_t n,
                                  uint16_t* k, uint16_t* v, void* stream);
 
@@ -540,9 +541,10 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache /* host */, c
  * Scores are fp32 numbers of magnitude below 2^126; a row with larger ones has no specified result.
  * Deterministic; a row's result depends on the other requests of the call only through the order in
  * which its partial sums are added.
- * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31; R * table_width < 2^31; scale finite and
- * positive, scale * k_gscale within [2^-126, 2^100]; window >= 0; query_offsets ascending; seq_lens <= 2^31 - 4096
- * (a greater one counts as that); out overlaps no input.
+ * Limits: 1 <= Hq / kv_heads <= 64; 0 <= R <= 4096; T * Hq < 2^31, in launches of less than 2^32 work-items each
+ * (T * Hq <= 2^28 always is); R * table_width < 2^31; scale finite and positive, scale * k_gscale within
+ * [2^-126, 2^100]; window >= 0; query_offsets ascending; seq_lens <= 2^31 - 4096 (a greater one counts as that);
+ * out overlaps no input.
  * workspace: moe_nvfp4_kv_attention_workspace_size bytes, 16-byte aligned, are enough for every table; a
  * narrow one may need less, down to none (NULL).  MOE_ERR_WORKSPACE_TOO_SMALL otherwise. */
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim);

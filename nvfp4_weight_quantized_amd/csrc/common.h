@@ -322,6 +322,8 @@ struct KvAttentionProblem {
 };
 size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim,
                               int64_t table_units);
+// Whether every launch of the call holds fewer than 2^32 work-items.
+bool kv_attention_launchable(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim, int64_t table_units);
 moe_status_t launch_kv_attention(const KvAttentionProblem& p, void* workspace, hipStream_t stream);
 
 }  // namespace moe

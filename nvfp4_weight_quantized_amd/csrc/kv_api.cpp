@@ -25,6 +25,11 @@ bool valid_cache(const moe_nvfp4_kv_cache_t* c) {
          valid_gscale(c->v_gscale) && c->pages && al16(c->pages);
 }
 
+// A launch holds fewer than 2^32 work-items: the append one per 32 elements of the rows, up to 2^15 more, the gather 256
+// per 32 rows.
+constexpr int64_t kMaxAppend = (int64_t)1 << 36;
+constexpr int32_t kMaxGather = (1 << 29) - 32;
+
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
@@ -44,8 +49,10 @@ moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, 
   if (!out || !al16(out)) return MOE_ERR_INVALID_ARGUMENT;
   if (R > 0 && (!q || !query_offsets || !seq_lens || !al16(q))) return MOE_ERR_INVALID_ARGUMENT;
   if (R > 0 && table_width > 0 && !block_table) return MOE_ERR_INVALID_ARGUMENT;
-  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim,
-                                                  (int64_t)table_width * (cache->page_size / moe::kKvUnit));
+  const int64_t table_units = (int64_t)table_width * (cache->page_size / moe::kKvUnit);
+  if (!moe::kv_attention_launchable(T, R, Hq, cache->kv_heads, cache->head_dim, table_units))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const size_t need = moe::kv_attention_workspace(T, R, Hq, cache->kv_heads, cache->head_dim, table_units);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && !al16(workspace)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;
@@ -103,6 +110,7 @@ moe_status_t moe_nvfp4_kv_append(const moe_nvfp4_kv_cache_t* cache, const uint16
   const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
   if (T > 1 && (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0))
     return MOE_ERR_INVALID_ARGUMENT;
+  if (T * row > kMaxAppend) return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0) return MOE_OK;
   if (!k || !v || !slots || !al16(k) || !al16(v) || !al4(slots)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;
@@ -111,7 +119,7 @@ moe_status_t moe_nvfp4_kv_append(const moe_nvfp4_kv_cache_t* cache, const uint16
 
 moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache, const int32_t* slots, int32_t n, uint16_t* k,
                                  uint16_t* v, void* stream) {
-  if (!valid_cache(cache) || n < 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (!valid_cache(cache) || n < 0 || n > kMaxGather) return MOE_ERR_INVALID_ARGUMENT;
   if (n == 0) return MOE_OK;
   if (!k || !v || !slots || !al16(k) || !al16(v) || !al4(slots)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;

@@ -1116,6 +1116,10 @@ size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int
   return bytes;
 }
 
+bool kv_attention_launchable(int32_t T, int32_t R, int32_t Hq, int32_t hkv, int32_t D, int64_t table_units) {
+  return T == 0 || R == 0 || launchable(plan_launches(T, R, Hq / hkv, hkv, D, table_units));
+}
+
 moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* workspace, hipStream_t stream) {
   KvAttentionProblem a = problem;
   const int hkv = a.cache.kv_heads, D = a.cache.head_dim;
@@ -1128,8 +1132,6 @@ moe_status_t launch_kv_attention(const KvAttentionProblem& problem, void* worksp
     return launch_status();
   }
   const Launches x = plan_launches(a.T, a.R, a.G, hkv, D, (int64_t)a.width * (a.cache.page_size / kKvUnit));
-  for (int i = 0; i < x.n; ++i)
-    if (x.l[i].grid + fill > 0x7FFFFFFFLL || x.l[i].tiles > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < x.n; ++i) {
     const Launch& p = x.l[i];
     KvPartials part{static_cast<float*>(workspace), nullptr};

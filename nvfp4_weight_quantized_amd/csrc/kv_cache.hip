@@ -311,7 +311,6 @@ moe_status_t launch_kv_append(const moe_nvfp4_kv_cache_t& c, const uint16_t* k, 
   const long long per = 2LL * c.kv_heads * (c.head_dim / 16);
   const bool quads = T * per >= kAppendQuadThreads;
   const long long total = (quads ? (T + 3LL) / 4 : T) * per, blocks = (total + 255) / 256;
-  if (blocks > 0x7FFFFFFFLL) return MOE_ERR_INVALID_ARGUMENT;
   with_head_dim(c.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     if (quads)

@@ -143,5 +143,12 @@ Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, 
   return x;
 }
 
+// A launch holds fewer than 2^32 work-items (512 per workgroup, those that fill rows included).
+bool launchable(const Launches& x) {
+  for (int i = 0; i < x.n; ++i)
+    if ((x.l[i].grid + kCus) * 512 >= (int64_t)1 << 32) return false;
+  return true;
+}
+
 }  // namespace
 }  // namespace moe

@@ -170,6 +170,17 @@ def test_attention_fill_refusals(bad, monkeypatch):
     assert _attend(_cache(), t=0) == L.MOE_OK
 
 
+def test_steps_past_one_launch_are_refused():
+    """More rows than a launch of 2^32 work-items holds."""
+    assert _append(_cache(), t=(1 << 28) + 1) == INV
+    g = L.lib().moe_nvfp4_kv_gather
+    assert g(ctypes.byref(_cache()), 0x4000, (1 << 29) - 31, 0x2000, 0x3000, None) == INV
+    assert g(ctypes.byref(_cache()), 0x4000, 2 ** 31 - 1, 0x2000, 0x3000, None) == INV
+    big = dict(heads=128, stride=128 * 128, t=(1 << 24) - 1)
+    assert _attend(_cache(), **big) == INV
+    assert _attend(_cache(), **{**big, "t": 1 << 21, "width": 1000}, ws=None) == SMALL      # 2^28 rows: accepted so far
+
+
 def test_attention_no_ops_and_sizes():
     assert _attend(None) == INV
     assert _attend(_cache(), t=0) == L.MOE_OK
