@@ -123,13 +123,16 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
 // takes every quad that begins among its W rows (a row whose slot is a multiple of 4 or does not follow
 // the row before it), with the rows after it that continue it, also those of the next window.  W = 1
 // stores bytes, row by row: for steps of few rows, where the threads of the quads would not fill the card.
-// Measured with 8 heads of 128 and a gather of the same rows after it: 1024 rows 13.4 (W = 4) against 10.3 us
-// (W = 1), 2048 rows 15.1 against 14.4, 4096 rows 18.6 against 19.8, 8192 rows 26.2 against 31.1 us.
+// Measured with 8 heads of 128, W = 4 against W = 1, rows of one request from a position that is a multiple of 4 / from
+// another / at scattered slots, where W = 4 takes its rows one after the other: 2048 rows 7.7 against 8.0 / 9.1 against
+// 8.2 / 11.5 against 8.9 us, 4096 rows 10.3 against 12.3 / 11.2 against 12.4 / 14.6 against 13.3 us, 8192 rows 14.3
+// against 20.0 / 15.4 against 20.2 / 30.6 against 25.8 us.  The host does not see the slots: the rule is for those of
+// prompts, which such steps mostly hold.
 // Bound by the vector unit: about 320 instructions per group (two fp32 quotients per element step to be
 // exact to the bit), 16.0 us for 8192 rows of 8 heads of 128, whose 43 MB pass in 8.3 us at the rate of a
 // copy.  Putting whole units together in LDS and writing them in order took 20.8 us: the scattered stores
 // are not what it waits for.
-constexpr long long kAppendQuadThreads = 1 << 18;      // rows * groups from which quads are taken
+constexpr long long kAppendQuadThreads = 1 << 19;      // rows * groups from which quads are taken
 
 __device__ __forceinline__ void load_group16(const uint16_t* __restrict__ row, float (&x)[16]) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
