@@ -51,7 +51,9 @@ constexpr int kTilesTarget = kCus;     // one workgroup is resident per compute 
 constexpr int kTilesMinChunk = 8;      // units: four steps
 // Many rows, block tables of at most so many steps: tiles are not cut, for the same reason (3 requests of 243 to
 // 337 tokens, 4/2 heads, dimension 64, 17 units: 13.2 against 16.2 us; 2 requests of 921, 8 heads, 29 units:
-// 20.7 against 24.4 us; but 3 of 140 to 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us).
+// 20.7 against 24.4 us; 5 of 527 to 763, 24 units, 8 heads on 1 of dimension 128: 25.3 against 35.3 us; but 3 of 140 to
+// 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us, and at 32 units whole tiles lose everywhere: 300 tokens
+// and 3 single ones on 1000 positions, 4/2 heads, dimension 64, 21.1 against 13.6 us).
 constexpr int kTilesWholeSteps = 12;
 constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
 // Requests of more rows go to the tile kernel where both run.  32 requests on 4000 positions, 32/8 heads,
@@ -59,9 +61,20 @@ constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 
 // 137 us, but then 12 short prompts of up to 32 tokens take 15.1 instead of 9.7 us (two more launches).
 constexpr int kRowsSplit = 64;
 // Requests * heads * units of the table up to which the tile kernel takes requests of few rows too, and two
-// launches are saved (5 prompts of 527 to 763 tokens, 2 heads: 24.5 against 28.9 us).  A request of one row and
+// launches are saved (5 prompts of 527 to 763 tokens, 4/2 heads, dimension 64: 17.5 against 21.3 us; 4 chunks of 100
+// on up to 900 positions, 32/8 heads, dimension 128: 36.9 against 41.3 us; 300 tokens and 3 single ones on 1000: 18.3
+// against 30.8 us).  A request of one row and
 // a long context takes several times longer there.
 constexpr int64_t kAloneWork = 2048;
+
+// Query rows, over all heads, beyond one token per request, from which a long request is taken to be among many short
+// ones and the tile kernel is launched beside the few-row kernel.  The few-row kernel alone against both:
+// 32/8 heads, dimension 128: 1000 single tokens and a chunk of 500 (16k rows) 246 against 408 us, 300 and 900 (29k)
+// 185 / 220, 200 requests of 6 tokens (32k) 129 / 153, 400 and 1500 on 4000 positions (48k) 513 / 417, 400 and 6000
+// (192k) 1418 / 592; 8/2 heads, dimension 64: 400 and 3000 (24k) 125 / 139, 400 and 6000 (48k) 245 / 210.
+// Where the tile kernel takes all requests (kAloneWork) from 1024 tokens on: 60 prompts of 1 to 59 tokens, 4/4 heads,
+// dimension 64, 14.8 / 7.0 us, 90 of 1 to 30, 32/8 heads, dimension 128, 44.3 / 24.4 us.
+constexpr int64_t kLikelyRows = 40960;
 
 int rows_resident(int D, int bm) {
   if (D == 64) return bm == 16 ? rows_occupancy<64, 1>() : rows_occupancy<64, 2>();
@@ -70,7 +83,7 @@ int rows_resident(int D, int bm) {
 }
 
 // Most requests of more than min_rows rows that a step of T tokens can hold.  (A padded batch of 1000 single tokens,
-// T = 1024, also launches the tile kernel: with R in place of this bound its workgroups, each with a search of all
+// T = 1024, once also launched the tile kernel: with R in place of this bound its workgroups, each with a search of all
 // lengths, made 384 us 1220 us.)
 int64_t requests_of(int min_rows, int32_t T, int32_t R, int32_t G) {
   return std::min({(int64_t)R, (int64_t)T, (int64_t)T * G / (min_rows + 1)});
@@ -121,10 +134,11 @@ struct Launches {
 Launches plan_launches(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int64_t table_units) {
   Launches x{};
   const int64_t rows = (int64_t)T * G;
-  // Requests of more than kRowsSplit rows are certain, or likely: a step of 1024 rows and more that are not all
-  // of single tokens.
-  const bool tiles = rows > (int64_t)kRowsSplit * R || (T >= 1024 && T > R);
-  const bool few = !tiles || (R > 1 && (int64_t)R * hkv * std::min(table_units, (int64_t)1 << 32) > kAloneWork);
+  // Requests of more than kRowsSplit rows are certain, or likely.
+  const bool alone = R == 1 || (int64_t)R * hkv * std::min(table_units, (int64_t)1 << 32) <= kAloneWork;
+  const bool likely = T > R && (alone ? T >= 1024 : ((int64_t)T - R) * G * hkv >= kLikelyRows);
+  const bool tiles = rows > (int64_t)kRowsSplit * R || likely;
+  const bool few = !tiles || !alone;
   if (tiles) {
     // 32 rows per wave (256 per tile) at twice the rate, 16 rows (128) with twice the tiles.  Measured, 32/8
     // heads, dimension 128: prompt of 8192 (264k units over all tiles) 572 against 849 us, 512 tokens on

@@ -17,7 +17,8 @@ def _case(seed, dim, kv_heads, group, reqs, **kw):
 
 @pytest.mark.parametrize("requests,most_new,most_old,dim,kv_heads,group,pad,extra", [
     (1100, 1, 60, 64, 2, 1, 0, 1),       # more tiles than shares, each share with some whole ones
-    (1100, 1, 60, 64, 2, 1, 30, 70),     # padded past 1024 rows: both kernels
+    (1100, 1, 60, 64, 2, 1, 30, 70),     # padded past 1024 rows
+    (600, 1, 20, 64, 1, 16, 2600, 70),    # padded by so many that the kernel of many rows is launched too
     (700, 3, 30, 128, 4, 2, 0, 1),
     (900, 2, 20, 256, 2, 3, 0, 40),
     (4096, 1, 20, 64, 1, 2, 0, 1),

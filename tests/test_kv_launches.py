@@ -99,3 +99,12 @@ def test_the_joining_launch_is_of_the_size_of_what_is_cut(launches):
                 assert p["join"] == min(p["tiles"], p["grid"] - 1)      # a boundary between shares each
             else:
                 assert p["join"] <= p["target"] * hkv
+
+
+def test_padding_does_not_bring_the_kernel_of_many_rows(launches):
+    """Batches of single tokens and short drafts past 1024 rows take one kernel; a prompt among them takes both."""
+    for r, t in ((1000, 1024), (1023, 1030), (4000, 4096), (600, 1200)):
+        (plan,) = launches([(t, r, 4, 8, 128, 400)])
+        assert [p["shares"] for p in plan] == [1], (r, t)
+    (plan,) = launches([(3400, 400, 4, 8, 128, 400)])
+    assert [p["shares"] for p in plan] == [0, 1]
