@@ -565,11 +565,14 @@ __global__ __launch_bounds__(64 * NW, (rows_occupancy<D, MI, NW>())) void kv_att
 //   even elements, then the odd ones).  Half the rows per operand read, which LDS bandwidth then bounds at
 //   half the matrix rate, and twice the tiles.  Taken where those fill the card better (plan_launches), and
 //   for head dimension 256, whose 32-row outputs and queries (128 + 64 of 256 registers) leave none to
-//   overlap anything: 249 us against 263 us for the chunks of 5 requests (16/2 heads, window 1024).
+//   overlap anything: 175 us against 350 us for the chunks of 5 requests (16/2 heads, window 1024).
 // Bound by the vector unit and LDS beside the matrix unit: a prompt of 8192 (32/8 heads, dimension 128)
-// runs at 963-996 TFLOP/s, the matrix unit 45% busy, 7.6 vector instructions per 32-cycle matrix
+// runs at 975-1002 TFLOP/s, the matrix unit 46% busy, 7.0 vector instructions beside each 32-cycle matrix
 // instruction (32 exponentials, 32 fused multiply-adds, 37 additions, 16 conversions, 16 maxima and the
-// wave's eighth of the dequantization per 32 of them).
+// wave's eighth of the dequantization per 32 of them).  The chunks (dimension 256) run at 470 TFLOP/s, the matrix unit
+// 25% busy, 5.2 vector instructions beside each 16-cycle one: matrix, LDS and vector work of a step of one unit follow
+// one another, with two waves per SIMD in step and a barrier every 32 positions, and about 620 items make 2.4 rounds of
+// the 256 places.
 template <int D, int NW, int NU, int RS>
 __global__ __launch_bounds__(64 * NW, 2) void kv_attention_tiles_kernel(KvAttentionProblem a, KvSchedule s,
                                                                         KvPartials part) {

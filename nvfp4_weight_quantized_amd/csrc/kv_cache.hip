@@ -128,10 +128,11 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(
 // 8.2 / 11.5 against 8.9 us, 4096 rows 10.3 against 12.3 / 11.2 against 12.4 / 14.6 against 13.3 us, 8192 rows 14.3
 // against 20.0 / 15.4 against 20.2 / 30.6 against 25.8 us.  The host does not see the slots: the rule is for those of
 // prompts, which such steps mostly hold.
-// Bound by the vector unit: about 320 instructions per group (two fp32 quotients per element step to be
-// exact to the bit), 16.0 us for 8192 rows of 8 heads of 128, whose 43 MB pass in 8.3 us at the rate of a
-// copy.  Putting whole units together in LDS and writing them in order took 20.8 us: the scattered stores
-// are not what it waits for.
+// Bound by the vector unit and the memory one after the other: 14.3 us for 8192 rows of 8 heads of 128 (16 us with
+// other work in the caches), of which about 335 instructions per group (32 of them the second quotient step) make 9 us
+// and the 43 MB at the rate of a copy 8.3 us.  It is one round of four waves per SIMD, and each begins with loads of
+// slots that wait for one another before its rows are asked for.  Putting whole units together in LDS and writing them
+// in order took 20.8 us: the scattered stores are not what it waits for.
 constexpr long long kAppendQuadThreads = 1 << 19;      // rows * groups from which quads are taken
 
 __device__ __forceinline__ void load_group16(const uint16_t* __restrict__ row, float (&x)[16]) {

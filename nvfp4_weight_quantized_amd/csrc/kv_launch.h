@@ -44,27 +44,27 @@ constexpr int kRowsMinChunk = 4;       // units: one per wave
 constexpr int kSwitch = 8;             // empty places before a tile's units in the order of the shares (KvShare)
 // Few rows, block tables of at most so many units and at most so many tiles: a workgroup of 8 waves takes a
 // tile whole.  These are bound by latency, and whole tiles save the combine launch and its gap (one request
-// of 1024 positions, 32/4 heads, dimension 128: 10.5 against 11.1 us on the GPU, 14.8 against 17.4 us with the
-// host's part; 16 waves: 12.4 us on the GPU).
+// of 1024 positions, 32/4 heads, dimension 128: 11.1 us on the GPU, 10.8 us a call, against 12.1 and 13.8 us; 16 waves
+// took 1.9 us longer than 8).
 constexpr int kWholeUnits = 64, kWholeTiles = 256;
 constexpr int kTilesTarget = kCus;     // one workgroup is resident per compute unit
 constexpr int kTilesMinChunk = 8;      // units: four steps
 // Many rows, block tables of at most so many steps: tiles are not cut, for the same reason (3 requests of 243 to
 // 337 tokens, 4/2 heads, dimension 64, 17 units: 13.2 against 16.2 us; 2 requests of 921, 8 heads, 29 units:
 // 20.7 against 24.4 us; 5 of 527 to 763, 24 units, 8 heads on 1 of dimension 128: 25.3 against 35.3 us; but 3 of 140 to
-// 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us, and at 32 units whole tiles lose everywhere: 300 tokens
-// and 3 single ones on 1000 positions, 4/2 heads, dimension 64, 21.1 against 13.6 us).
+// 439, 3 heads, dimension 128, 26 units: 24.9 against 21.9 us).  Past that it goes by the number of tiles, which the
+// host does not know well: 4 chunks of 100 on up to 900 positions, 30 units, dimension 128, 29.5 against 36.9 us with
+// 32/8 heads, 28.4 against 20.5 us with 8/1; 300 tokens and 3 single ones on 1000, 32 units, 29.4 against 18.3 us.
 constexpr int kTilesWholeSteps = 12;
 constexpr int64_t kWideWork = 32768;   // tiles * units of the table from which 32-row waves are taken
 // Requests of more rows go to the tile kernel where both run.  32 requests on 4000 positions, 32/8 heads,
-// dimension 128: 64 rows each 83 us, in the tile kernel 144 us; 128 rows each 153 us, in the few-row kernel
-// 137 us, but then 12 short prompts of up to 32 tokens take 15.1 instead of 9.7 us (two more launches).
+// dimension 128: 64 rows each 96 us, in the tile kernel 145 us; 128 rows each 149 us, in the few-row kernel
+// 144 us, but then 12 short prompts of up to 32 tokens take 14.2 instead of 7.9 us (two more launches).
 constexpr int kRowsSplit = 64;
 // Requests * heads * units of the table up to which the tile kernel takes requests of few rows too, and two
 // launches are saved (5 prompts of 527 to 763 tokens, 4/2 heads, dimension 64: 17.5 against 21.3 us; 4 chunks of 100
 // on up to 900 positions, 32/8 heads, dimension 128: 36.9 against 41.3 us; 300 tokens and 3 single ones on 1000: 18.3
-// against 30.8 us).  A request of one row and
-// a long context takes several times longer there.
+// against 30.8 us).  A request of one row and a long context takes several times longer there.
 constexpr int64_t kAloneWork = 2048;
 
 // Query rows, over all heads, beyond one token per request, from which a long request is taken to be among many short
