@@ -247,7 +247,7 @@ def kv_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tens
     that sees nothing, whose output is zero).  Rows outside every request (a padded batch) are left as
     they were in a given ``out`` and zeros without it; their ``lse`` is -inf.  q may be a slice of a fused
     projection's output.  Without ``workspace`` the call takes one from torch's allocator where it needs
-    one, so calls on several streams do not share it.
+    one, so calls on several streams do not share it.  ``out`` and ``workspace`` overlap no other argument.
     """
     c, dev = cache._struct, cache._dev
     dim, kv_heads = c.head_dim, c.kv_heads
