@@ -80,6 +80,14 @@ def test_large_scores_of_one_sign(dim, group, reqs, extra, exponent, sign):
     _check_largest(case, *case.run())
 
 
+@pytest.mark.parametrize("dim,group,reqs,extra", SHAPES)
+def test_scores_near_the_end_of_fp32(dim, group, reqs, extra):
+    """Scores of about 2^120, from large keys and large queries."""
+    case = _case(dim, group, reqs, extra, 62, seed=54)
+    case.q *= 2.0 ** 58
+    _check_largest(case, *case.run())
+
+
 @pytest.mark.parametrize("exponent", [16, 30, 40])
 @pytest.mark.parametrize("dim,group,reqs,extra", SHAPES)
 def test_equal_large_scores_share(dim, group, reqs, extra, exponent):
