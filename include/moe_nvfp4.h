@@ -560,6 +560,46 @@ moe_status_t moe_nvfp4_kv_attention_fill(const moe_nvfp4_kv_cache_t* cache /* ho
                                          int32_t window, uint16_t* out, float* lse, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ * Queries and keys turned by their positions before the attention.  Pair i of a head, i < pairs, turns by the angle
+ * a = positions[axis[i]][t] * inv_freq[i] (one fp64 product):
+ *   y1 = x1 * c - x2 * s,  y2 = x2 * c + x1 * s,  c = fp32(scale * cos a),  s = fp32(scale * sin a),
+ * every fp32 product and sum rounded on its own and y rounded to bf16.  The pair is elements (i, pairs + i) of the head,
+ * or with `interleaved` (2i, 2i + 1); elements from 2 * pairs on pass unchanged.  Several axes (time, height, width of
+ * images and video) give each pair the position of its own axis.
+ * Limits: head_dim a multiple of 16, at most 512; pairs a multiple of 8, 2 * pairs <= head_dim; 1 <= axes <= 4; scale
+ * finite.  inv_freq is finite with magnitude at most 256 (others give unspecified values in the row); an axis outside
+ * [0, axes) counts as the nearest one inside. */
+typedef struct {
+  int32_t head_dim;        /* D */
+  int32_t pairs;
+  int32_t axes;
+  int32_t interleaved;     /* 0 or 1 */
+  float scale;             /* of cosines and sines (1 unless a long-context rule says otherwise) */
+  const double* inv_freq;  /* device [pairs] */
+  const int32_t* axis;     /* device [pairs], or NULL: axis 0 for every pair */
+} moe_rotary_t;
+
+/* Rotates the rows x [T][heads][D] bf16 into out [T][heads][D] bf16; x_stride, out_stride: elements from token to token
+ * (at least heads*D, multiples of 8; heads are contiguous).  positions: int32 [axes][T], position_stride elements from
+ * axis to axis (at least T).  out is x, with the same stride, or overlaps no input.
+ * Limits: T * heads * D <= 2^36, T < 2^24, heads <= 65536. */
+moe_status_t moe_rotary(const moe_rotary_t* rotary /* host */, const uint16_t* x, int64_t x_stride, int32_t T,
+                        int32_t heads, const int32_t* positions, int64_t position_stride, uint16_t* out,
+                        int64_t out_stride, void* stream);
+
+/* A step's rows on their way into the cache, in one launch: q [T][Hq][D] rotated into q_out [T][Hq][D], k rotated and
+ * then quantized, v quantized into the cache at slots [T]: the same bytes as moe_rotary on q and on k, then
+ * moe_nvfp4_kv_append.  Arguments as for those two; the rotary's head_dim is the cache's.  q_out is q, with the same
+ * stride, or overlaps no input.  Limits: T * Hq * D <= 2^35, T * kv_heads * D <= 2^35,
+ * T < 2^24, Hq <= 65536. */
+moe_status_t moe_nvfp4_kv_append_rotary(const moe_nvfp4_kv_cache_t* cache /* host */,
+                                        const moe_rotary_t* rotary /* host */, const uint16_t* q, int64_t q_stride,
+                                        int32_t Hq, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                        int64_t v_stride, const int32_t* positions, int64_t position_stride,
+                                        const int32_t* slots, int32_t T, uint16_t* q_out, int64_t q_out_stride,
+                                        void* stream);
+
 /* ---------------------------------------------------------------- measurement helper
  * Not a step of the layer: reads `bytes` bytes of device memory at `buf` once with a plain
  * streaming-read kernel (16-byte non-temporal loads, at most `workgroups` workgroups of 256 threads

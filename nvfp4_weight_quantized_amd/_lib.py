@@ -60,6 +60,12 @@ class KvCache(ctypes.Structure):
                 ("k_gscale", ctypes.c_float), ("v_gscale", ctypes.c_float), ("pages", c_void_p)]
 
 
+class RotaryStruct(ctypes.Structure):
+    """moe_rotary_t"""
+    _fields_ = [("head_dim", i32), ("pairs", i32), ("axes", i32), ("interleaved", i32), ("scale", ctypes.c_float),
+                ("inv_freq", c_void_p), ("axis", c_void_p)]
+
+
 MOE_FORWARD_FUSED_DECODE = 1
 
 
@@ -110,6 +116,10 @@ SIGNATURES = {
     "moe_kv_plan": (i32, [c_void_p, c_void_p, i32, i32, i32, c_void_p, i32, c_void_p, i32, i32, c_void_p, c_void_p,
                           c_void_p, c_void_p, c_void_p, c_void_p]),
     "moe_nvfp4_kv_append": (i32, [ctypes.POINTER(KvCache), c_void_p, c_void_p, i64, i64, c_void_p, i32, c_void_p]),
+    "moe_rotary": (i32, [ctypes.POINTER(RotaryStruct), c_void_p, i64, i32, i32, c_void_p, i64, c_void_p, i64, c_void_p]),
+    "moe_nvfp4_kv_append_rotary": (i32, [ctypes.POINTER(KvCache), ctypes.POINTER(RotaryStruct), c_void_p, i64, i32,
+                                         c_void_p, i64, c_void_p, i64, c_void_p, i64, c_void_p, i32, c_void_p, i64,
+                                         c_void_p]),
     "moe_nvfp4_kv_gather": (i32, [ctypes.POINTER(KvCache), c_void_p, i32, c_void_p, c_void_p, c_void_p]),
     "moe_nvfp4_kv_attention_workspace_size": (size_t, [i32, i32, i32, i32, i32]),
     "moe_nvfp4_kv_attention": (i32, [ctypes.POINTER(KvCache), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32,

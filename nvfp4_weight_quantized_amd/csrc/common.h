@@ -303,6 +303,22 @@ moe_status_t launch_kv_append(const moe_nvfp4_kv_cache_t& c, const uint16_t* k, 
 moe_status_t launch_kv_gather(const moe_nvfp4_kv_cache_t& c, const int32_t* slots, int32_t n, uint16_t* k,
                               uint16_t* v, hipStream_t stream);
 
+// Rotary positions -------------------------------------------------------------------------------
+struct RotaryProblem {
+  moe_rotary_t r;
+  const uint16_t* x;        // [T][heads][head_dim], x_stride elements per token
+  int64_t x_stride;
+  int32_t T, heads;
+  const int32_t* positions; // [axes][T], position_stride elements per axis
+  int64_t position_stride;
+  uint16_t* out;            // [T][heads][head_dim], out_stride elements per token; may be x
+  int64_t out_stride;
+};
+moe_status_t launch_rotary(const RotaryProblem& p, hipStream_t stream);
+moe_status_t launch_kv_append_rotary(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q, const uint16_t* k,
+                                     const uint16_t* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                     hipStream_t stream);
+
 struct KvAttentionProblem {
   moe_nvfp4_kv_cache_t cache;
   const uint16_t* q;        // [T][Hq][D], q_stride elements per token

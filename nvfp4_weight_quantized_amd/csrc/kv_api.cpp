@@ -1,5 +1,5 @@
-// C ABI of the paged NVFP4 key/value cache: host-side validation, then the launches of kv_cache.hip
-// and kv_attention.hip.  Nothing is enqueued on an error, nothing synchronises or allocates.
+// C ABI of the paged NVFP4 key/value cache and of rotary positions: host-side validation, then the launches of
+// kv_cache.hip, rotary.hip and kv_attention.hip.  Nothing is enqueued on an error, nothing synchronises or allocates.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -31,6 +31,28 @@ constexpr int64_t kMaxAppend = (int64_t)1 << 36;
 constexpr int32_t kMaxGather = (1 << 29) - 32;
 
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+bool valid_rotary(const moe_rotary_t* r) {
+  if (!r || r->head_dim < 16 || r->head_dim > 512 || r->head_dim % 16 != 0) return false;
+  if (r->pairs < 8 || r->pairs % 8 != 0 || 2 * r->pairs > r->head_dim || r->axes < 1 || r->axes > 4) return false;
+  if ((r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->scale)) return false;
+  return r->inv_freq && (reinterpret_cast<uintptr_t>(r->inv_freq) & 7) == 0 && al4(r->axis);
+}
+
+// Rows [T][heads][dim] and the token stride that reaches them.
+bool valid_stride(int32_t T, int64_t stride, int64_t row) { return T <= 1 || (stride >= row && stride % 8 == 0); }
+
+// A launch of the rotary kernels holds fewer than 2^32 work-items: the rows one per 8 elements and up to 255 more per
+// token, of which there are at least 16 (32 and 2^35 for the append's three kinds together).
+constexpr int64_t kMaxRotary = (int64_t)1 << 36, kMaxAppendRotary = (int64_t)1 << 35;
+
+bool valid_rotary_rows(const moe_rotary_t& r, int64_t x_stride, int32_t T, int32_t heads, int64_t position_stride,
+                       int64_t out_stride, int64_t most) {
+  const int64_t row = (int64_t)heads * r.head_dim;
+  if (T < 0 || heads < 1 || heads > 65536 || T * row > most || (int64_t)T >= (int64_t)1 << 24) return false;
+  if (r.axes > 1 && position_stride < T) return false;
+  return valid_stride(T, x_stride, row) && valid_stride(T, out_stride, row);
+}
 
 moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
                           int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
@@ -124,6 +146,41 @@ moe_status_t moe_nvfp4_kv_gather(const moe_nvfp4_kv_cache_t* cache, const int32_
   if (!k || !v || !slots || !al16(k) || !al16(v) || !al4(slots)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;
   return moe::launch_kv_gather(*cache, slots, n, k, v, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t moe_rotary(const moe_rotary_t* rotary, const uint16_t* x, int64_t x_stride, int32_t T, int32_t heads,
+                        const int32_t* positions, int64_t position_stride, uint16_t* out, int64_t out_stride,
+                        void* stream) {
+  if (!valid_rotary(rotary) || !valid_rotary_rows(*rotary, x_stride, T, heads, position_stride, out_stride, kMaxRotary))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0) return MOE_OK;
+  if (!x || !positions || !out || !al16(x) || !al16(out) || !al4(positions)) return MOE_ERR_INVALID_ARGUMENT;
+  if (x == out && T > 1 && x_stride != out_stride) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  const moe::RotaryProblem p{*rotary, x, x_stride, T, heads, positions, position_stride, out, out_stride};
+  return moe::launch_rotary(p, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t moe_nvfp4_kv_append_rotary(const moe_nvfp4_kv_cache_t* cache, const moe_rotary_t* rotary,
+                                        const uint16_t* q, int64_t q_stride, int32_t Hq, const uint16_t* k,
+                                        int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                        const int32_t* positions, int64_t position_stride, const int32_t* slots,
+                                        int32_t T, uint16_t* q_out, int64_t q_out_stride, void* stream) {
+  if (!valid_cache(cache) || !valid_rotary(rotary) || rotary->head_dim != cache->head_dim)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!valid_rotary_rows(*rotary, q_stride, T, Hq, position_stride, q_out_stride, kMaxAppendRotary))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+  if (!valid_stride(T, k_stride, row) || !valid_stride(T, v_stride, row) || T * row > kMaxAppendRotary)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0) return MOE_OK;
+  if (!q || !k || !v || !positions || !slots || !q_out) return MOE_ERR_INVALID_ARGUMENT;
+  if (!al16(q) || !al16(k) || !al16(v) || !al16(q_out) || !al4(positions) || !al4(slots))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (q == q_out && T > 1 && q_stride != q_out_stride) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  const moe::RotaryProblem p{*rotary, q, q_stride, T, Hq, positions, position_stride, q_out, q_out_stride};
+  return moe::launch_kv_append_rotary(*cache, p, k, v, k_stride, v_stride, slots, static_cast<hipStream_t>(stream));
 }
 
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim) {
