@@ -560,6 +560,69 @@ moe_status_t moe_nvfp4_kv_attention_fill(const moe_nvfp4_kv_cache_t* cache /* ho
                                          int32_t window, uint16_t* out, float* lse, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- sparse attention over the cache
+ * For long contexts: each query row reads only the pages that a cheap score chooses for it ("Qwen3.8-Flash-Next-NVFP4",
+ * the sparse attention whose indexer scores the cache; the form of the score below is this library's own).
+ *
+ * The index holds, per page and kv head, the mean of the page's keys in 8 bits: codes [num_pages][kv_heads][D] and
+ * scales [num_pages][kv_heads], mean = code * scale * k_gscale.  With S_d the sum of e2m1 * e4m3 over the page's
+ * positions in units of 2^-10 (a whole number, exact) and A = max_d |S_d|: code_d = 127 S_d / A to the nearest whole
+ * number (ties to even), scale = fp32(A / (127 * 1024 * positions)); zeros where A = 0. */
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int8_t* codes;       /* device, 16-byte aligned */
+  float* scales;       /* device */
+} moe_nvfp4_kv_index_t;
+
+/* The index of every page that holds a row of the step, from what the cache holds of it now (append first): row i of n
+ * of request r has position seq_lens[r] - n + i, and a page's mean is over its positions below seq_lens[r].  Offsets,
+ * lengths and table as for moe_nvfp4_kv_attention; pages whose table entry lies outside [0, num_pages) or behind the
+ * table are skipped.  T: token rows of the step.  With offsets that count whole lengths the index of a cache filled
+ * earlier is built.  A physical page is touched by one request of a call.  The index and the cache have equal sizes.
+ * Limits: as for the cache and its attention; (T / page_size + 2 R) * kv_heads < 2^24. */
+moe_status_t moe_nvfp4_kv_index_update(const moe_nvfp4_kv_cache_t* cache /* host */,
+                                       const moe_nvfp4_kv_index_t* index /* host */, const int32_t* query_offsets,
+                                       const int32_t* seq_lens, int32_t R, const int32_t* block_table,
+                                       int32_t table_width, int32_t T, void* stream);
+
+/* The pages each row reads: selected [T][kv_heads][top_k], logical page numbers (columns of the block table), ascending,
+ * -1 behind them.  A row at position i chooses among the pages 0 .. i / page_size: always the first `first` and the last
+ * `last` of them, and of the others the highest scores, equal ones the lowest page first.  With x the row of one of the
+ * kv head's Hq / kv_heads heads, a = max |x_d| and x8_d = x_d * fp32(127 / a) to the nearest whole number (ties to even),
+ *   score = max over the heads of fp32(fp32((x8 . codes) * a)) * scale, in fp32;
+ * a row of a head with a value that is not finite or above 2^100, or with a < 2^-100, counts as zeros.  Pages whose table
+ * entry is outside [0, num_pages) are not chosen by score; those of the last `last` that lie behind the table are listed
+ * (the attention makes such rows NaN).  Rows of no request, and rows at negative positions, get -1 only.
+ * q as for moe_nvfp4_kv_attention.
+ * Limits: 1 <= first + last <= top_k <= 1024, first >= 0, last >= 1; table_width <= 32768; T * kv_heads < 2^24. */
+moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index /* host */, const uint16_t* q, int64_t q_stride,
+                                 int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                                 const int32_t* block_table, int32_t table_width, int32_t top_k, int32_t first,
+                                 int32_t last, int32_t* selected, void* stream);
+
+/* Attention of the step's query rows over the pages chosen for them.  As moe_nvfp4_kv_attention without a window, but a
+ * row of kv head h of token t sees, of the positions up to its own, only those in the pages selected[t][h][0 .. top_k):
+ * page numbers (columns of the block table) in ascending order, negative ones behind them.  A page listed twice counts
+ * once; one behind the row's own position is not seen; one whose table entry is outside [0, num_pages), or behind the
+ * table, makes the row NaN.  A row that sees nothing gets zeros and lse = -inf.  Lists in another order give
+ * unspecified rows of their token and of the tokens around it, and nothing else.
+ * Limits: those of moe_nvfp4_kv_attention, 1 <= top_k <= 1024, and the launch holds fewer than 2^32 work-items (T * Hq <=
+ * 2^23 always does).  out and lse overlap no input.  No workspace. */
+moe_status_t moe_nvfp4_kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q,
+                                           int64_t q_stride, int32_t T, int32_t Hq, const int32_t* query_offsets,
+                                           const int32_t* seq_lens, int32_t R, const int32_t* block_table,
+                                           int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
+                                           uint16_t* out, float* lse, void* stream);
+/* The same for out and lse without content yet: rows outside every request get zeros and lse = -inf. */
+moe_status_t moe_nvfp4_kv_sparse_attention_fill(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q,
+                                                int64_t q_stride, int32_t T, int32_t Hq, const int32_t* query_offsets,
+                                                const int32_t* seq_lens, int32_t R, const int32_t* block_table,
+                                                int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
+                                                uint16_t* out, float* lse, void* stream);
+
 /* ---------------------------------------------------------------- rotary positions
  * Queries and keys turned by their positions before the attention.  Pair i of a head, i < pairs, turns by the angle
  * a = positions[axis[i]][t] * inv_freq[i] (one fp64 product):

@@ -60,6 +60,12 @@ class KvCache(ctypes.Structure):
                 ("k_gscale", ctypes.c_float), ("v_gscale", ctypes.c_float), ("pages", c_void_p)]
 
 
+class KvIndex(ctypes.Structure):
+    """moe_nvfp4_kv_index_t"""
+    _fields_ = [("num_pages", i32), ("page_size", i32), ("kv_heads", i32), ("head_dim", i32), ("codes", c_void_p),
+                ("scales", c_void_p)]
+
+
 class RotaryStruct(ctypes.Structure):
     """moe_rotary_t"""
     _fields_ = [("head_dim", i32), ("pairs", i32), ("axes", i32), ("interleaved", i32), ("scale", ctypes.c_float),
@@ -120,6 +126,10 @@ SIGNATURES = {
     "moe_nvfp4_kv_append_rotary": (i32, [ctypes.POINTER(KvCache), ctypes.POINTER(RotaryStruct), c_void_p, i64, i32,
                                          c_void_p, i64, c_void_p, i64, c_void_p, i64, c_void_p, i32, c_void_p, i64,
                                          c_void_p]),
+    "moe_nvfp4_kv_index_update": (i32, [ctypes.POINTER(KvCache), ctypes.POINTER(KvIndex), c_void_p, c_void_p, i32,
+                                        c_void_p, i32, i32, c_void_p]),
+    "moe_nvfp4_kv_select": (i32, [ctypes.POINTER(KvIndex), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32, c_void_p,
+                                  i32, i32, i32, i32, c_void_p, c_void_p]),
     "moe_nvfp4_kv_gather": (i32, [ctypes.POINTER(KvCache), c_void_p, i32, c_void_p, c_void_p, c_void_p]),
     "moe_nvfp4_kv_attention_workspace_size": (size_t, [i32, i32, i32, i32, i32]),
     "moe_nvfp4_kv_attention": (i32, [ctypes.POINTER(KvCache), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32,
@@ -127,6 +137,9 @@ SIGNATURES = {
                                      c_void_p]),
 }
 SIGNATURES["moe_nvfp4_kv_attention_fill"] = SIGNATURES["moe_nvfp4_kv_attention"]
+SIGNATURES["moe_nvfp4_kv_sparse_attention"] = SIGNATURES["moe_nvfp4_kv_sparse_attention_fill"] = (
+    i32, [ctypes.POINTER(KvCache), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32, c_void_p, i32, c_void_p, i32,
+          ctypes.c_float, c_void_p, c_void_p, c_void_p])
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 

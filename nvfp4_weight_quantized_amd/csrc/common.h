@@ -319,6 +319,27 @@ moe_status_t launch_kv_append_rotary(const moe_nvfp4_kv_cache_t& c, const Rotary
                                      const uint16_t* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
                                      hipStream_t stream);
 
+// Choice of pages --------------------------------------------------------------------------------
+struct KvStep {
+  const int32_t* offsets;   // [R + 1]
+  const int32_t* lens;      // [R]
+  const int32_t* table;     // [R][width]
+  int32_t R, T, width, page_size;
+};
+int64_t kv_index_items(int32_t T, int32_t R, int32_t page_size);      // bound on the pages that a step touches
+moe_status_t launch_kv_index_update(const moe_nvfp4_kv_cache_t& c, const moe_nvfp4_kv_index_t& index, const KvStep& s,
+                                    hipStream_t stream);
+struct KvSelectProblem {
+  moe_nvfp4_kv_index_t index;
+  KvStep step;
+  const uint16_t* q;        // [T][kv_heads * G][head_dim], q_stride elements per token
+  int64_t q_stride;
+  int32_t G;
+  int32_t top_k, first, last;
+  int32_t* selected;        // [T][kv_heads][top_k]
+};
+moe_status_t launch_kv_select(const KvSelectProblem& p, hipStream_t stream);
+
 struct KvAttentionProblem {
   moe_nvfp4_kv_cache_t cache;
   const uint16_t* q;        // [T][Hq][D], q_stride elements per token
@@ -341,5 +362,13 @@ size_t kv_attention_workspace(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads
 // Whether every launch of the call holds fewer than 2^32 work-items.
 bool kv_attention_launchable(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim, int64_t table_units);
 moe_status_t launch_kv_attention(const KvAttentionProblem& p, void* workspace, hipStream_t stream);
+
+struct KvSparseProblem {
+  KvAttentionProblem a;     // without a window
+  const int32_t* selected;  // [T][kv_heads][top_k]
+  int32_t top_k;
+};
+bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t kv_heads, int32_t top_k);
+moe_status_t launch_kv_sparse_attention(const KvSparseProblem& p, hipStream_t stream);
 
 }  // namespace moe

@@ -1,5 +1,5 @@
 // C ABI of the paged NVFP4 key/value cache and of rotary positions: host-side validation, then the launches of
-// kv_cache.hip, rotary.hip and kv_attention.hip.  Nothing is enqueued on an error, nothing synchronises or allocates.
+// kv_cache.hip, rotary.hip, kv_index.hip, kv_sparse.hip and kv_attention.hip.  Nothing is enqueued on an error, nothing synchronises or allocates.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -31,6 +31,19 @@ constexpr int64_t kMaxAppend = (int64_t)1 << 36;
 constexpr int32_t kMaxGather = (1 << 29) - 32;
 
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+bool valid_index(const moe_nvfp4_kv_index_t* x) {
+  return x && valid_cache_dims(x->num_pages, x->page_size, x->kv_heads, x->head_dim) && x->codes && x->scales &&
+         al16(x->codes) && al4(x->scales);
+}
+
+// Offsets, lengths and table of a step of R > 0 requests.
+bool valid_step(const moe::KvStep& s) {
+  if (s.T < 0 || s.R < 0 || s.R > moe::kKvMaxRequests || s.width < 0) return false;
+  if ((int64_t)s.R * s.width >= ((int64_t)1 << 31)) return false;
+  if (s.R == 0 || s.T == 0) return true;
+  return s.offsets && s.lens && (s.width == 0 || s.table) && al4(s.offsets) && al4(s.lens) && al4(s.table);
+}
 
 bool valid_rotary(const moe_rotary_t* r) {
   if (!r || r->head_dim < 16 || r->head_dim > 512 || r->head_dim % 16 != 0) return false;
@@ -96,6 +109,47 @@ moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, 
   p.lse = lse;
   p.fill = fill;
   return moe::launch_kv_attention(p, workspace, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
+                                 int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                                 const int32_t* block_table, int32_t table_width, const int32_t* selected,
+                                 int32_t top_k, float scale, uint16_t* out, float* lse, bool fill, void* stream) {
+  if (!valid_cache(cache)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::KvStep step{query_offsets, seq_lens, block_table, R, T, table_width, cache->page_size};
+  if (!valid_step(step)) return MOE_ERR_INVALID_ARGUMENT;
+  if (Hq < 1 || Hq % cache->kv_heads != 0 || Hq / cache->kv_heads > 64 || (int64_t)T * Hq >= ((int64_t)1 << 31))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (top_k < 1 || top_k > moe::kKvMaxSelected) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(std::isfinite(scale) && scale > 0.f)) return MOE_ERR_INVALID_ARGUMENT;
+  const float s = scale * cache->k_gscale;
+  if (!(s >= 0x1p-126f && s <= 0x1p100f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!valid_stride(T, q_stride, (int64_t)Hq * cache->head_dim)) return MOE_ERR_INVALID_ARGUMENT;
+  const int32_t G = Hq / cache->kv_heads;
+  if (!moe::kv_sparse_launchable(T, R, G, cache->kv_heads, top_k)) return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0 || (R == 0 && !fill)) return MOE_OK;
+  if (!out || !al16(out) || !al4(lse)) return MOE_ERR_INVALID_ARGUMENT;
+  if (R > 0 && (!q || !al16(q) || !selected || !al4(selected))) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  moe::KvSparseProblem p{};
+  p.a.cache = *cache;
+  p.a.q = q;
+  p.a.q_stride = q_stride;
+  p.a.T = T;
+  p.a.Hq = Hq;
+  p.a.G = G;
+  p.a.offsets = query_offsets;
+  p.a.lens = seq_lens;
+  p.a.R = R;
+  p.a.table = block_table;
+  p.a.width = table_width;
+  p.a.scale = s;
+  p.a.out = out;
+  p.a.lse = lse;
+  p.a.fill = fill;
+  p.selected = selected;
+  p.top_k = top_k;
+  return moe::launch_kv_sparse_attention(p, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace
@@ -181,6 +235,58 @@ moe_status_t moe_nvfp4_kv_append_rotary(const moe_nvfp4_kv_cache_t* cache, const
   if (moe_status_t st = check_arch(nullptr)) return st;
   const moe::RotaryProblem p{*rotary, q, q_stride, T, Hq, positions, position_stride, q_out, q_out_stride};
   return moe::launch_kv_append_rotary(*cache, p, k, v, k_stride, v_stride, slots, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t moe_nvfp4_kv_index_update(const moe_nvfp4_kv_cache_t* cache, const moe_nvfp4_kv_index_t* index,
+                                       const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                                       const int32_t* block_table, int32_t table_width, int32_t T, void* stream) {
+  if (!valid_cache(cache) || !valid_index(index)) return MOE_ERR_INVALID_ARGUMENT;
+  if (index->num_pages != cache->num_pages || index->page_size != cache->page_size ||
+      index->kv_heads != cache->kv_heads || index->head_dim != cache->head_dim)
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::KvStep s{query_offsets, seq_lens, block_table, R, T, table_width, cache->page_size};
+  if (!valid_step(s)) return MOE_ERR_INVALID_ARGUMENT;
+  if ((T / cache->page_size + 2 * (int64_t)R) * cache->kv_heads >= (int64_t)1 << 24) return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0 || R == 0 || table_width == 0) return MOE_OK;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  return moe::launch_kv_index_update(*cache, *index, s, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index, const uint16_t* q, int64_t q_stride, int32_t T,
+                                 int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
+                                 const int32_t* block_table, int32_t table_width, int32_t top_k, int32_t first,
+                                 int32_t last, int32_t* selected, void* stream) {
+  if (!valid_index(index)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::KvStep s{query_offsets, seq_lens, block_table, R, T, table_width, index->page_size};
+  if (!valid_step(s) || table_width > moe::kKvMaxSelectPages) return MOE_ERR_INVALID_ARGUMENT;
+  if (Hq < 1 || Hq % index->kv_heads != 0 || Hq / index->kv_heads > 64) return MOE_ERR_INVALID_ARGUMENT;
+  if (!valid_stride(T, q_stride, (int64_t)Hq * index->head_dim)) return MOE_ERR_INVALID_ARGUMENT;
+  if (top_k < 1 || top_k > moe::kKvMaxSelected || first < 0 || last < 1 || first > top_k || last > top_k - first)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((int64_t)T * index->kv_heads >= (int64_t)1 << 24) return MOE_ERR_INVALID_ARGUMENT;
+  if (T == 0) return MOE_OK;
+  if (!q || !al16(q) || !selected || !al4(selected)) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
+  const moe::KvSelectProblem p{*index, s, q, q_stride, Hq / index->kv_heads, top_k, first, last, selected};
+  return moe::launch_kv_select(p, static_cast<hipStream_t>(stream));
+}
+
+moe_status_t moe_nvfp4_kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride,
+                                           int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens,
+                                           int32_t R, const int32_t* block_table, int32_t table_width,
+                                           const int32_t* selected, int32_t top_k, float scale, uint16_t* out,
+                                           float* lse, void* stream) {
+  return kv_sparse_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, selected,
+                             top_k, scale, out, lse, false, stream);
+}
+
+moe_status_t moe_nvfp4_kv_sparse_attention_fill(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride,
+                                                int32_t T, int32_t Hq, const int32_t* query_offsets,
+                                                const int32_t* seq_lens, int32_t R, const int32_t* block_table,
+                                                int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
+                                                uint16_t* out, float* lse, void* stream) {
+  return kv_sparse_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, selected,
+                             top_k, scale, out, lse, true, stream);
 }
 
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim) {

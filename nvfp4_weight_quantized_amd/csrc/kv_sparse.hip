@@ -1,0 +1,408 @@
+// Attention of query rows over the pages chosen for them (kv_select), from the paged NVFP4 key/value cache.
+//
+// The mathematics, the operands and the softmax reference are those of kv_attention.hip: scores, maxima, sums and
+// outputs in fp32, keys and values exact in fp16, p rounded to fp16 for the value product.  What differs is which
+// units a row sees: those of the pages in its token's list for its kv head, up to its own position.
+#include "kv_operands.h"
+#include "kv_step.h"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------------------------ tiles
+// A workgroup takes a tile: the rows of one kv head of up to `tokens` consecutive tokens of a request, 16 * MI rows at
+// most (a token with more rows than that is cut into `parts`).  It goes through the union of its tokens' lists, a page
+// once for all of them, with a bit per token that says whose list holds the page: a unit's codes are turned into
+// operands once, which is most of the work, and the rows that do not see it are masked.  Where lists have nothing in
+// common this costs what tiles of one token would, since the columns of the matrix products would lie idle there.
+// Each of the NW waves takes every NW-th unit through an LDS ring of its own; their sums meet in LDS at the end.
+struct SparseTiles {
+  int tokens;      // per tile
+  int parts;       // tiles per token (tokens == 1)
+};
+
+constexpr int kEntries = kKvMaxSelected;      // of a tile's lists
+
+template <int D, int MI, int NW>
+__global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void kv_sparse_kernel(KvSparseProblem p,
+                                                                                               SparseTiles tiles) {
+  using U = KvUnit<D>;
+  constexpr int NS = D / 32, BM = 16 * MI, NL = NS / 2;
+  constexpr int kFull = U::kBytes / 1024, kTail = U::kBytes % 1024 / 256;   // 1024- and 256-byte loads of a unit
+  constexpr int kOut = NW * BM * 36 * 4, kRings = NW * kRing * U::kBytes;
+  // the lists; then the waves' rings; at the end one 32-element range of the sums (rows padded to 36 floats)
+  __shared__ __align__(16) uint8_t lds[kOut > kRings ? kOut : kRings];
+  static_assert(sizeof(lds) >= 4 * kEntries, "the lists lie where the rings will");
+  __shared__ float m_lds[NW][BM], l_lds[NW][BM];
+  __shared__ int entry_page[kEntries], entry_phys[kEntries];      // logical page, page of the cache (-1: bad)
+  __shared__ uint16_t entry_mask[kEntries];
+  __shared__ int chunk_count[kEntries / 64];
+  const KvAttentionProblem& a = p.a;
+  if (blockIdx.x >= a.work_groups) return kv_fill_rows<D>(a, blockIdx.x - a.work_groups, gridDim.x - a.work_groups);
+  using lds_bytes = __attribute__((address_space(3))) uint8_t*;
+  float(*o_lds)[BM][36] = reinterpret_cast<float(*)[BM][36]>(lds);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q4 = lane >> 4, n16 = lane & 15;
+  const int hkv = a.cache.kv_heads, ps = a.cache.page_size, upp = ps / kKvUnit;
+  const int h = blockIdx.x % hkv;
+  StepRequest rq;
+  int item;
+  {
+    const KvStep s{a.offsets, a.lens, a.table, a.R, a.T, a.width, ps};
+    if (!step_find(s, blockIdx.x / hkv, [&](const StepRequest& x) {
+          return (x.n + tiles.tokens - 1) / tiles.tokens * tiles.parts;
+        }, &rq, &item))
+      return;
+  }
+  const int part = item % tiles.parts, tok0 = item / tiles.parts * tiles.tokens;
+  const int toks = min(tiles.tokens, rq.n - tok0), g0 = part * BM;
+  const int rows = tiles.parts > 1 ? min(BM, a.G - g0) : toks * a.G;
+  const int pos0 = rq.len - rq.n + tok0, pos_last = pos0 + toks - 1;      // positions of the first and last token
+
+  // ---- the union of the lists
+  int entries = 0;
+  {
+    uint32_t* lists = reinterpret_cast<uint32_t*>(lds);
+    const int K = p.top_k, all = toks * K;
+    const int32_t* src = p.selected + ((size_t)(rq.row0 + tok0) * hkv + h) * K;
+    for (int i = tid; i < all; i += 64 * NW) {
+      const int t = i / K;
+      lists[i] = (uint32_t)src[(size_t)t * hkv * K + (i - t * K)];
+    }
+    __syncthreads();
+    const int32_t* table = a.table + (size_t)rq.r * a.width;
+    // entry i of the lists opens an entry of the union where no earlier token lists its page
+    auto look = [&](int i, uint32_t* mask) {
+      const int t = i / K, k = i - t * K;
+      const uint32_t b = lists[i];
+      *mask = 1u << t;
+      if ((int)b < 0 || (long long)b * ps > pos0 + t || (k > 0 && lists[i - 1] == b)) return false;
+      bool first = true;
+      for (int o = 0; o < toks; ++o) {
+        if (o == t) continue;
+        int lo = 0, hi = K;      // the first element of list o not below b
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (lists[o * K + mid] < b) lo = mid + 1;
+          else hi = mid;
+        }
+        // an earlier token that lists a page ahead of its own position does not see it
+        if (lo < K && lists[o * K + lo] == b && (long long)b * ps <= pos0 + o) {
+          *mask |= 1u << o;
+          first &= o > t;
+        }
+      }
+      return first;
+    };
+    for (int c = wave; c < (all + 63) / 64; c += NW) {
+      uint32_t mask;
+      const uint64_t opens = __ballot(64 * c + lane < all && look(64 * c + lane, &mask));
+      if (lane == 0) chunk_count[c] = __popcll(opens);
+    }
+    __syncthreads();
+    for (int c = 0; c < (all + 63) / 64; ++c) {
+      if (c % NW == wave) {
+        uint32_t mask = 0;
+        const bool open = 64 * c + lane < all && look(64 * c + lane, &mask);
+        const uint64_t opens = __ballot(open), below = lane == 0 ? 0 : ~0ull >> (64 - lane);
+        if (open) {
+          const int at = entries + __popcll(opens & below), b = (int)lists[64 * c + lane];
+          const int page = b < a.width ? table[b] : -1;
+          entry_page[at] = b;
+          entry_phys[at] = page >= 0 && page < a.cache.num_pages ? page : -1;
+          entry_mask[at] = (uint16_t)mask;
+        }
+      }
+      entries += chunk_count[c];
+    }
+    __syncthreads();      // the lists have been read
+  }
+  const int units = entries * upp, mine = units > wave ? (units - wave + NW - 1) / NW : 0;
+  const lds_bytes ring = (lds_bytes)lds + wave * kRing * U::kBytes;
+
+  // the wave's unit i is unit wave + NW * i of the union
+  auto issue = [&](int i, int slot) {
+    const int u = wave + NW * i, e = u / upp, page = __builtin_amdgcn_readfirstlane(entry_phys[e]);
+    const uint8_t* base = a.cache.pages;
+    if (page >= 0) base += (((uint64_t)page * hkv + h) * upp + (u - e * upp)) * (uint64_t)U::kBytes;
+    const uint32_t dst = (uint32_t)(uintptr_t)ring + slot * U::kBytes;
+#pragma unroll
+    for (int j = 0; j < kFull; ++j) direct_load16(base + 1024 * j, 16 * lane, dst + 1024 * j);
+#pragma unroll
+    for (int j = 0; j < kTail; ++j) direct_load4(base + 1024 * kFull + 256 * j, 4 * lane, dst + 1024 * kFull + 256 * j);
+  };
+  for (int i = 0; i < min(mine, kRing); ++i) issue(i, i);
+
+  // query operands: row n16 of block mi, elements [32s + 8*q4, +8)
+  f16x8 qf[MI][NS];
+  float c[MI];
+  int pos[MI], bit[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int row = 16 * mi + n16;
+    const bool valid = row < rows;
+    const int t = valid && tiles.parts == 1 ? row / a.G : 0, g = valid ? g0 + row - t * a.G : 0;
+    pos[mi] = valid ? pos0 + t : -1;
+    bit[mi] = t;
+    const uint16_t* src = a.q + (int64_t)(rq.row0 + tok0 + t) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * q4;
+    u32x4 w[NS];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      w[k] = *reinterpret_cast<const u32x4*>(src + 32 * k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[k][j] & 0x7FFFu, (w[k][j] >> 16) & 0x7FFFu));
+    }
+    int e = (int)(top >> 7);    // the row's largest exponent field
+    e = max(e, __shfl_xor(e, 16));
+    e = max(e, __shfl_xor(e, 32));
+    const int shift = row_shift(e, a.scale * kLog2e);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const f16x2 p0 = bf16x2_to_f16(w[k][0], shift), p1 = bf16x2_to_f16(w[k][1], shift);
+      const f16x2 p2 = bf16x2_to_f16(w[k][2], shift), p3 = bf16x2_to_f16(w[k][3], shift);
+      qf[mi][k] = f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    }
+    c[mi] = fminf(ldexpf(a.scale * kLog2e, -shift), FLT_MAX);      // a score of 0 stays 0
+  }
+
+  f32x4 o[MI][NS][2];
+  float m[MI], l[MI];
+  bool far[MI], any_far = false;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    far[mi] = false;
+    m[mi] = kNone;
+    l[mi] = 0.f;
+#pragma unroll
+    for (int r = 0; r < NS; ++r) o[mi][r][0] = o[mi][r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const int full = (1 << toks) - 1;
+
+  auto compute = [&](int i, int slot) {
+    const int u = wave + NW * i, e = u / upp;
+    const int key0 = __builtin_amdgcn_readfirstlane(entry_page[e]) * ps + (u - e * upp) * kKvUnit;
+    if (key0 > pos_last) return;
+    const int mask = __builtin_amdgcn_readfirstlane((int)entry_mask[e]);
+    const bool bad = __builtin_amdgcn_readfirstlane(entry_phys[e]) < 0;
+    const lds_bytes unit_lds = ring + slot * U::kBytes;
+    u32x4 kc[NL];
+    uint32_t ks[NS / 2];      // 2*NS scale bytes: word w = block*NS + step
+#pragma unroll
+    for (int j = 0; j < NL; ++j)
+      kc[j] = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(unit_lds + 1024 * j + 16 * lane);
+#pragma unroll
+    for (int j = 0; j < NS / 2; ++j)
+      ks[j] = *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(
+          unit_lds + U::kKScales + (16 * (q4 >> 1) + n16) * 2 * NS + 4 * j);
+    f32x4 sc[MI][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) sc[mi][kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        const int w = kb * NS + k;
+        const f16x2 sp = scale_pair(ks[w >> 2], (w & 2) != 0);
+        const f16x8 kf = k_operand(kc[w >> 2][w & 3], (w & 1) ? sp[1] : sp[0]);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+          sc[mi][kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mi][k], sc[mi][kb], 0, 0, 0);
+      }
+    }
+    // units that some row does not see whole: masks, and nothing from positions past the length
+    if (mask != full || key0 + kKvUnit - 1 > pos0 || bad) {
+      const int quarter = 4 * (lane_now() >> 4);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const int reach = (mask >> bit[mi]) & 1 ? pos[mi] : -1;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const bool seen = key0 + 16 * kb + quarter + k <= reach;
+            sc[mi][kb][k] = !seen ? -INFINITY : bad ? NAN : sc[mi][kb][k];
+          }
+      }
+      if (key0 + kKvUnit > rq.len || bad) {
+        // value scales of positions past the length to zero, in the ring
+        const u32x2 keep = {bad ? 0u : keep_bytes(key0 + quarter, rq.len),
+                            bad ? 0u : keep_bytes(key0 + 16 + quarter, rq.len)};
+        const int half = (lane_now() & 15) >> 3;
+#pragma unroll
+        for (int r = 0; r < NS; ++r) {
+          auto* vs = reinterpret_cast<__attribute__((address_space(3))) u32x2*>(
+              unit_lds + U::kVScales + ((quarter / 2 + half) * NS + r) * 8);
+          *vs &= keep;      // the eight lanes that share the bytes write the same
+        }
+      }
+    }
+    f16x8 pf[MI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      float t[8];
+      auto exponents = [&]() {
+        const float ref = m[mi] - kPExp;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(sc[mi][k >> 2][k & 3], c[mi], -ref);
+        if (__builtin_expect(any_far, 0)) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            t[k] = far[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
+        }
+      };
+      exponents();
+      const float most =
+          fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+      if (__any(most > kSlack + kPExp)) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sc[mi][k >> 2][k & 3]);
+        const float f = kv_move(quarter_max(mx), c[mi], m[mi], far[mi]);
+        any_far |= __any(far[mi]);
+        l[mi] *= f;
+#pragma unroll
+        for (int r = 0; r < NS; ++r)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[mi][r][x][k] *= f;
+        exponents();
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = exp2_hw(t[k]);
+      l[mi] += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const f16x2 pr = __builtin_convertvector((f32x2){t[k], t[4 + k]}, f16x2);      // the order of v_octet
+        pf[mi][2 * k] = pr[0];
+        pf[mi][2 * k + 1] = pr[1];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+      const u32x2 vc = *reinterpret_cast<const __attribute__((address_space(3))) u32x2*>(
+          unit_lds + U::kVCodes + 1024 * (r >> 1) + 16 * lane + 8 * (r & 1));
+      const u32x2 vs = *reinterpret_cast<const __attribute__((address_space(3))) u32x2*>(
+          unit_lds + U::kVScales + ((2 * q4 + (n16 >> 3)) * NS + r) * 8);
+      f16x8 ve, vo;
+      v_octet(vc[0], vc[1], vs[0], vs[1], &ve, &vo);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        o[mi][r][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ve, pf[mi], o[mi][r][0], 0, 0, 0);
+        o[mi][r][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo, pf[mi], o[mi][r][1], 0, 0, 0);
+      }
+    }
+  };
+
+  for (int i = 0, slot = 0; i < mine; ++i) {
+    wait_units<kFull + kTail>(min(kRing, mine - i) - 1);
+    compute(i, slot);
+    if (i + kRing < mine) {
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the slot has been read
+      issue(i + kRing, slot);
+    }
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+  }
+
+  // the waves' sums: common reference maximum per row, then range by range through LDS
+  __syncthreads();      // every wave has read its ring
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const float ls = quarter_sum(l[mi]);
+    m[mi] = kv_reference(m[mi], c[mi], far[mi]);
+    if (q4 == 0) {
+      m_lds[wave][16 * mi + n16] = m[mi];
+      l_lds[wave][16 * mi + n16] = ls;
+    }
+  }
+  __syncthreads();
+  float f[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int rr = 16 * mi + n16;
+    float top = m_lds[0][rr];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) top = fmaxf(top, m_lds[w][rr]);
+    f[mi] = exp2_hw(m[mi] - top);
+  }
+  // of the first 256 threads: thread -> row tid / (256 / BM), consecutive elements of the range
+  constexpr int TPR = 256 / BM, EPT = 32 / TPR;
+  const int orow = (tid & 255) / TPR, oc = (tid % TPR) * EPT;
+  float top = kNone, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) top = fmaxf(top, m_lds[w][orow]);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) sum += l_lds[w][orow] * exp2_hw(m_lds[w][orow] - top);
+  const bool valid = orow < rows && tid < 256, any = sum > 0.f || sum != sum;
+  const int t = tiles.parts == 1 ? orow / a.G : 0, g = g0 + orow - t * a.G;
+  const size_t dst_row = (size_t)(rq.row0 + tok0 + t) * a.Hq + h * a.G + g;
+  const float norm = any ? a.cache.v_gscale / sum : 0.f;
+  if (tid % TPR == 0 && valid && a.lse)
+    a.lse[dst_row] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+#pragma unroll
+  for (int r = 0; r < NS; ++r) {
+    if (r > 0) __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      float* dst = &o_lds[wave][16 * mi + n16][8 * q4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dst[2 * k] = o[mi][r][0][k] * f[mi];
+        dst[2 * k + 1] = o[mi][r][1][k] * f[mi];
+      }
+    }
+    __syncthreads();
+    float v[EPT];
+#pragma unroll
+    for (int x = 0; x < EPT; ++x) v[x] = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; w += 2)
+#pragma unroll
+      for (int x = 0; x < EPT; ++x) v[x] += o_lds[w][orow][oc + x] + o_lds[w + 1][orow][oc + x];
+    if (valid) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + dst_row * D + 32 * r + oc);
+#pragma unroll
+      for (int x = 0; x < EPT / 2; ++x) dst[x] = f32x2_to_bf16x2(v[2 * x] * norm, v[2 * x + 1] * norm);
+    }
+  }
+}
+
+// Tiles of a call, and a bound on their number over all heads.
+SparseTiles sparse_tiles(int32_t G, int32_t top_k) {
+  const int rows = G > 16 ? 32 : 16;
+  SparseTiles t;
+  t.tokens = std::max(1, std::min(rows / G, kEntries / top_k));
+  t.parts = (G + rows - 1) / rows;
+  return t;
+}
+
+int64_t sparse_grid(const SparseTiles& t, int32_t T, int32_t R, int32_t hkv) {
+  return std::min((int64_t)T, (int64_t)T / t.tokens + std::min(T, R)) * t.parts * hkv;
+}
+
+}  // namespace
+
+bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t top_k) {
+  return (sparse_grid(sparse_tiles(G, top_k), T, R, hkv) + 256) * 256 < (int64_t)1 << 32;
+}
+
+moe_status_t launch_kv_sparse_attention(const KvSparseProblem& problem, hipStream_t stream) {
+  KvSparseProblem p = problem;
+  KvAttentionProblem& a = p.a;
+  const int64_t fill = a.fill ? std::min(((int64_t)a.T + 3) / 4, (int64_t)256) : 0;
+  const SparseTiles t = sparse_tiles(a.G, p.top_k);
+  const int64_t grid = a.R == 0 ? 0 : sparse_grid(t, a.T, a.R, a.cache.kv_heads);
+  a.work_groups = (uint32_t)grid;
+  with_head_dim(a.cache.head_dim, [&](auto tag) {
+    constexpr int D = decltype(tag)::value;
+    const dim3 blocks((unsigned)(grid + fill));
+    if (a.G <= 16)
+      hipLaunchKernelGGL((kv_sparse_kernel<D, 1, 4>), blocks, dim3(256), 0, stream, p, t);
+    else
+      hipLaunchKernelGGL((kv_sparse_kernel<D, 2, 4>), blocks, dim3(256), 0, stream, p, t);
+  });
+  return launch_status();
+}
+
+}  // namespace moe
