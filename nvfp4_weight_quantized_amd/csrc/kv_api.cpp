@@ -263,7 +263,7 @@ moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index, const uint16
   if (!valid_stride(T, q_stride, (int64_t)Hq * index->head_dim)) return MOE_ERR_INVALID_ARGUMENT;
   if (top_k < 1 || top_k > moe::kKvMaxSelected || first < 0 || last < 1 || first > top_k || last > top_k - first)
     return MOE_ERR_INVALID_ARGUMENT;
-  if ((int64_t)T * index->kv_heads >= (int64_t)1 << 24) return MOE_ERR_INVALID_ARGUMENT;
+  if ((int64_t)T * index->kv_heads > (int64_t)1 << 21) return MOE_ERR_INVALID_ARGUMENT;      // of 1024 threads each
   if (T == 0) return MOE_OK;
   if (!q || !al16(q) || !selected || !al4(selected)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;
