@@ -610,18 +610,24 @@ moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index /* host */, c
  * table, makes the row NaN.  A row that sees nothing gets zeros and lse = -inf.  Lists in another order give
  * unspecified rows of their token and of the tokens around it, and nothing else.
  * Limits: those of moe_nvfp4_kv_attention, 1 <= top_k <= 1024, and the launch holds fewer than 2^32 work-items (T * Hq <=
- * 2^23 always does).  out and lse overlap no input.  No workspace. */
+ * 2^23 always does).  out and lse overlap no input.
+ * workspace: moe_nvfp4_kv_sparse_attention_workspace_size bytes, 16-byte aligned (0: NULL), else
+ * MOE_ERR_WORKSPACE_TOO_SMALL. */
+size_t moe_nvfp4_kv_sparse_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads,
+                                                    int32_t head_dim, int32_t page_size, int32_t top_k);
 moe_status_t moe_nvfp4_kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q,
                                            int64_t q_stride, int32_t T, int32_t Hq, const int32_t* query_offsets,
                                            const int32_t* seq_lens, int32_t R, const int32_t* block_table,
                                            int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
-                                           uint16_t* out, float* lse, void* stream);
+                                           uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                           void* stream);
 /* The same for out and lse without content yet: rows outside every request get zeros and lse = -inf. */
 moe_status_t moe_nvfp4_kv_sparse_attention_fill(const moe_nvfp4_kv_cache_t* cache /* host */, const uint16_t* q,
                                                 int64_t q_stride, int32_t T, int32_t Hq, const int32_t* query_offsets,
                                                 const int32_t* seq_lens, int32_t R, const int32_t* block_table,
                                                 int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
-                                                uint16_t* out, float* lse, void* stream);
+                                                uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                                void* stream);
 
 /* ---------------------------------------------------------------- rotary positions
  * Queries and keys turned by their positions before the attention.  Pair i of a head, i < pairs, turns by the angle

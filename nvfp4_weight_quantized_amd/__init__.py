@@ -11,7 +11,8 @@ from .ops import (NvFp4Experts, NvFp4MoELayer, combine, forward, forward_workspa
                   grouped_gemm, grouped_gemm_w4a4, pack_tiles, permute, quantize, quantize_act_nv, route,
                   route_from_logits, validate_forward, workspace_for)
 from .kv import (KvPlan, NvFp4KvCache, kv_append, kv_attention, kv_attention_workspace_size, kv_gather, kv_plan)
-from .kv_sparse import NvFp4KvIndex, kv_index_update, kv_select, kv_sparse_attention
+from .kv_sparse import (NvFp4KvIndex, kv_index_update, kv_select, kv_sparse_attention,
+                        kv_sparse_attention_workspace_size)
 from .positions import Rotary, kv_append_rotary, rotary
 from .workloads import build_bank, build_layer
 
@@ -20,4 +21,5 @@ __all__ = ["synth", "LIB_PATH", "MoeError", "NvFp4Experts", "NvFp4MoELayer", "co
            "permute", "quantize", "quantize_act_nv", "route", "route_from_logits", "validate_forward",
            "workspace_for", "KvPlan", "NvFp4KvCache", "kv_append", "kv_attention", "kv_attention_workspace_size",
            "kv_gather", "kv_plan", "NvFp4KvIndex", "kv_index_update", "kv_select", "kv_sparse_attention",
+           "kv_sparse_attention_workspace_size",
            "Rotary", "kv_append_rotary", "rotary", "build_bank", "build_layer"]

@@ -139,7 +139,8 @@ SIGNATURES = {
 SIGNATURES["moe_nvfp4_kv_attention_fill"] = SIGNATURES["moe_nvfp4_kv_attention"]
 SIGNATURES["moe_nvfp4_kv_sparse_attention"] = SIGNATURES["moe_nvfp4_kv_sparse_attention_fill"] = (
     i32, [ctypes.POINTER(KvCache), c_void_p, i64, i32, i32, c_void_p, c_void_p, i32, c_void_p, i32, c_void_p, i32,
-          ctypes.c_float, c_void_p, c_void_p, c_void_p])
+          ctypes.c_float, c_void_p, c_void_p, c_void_p, size_t, c_void_p])
+SIGNATURES["moe_nvfp4_kv_sparse_attention_workspace_size"] = (size_t, [i32, i32, i32, i32, i32, i32, i32])
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 

@@ -368,7 +368,10 @@ struct KvSparseProblem {
   const int32_t* selected;  // [T][kv_heads][top_k]
   int32_t top_k;
 };
-bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t kv_heads, int32_t top_k);
-moe_status_t launch_kv_sparse_attention(const KvSparseProblem& p, hipStream_t stream);
+bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                          int32_t top_k);
+size_t kv_sparse_workspace(int32_t T, int32_t R, int32_t G, int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                           int32_t top_k);
+moe_status_t launch_kv_sparse_attention(const KvSparseProblem& p, void* workspace, hipStream_t stream);
 
 }  // namespace moe

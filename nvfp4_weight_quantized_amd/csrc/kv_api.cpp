@@ -114,7 +114,8 @@ moe_status_t kv_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, 
 moe_status_t kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride, int32_t T,
                                  int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
                                  const int32_t* block_table, int32_t table_width, const int32_t* selected,
-                                 int32_t top_k, float scale, uint16_t* out, float* lse, bool fill, void* stream) {
+                                 int32_t top_k, float scale, uint16_t* out, float* lse, bool fill,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_cache(cache)) return MOE_ERR_INVALID_ARGUMENT;
   const moe::KvStep step{query_offsets, seq_lens, block_table, R, T, table_width, cache->page_size};
   if (!valid_step(step)) return MOE_ERR_INVALID_ARGUMENT;
@@ -126,10 +127,14 @@ moe_status_t kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16
   if (!(s >= 0x1p-126f && s <= 0x1p100f)) return MOE_ERR_INVALID_ARGUMENT;
   if (!valid_stride(T, q_stride, (int64_t)Hq * cache->head_dim)) return MOE_ERR_INVALID_ARGUMENT;
   const int32_t G = Hq / cache->kv_heads;
-  if (!moe::kv_sparse_launchable(T, R, G, cache->kv_heads, top_k)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!moe::kv_sparse_launchable(T, R, G, cache->kv_heads, cache->head_dim, cache->page_size, top_k))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (T == 0 || (R == 0 && !fill)) return MOE_OK;
   if (!out || !al16(out) || !al4(lse)) return MOE_ERR_INVALID_ARGUMENT;
   if (R > 0 && (!q || !al16(q) || !selected || !al4(selected))) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t need = moe::kv_sparse_workspace(T, R, G, cache->kv_heads, cache->head_dim, cache->page_size, top_k);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && !al16(workspace)) return MOE_ERR_INVALID_ARGUMENT;
   if (moe_status_t st = check_arch(nullptr)) return st;
   moe::KvSparseProblem p{};
   p.a.cache = *cache;
@@ -149,7 +154,7 @@ moe_status_t kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16
   p.a.fill = fill;
   p.selected = selected;
   p.top_k = top_k;
-  return moe::launch_kv_sparse_attention(p, static_cast<hipStream_t>(stream));
+  return moe::launch_kv_sparse_attention(p, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace
@@ -271,22 +276,32 @@ moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index, const uint16
   return moe::launch_kv_select(p, static_cast<hipStream_t>(stream));
 }
 
+size_t moe_nvfp4_kv_sparse_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads,
+                                                    int32_t head_dim, int32_t page_size, int32_t top_k) {
+  if (T < 0 || R < 0 || R > moe::kKvMaxRequests || Hq < 1 || kv_heads < 1 || Hq % kv_heads != 0 || Hq / kv_heads > 64 ||
+      (int64_t)T * Hq >= ((int64_t)1 << 31) || top_k < 1 || top_k > moe::kKvMaxSelected ||
+      !valid_cache_dims(1, page_size, kv_heads, head_dim))
+    return 0;
+  return moe::kv_sparse_workspace(T, R, Hq / kv_heads, kv_heads, head_dim, page_size, top_k);
+}
+
 moe_status_t moe_nvfp4_kv_sparse_attention(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride,
                                            int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens,
                                            int32_t R, const int32_t* block_table, int32_t table_width,
                                            const int32_t* selected, int32_t top_k, float scale, uint16_t* out,
-                                           float* lse, void* stream) {
+                                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   return kv_sparse_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, selected,
-                             top_k, scale, out, lse, false, stream);
+                             top_k, scale, out, lse, false, workspace, workspace_bytes, stream);
 }
 
 moe_status_t moe_nvfp4_kv_sparse_attention_fill(const moe_nvfp4_kv_cache_t* cache, const uint16_t* q, int64_t q_stride,
                                                 int32_t T, int32_t Hq, const int32_t* query_offsets,
                                                 const int32_t* seq_lens, int32_t R, const int32_t* block_table,
                                                 int32_t table_width, const int32_t* selected, int32_t top_k, float scale,
-                                                uint16_t* out, float* lse, void* stream) {
+                                                uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                                void* stream) {
   return kv_sparse_attention(cache, q, q_stride, T, Hq, query_offsets, seq_lens, R, block_table, table_width, selected,
-                             top_k, scale, out, lse, true, stream);
+                             top_k, scale, out, lse, true, workspace, workspace_bytes, stream);
 }
 
 size_t moe_nvfp4_kv_attention_workspace_size(int32_t T, int32_t R, int32_t Hq, int32_t kv_heads, int32_t head_dim) {

@@ -16,12 +16,30 @@ namespace {
 // operands once, which is most of the work, and the rows that do not see it are masked.  Where lists have nothing in
 // common this costs what tiles of one token would, since the columns of the matrix products would lie idle there.
 // Each of the NW waves takes every NW-th unit through an LDS ring of its own; their sums meet in LDS at the end.
+// Few tiles with long lists are cut into splits of their units, whose partial sums a second launch joins.
 struct SparseTiles {
   int tokens;      // per tile
   int parts;       // tiles per token (tokens == 1)
+  int splits;      // of a tile's units
+  int bm;          // rows of a tile
+  float* o;        // partial sums [tile][split][bm][D], unnormalised
+  float* ml;       // [tile][split][2][bm]: reference maximum, sum
 };
 
 constexpr int kEntries = kKvMaxSelected;      // of a tile's lists
+
+// The tile `index` (over requests, tokens and parts) of the step: its request, first token and part.
+__device__ __forceinline__ bool sparse_find(const KvAttentionProblem& a, const SparseTiles& tiles, int index,
+                                            StepRequest* rq, int* tok0, int* part) {
+  const KvStep s{a.offsets, a.lens, a.table, a.R, a.T, a.width, a.cache.page_size};
+  int item;
+  if (!step_find(s, index, [&](const StepRequest& x) { return (x.n + tiles.tokens - 1) / tiles.tokens * tiles.parts; },
+                 rq, &item))
+    return false;
+  *part = item % tiles.parts;
+  *tok0 = item / tiles.parts * tiles.tokens;
+  return true;
+}
 
 template <int D, int MI, int NW>
 __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void kv_sparse_kernel(KvSparseProblem p,
@@ -34,8 +52,8 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
   __shared__ __align__(16) uint8_t lds[kOut > kRings ? kOut : kRings];
   static_assert(sizeof(lds) >= 4 * kEntries, "the lists lie where the rings will");
   __shared__ float m_lds[NW][BM], l_lds[NW][BM];
-  __shared__ int entry_page[kEntries], entry_phys[kEntries];      // logical page, page of the cache (-1: bad)
-  __shared__ uint16_t entry_mask[kEntries];
+  // logical page and page of the cache (-1: bad) of each entry, then the tokens that list it
+  extern __shared__ __align__(16) int entry[];
   __shared__ int chunk_count[kEntries / 64];
   const KvAttentionProblem& a = p.a;
   if (blockIdx.x >= a.work_groups) return kv_fill_rows<D>(a, blockIdx.x - a.work_groups, gridDim.x - a.work_groups);
@@ -44,18 +62,14 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q4 = lane >> 4, n16 = lane & 15;
   const int hkv = a.cache.kv_heads, ps = a.cache.page_size, upp = ps / kKvUnit;
-  const int h = blockIdx.x % hkv;
+  const int h = blockIdx.x % hkv, split = blockIdx.x / hkv % tiles.splits, tile = blockIdx.x / hkv / tiles.splits;
   StepRequest rq;
-  int item;
-  {
-    const KvStep s{a.offsets, a.lens, a.table, a.R, a.T, a.width, ps};
-    if (!step_find(s, blockIdx.x / hkv, [&](const StepRequest& x) {
-          return (x.n + tiles.tokens - 1) / tiles.tokens * tiles.parts;
-        }, &rq, &item))
-      return;
-  }
-  const int part = item % tiles.parts, tok0 = item / tiles.parts * tiles.tokens;
-  const int toks = min(tiles.tokens, rq.n - tok0), g0 = part * BM;
+  int tok0, part;
+  if (!sparse_find(a, tiles, tile, &rq, &tok0, &part)) return;
+  const int toks = min(tiles.tokens, rq.n - tok0), g0 = part * BM, most = tiles.tokens * p.top_k;
+  int* const entry_page = entry;
+  int* const entry_phys = entry + most;
+  uint16_t* const entry_mask = reinterpret_cast<uint16_t*>(entry + 2 * most);
   const int rows = tiles.parts > 1 ? min(BM, a.G - g0) : toks * a.G;
   const int pos0 = rq.len - rq.n + tok0, pos_last = pos0 + toks - 1;      // positions of the first and last token
 
@@ -117,12 +131,15 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
     }
     __syncthreads();      // the lists have been read
   }
-  const int units = entries * upp, mine = units > wave ? (units - wave + NW - 1) / NW : 0;
+  // this split's units of the union, a whole number of rounds of the waves
+  const int all_units = entries * upp, per = ((all_units + tiles.splits - 1) / tiles.splits + NW - 1) / NW * NW;
+  const int u0 = min(split * per, all_units), units = min(all_units - u0, per);
+  const int mine = units > wave ? (units - wave + NW - 1) / NW : 0;
   const lds_bytes ring = (lds_bytes)lds + wave * kRing * U::kBytes;
 
-  // the wave's unit i is unit wave + NW * i of the union
+  // the wave's unit i is unit u0 + wave + NW * i of the union
   auto issue = [&](int i, int slot) {
-    const int u = wave + NW * i, e = u / upp, page = __builtin_amdgcn_readfirstlane(entry_phys[e]);
+    const int u = u0 + wave + NW * i, e = u / upp, page = __builtin_amdgcn_readfirstlane(entry_phys[e]);
     const uint8_t* base = a.cache.pages;
     if (page >= 0) base += (((uint64_t)page * hkv + h) * upp + (u - e * upp)) * (uint64_t)U::kBytes;
     const uint32_t dst = (uint32_t)(uintptr_t)ring + slot * U::kBytes;
@@ -180,7 +197,7 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
   const int full = (1 << toks) - 1;
 
   auto compute = [&](int i, int slot) {
-    const int u = wave + NW * i, e = u / upp;
+    const int u = u0 + wave + NW * i, e = u / upp;
     const int key0 = __builtin_amdgcn_readfirstlane(entry_page[e]) * ps + (u - e * upp) * kKvUnit;
     if (key0 > pos_last) return;
     const int mask = __builtin_amdgcn_readfirstlane((int)entry_mask[e]);
@@ -338,8 +355,17 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
   const int t = tiles.parts == 1 ? orow / a.G : 0, g = g0 + orow - t * a.G;
   const size_t dst_row = (size_t)(rq.row0 + tok0 + t) * a.Hq + h * a.G + g;
   const float norm = any ? a.cache.v_gscale / sum : 0.f;
-  if (tid % TPR == 0 && valid && a.lse)
-    a.lse[dst_row] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+  const size_t slot = ((size_t)tile * hkv + h) * tiles.splits + split;
+  const bool whole = tiles.splits == 1;
+  if (tid % TPR == 0 && valid) {
+    if (!whole) {
+      tiles.ml[slot * 2 * BM + orow] = top;
+      tiles.ml[slot * 2 * BM + BM + orow] = sum;
+    } else if (a.lse) {
+      a.lse[dst_row] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
+    }
+  }
+  if (!whole && units == 0) return;      // the join does not read the outputs of an empty split
 #pragma unroll
   for (int r = 0; r < NS; ++r) {
     if (r > 0) __syncthreads();
@@ -360,47 +386,139 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
     for (int w = 0; w < NW; w += 2)
 #pragma unroll
       for (int x = 0; x < EPT; ++x) v[x] += o_lds[w][orow][oc + x] + o_lds[w + 1][orow][oc + x];
-    if (valid) {
+    if (valid && whole) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + dst_row * D + 32 * r + oc);
 #pragma unroll
       for (int x = 0; x < EPT / 2; ++x) dst[x] = f32x2_to_bf16x2(v[2 * x] * norm, v[2 * x + 1] * norm);
+    } else if (valid) {
+      float* dst = tiles.o + (slot * BM + orow) * D + 32 * r + oc;
+#pragma unroll
+      for (int x = 0; x < EPT; ++x) dst[x] = v[x];
     }
   }
 }
 
-// Tiles of a call, and a bound on their number over all heads.
-SparseTiles sparse_tiles(int32_t G, int32_t top_k) {
-  const int rows = G > 16 ? 32 : 16;
-  SparseTiles t;
-  t.tokens = std::max(1, std::min(rows / G, kEntries / top_k));
-  t.parts = (G + rows - 1) / rows;
-  return t;
+// The splits of a tile joined, a wave per row: the splits' weights from their references and sums, one lane per split,
+// then the outputs, four elements per lane and 256 / D splits at once.
+template <int D>
+__global__ __launch_bounds__(256) void kv_sparse_join_kernel(KvSparseProblem p, SparseTiles tiles) {
+  constexpr int LPR = D / 4, PER = 64 / LPR, kAhead = 4;
+  const KvAttentionProblem& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, hkv = a.cache.kv_heads;
+  const int h = blockIdx.x % hkv, tile = blockIdx.x / hkv, row = 4 * blockIdx.y + wave, S = tiles.splits;
+  StepRequest rq;
+  int tok0, part;
+  if (!sparse_find(a, tiles, tile, &rq, &tok0, &part)) return;
+  const int toks = min(tiles.tokens, rq.n - tok0), g0 = part * tiles.bm;
+  if (row >= (tiles.parts > 1 ? min(tiles.bm, a.G - g0) : toks * a.G)) return;
+  const size_t slot0 = ((size_t)tile * hkv + h) * S;
+  const int sub = lane / LPR, d0 = 4 * (lane % LPR);
+  float top = kNone, sum = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < S; i0 += 64) {
+    float mi = kNone, li = 0.f;
+    if (i0 + lane < S) {
+      const float* ml = tiles.ml + (slot0 + i0 + lane) * 2 * tiles.bm + row;
+      mi = ml[0];
+      li = ml[tiles.bm];
+    }
+    float most = fmaxf(mi, top);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
+    const float f = exp2_hw(top - most), w = li != 0.f ? exp2_hw(mi - most) : 0.f;
+    top = most;
+    sum = sum * f + w * li;
+    v *= f;
+    const int n = min(64, S - i0);
+    for (int j = 0; j < n; j += kAhead * PER) {
+      f32x4 x[kAhead];
+      float wk[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = j + k * PER + sub;
+        wk[k] = __shfl(w, min(i, 63));
+        x[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i >= n) wk[k] = 0.f;
+        if (wk[k] != 0.f) x[k] = *reinterpret_cast<const f32x4*>(tiles.o + ((slot0 + i0 + i) * tiles.bm + row) * D + d0);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) v += wk[k] * x[k];
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off);
+#pragma unroll
+  for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], off);
+  const bool any = sum > 0.f || sum != sum;
+  const float norm = any ? a.cache.v_gscale / sum : 0.f;
+  const int t = tiles.parts == 1 ? row / a.G : 0, g = g0 + row - t * a.G;
+  const size_t dst = (size_t)(rq.row0 + tok0 + t) * a.Hq + h * a.G + g;
+  if (sub == 0)
+    *reinterpret_cast<u32x2*>(a.out + dst * D + d0) =
+        u32x2{f32x2_to_bf16x2(v[0] * norm, v[1] * norm), f32x2_to_bf16x2(v[2] * norm, v[3] * norm)};
+  if (a.lse && lane == 0) a.lse[dst] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
 }
 
-int64_t sparse_grid(const SparseTiles& t, int32_t T, int32_t R, int32_t hkv) {
-  return std::min((int64_t)T, (int64_t)T / t.tokens + std::min(T, R)) * t.parts * hkv;
+constexpr int kPlaces = 512;      // workgroups of four waves that splits aim at
+
+// Tiles of a call.  A token per tile while that leaves the card unfilled, else as many as the rows hold.
+struct SparsePlan {
+  SparseTiles t;
+  int64_t tiles;      // bound on their number, over requests, tokens and parts
+  size_t o_bytes, bytes;
+};
+
+SparsePlan sparse_plan(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
+  SparsePlan p{};
+  p.t.bm = G > 16 ? 32 : 16;
+  p.t.parts = (G + p.t.bm - 1) / p.t.bm;
+  p.t.tokens = (int64_t)T * hkv * p.t.parts <= kPlaces ? 1 : std::max(1, std::min(p.t.bm / G, kEntries / top_k));
+  p.tiles = std::min((int64_t)T, (int64_t)T / p.t.tokens + std::min(T, R)) * p.t.parts;
+  const int64_t most = (int64_t)p.t.tokens * top_k * (page_size / kKvUnit), grid = std::max(p.tiles * hkv, (int64_t)1);
+  p.t.splits = 1;
+  if (most > 64 && grid * 2 <= kPlaces) p.t.splits = (int)std::min(kPlaces / grid, (most + 3) / 4);
+  if (p.t.splits > 1) {
+    p.o_bytes = (size_t)grid * p.t.splits * p.t.bm * D * 4;
+    p.bytes = p.o_bytes + (size_t)grid * p.t.splits * 2 * p.t.bm * 4;
+  }
+  return p;
 }
 
 }  // namespace
 
-bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t top_k) {
-  return (sparse_grid(sparse_tiles(G, top_k), T, R, hkv) + 256) * 256 < (int64_t)1 << 32;
+bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
+  const SparsePlan p = sparse_plan(T, R, G, hkv, D, page_size, top_k);
+  return (p.tiles * hkv * p.t.splits + 256) * 256 < (int64_t)1 << 32;
 }
 
-moe_status_t launch_kv_sparse_attention(const KvSparseProblem& problem, hipStream_t stream) {
+size_t kv_sparse_workspace(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
+  return T == 0 || R == 0 ? 0 : sparse_plan(T, R, G, hkv, D, page_size, top_k).bytes;
+}
+
+moe_status_t launch_kv_sparse_attention(const KvSparseProblem& problem, void* workspace, hipStream_t stream) {
   KvSparseProblem p = problem;
   KvAttentionProblem& a = p.a;
+  const int hkv = a.cache.kv_heads;
   const int64_t fill = a.fill ? std::min(((int64_t)a.T + 3) / 4, (int64_t)256) : 0;
-  const SparseTiles t = sparse_tiles(a.G, p.top_k);
-  const int64_t grid = a.R == 0 ? 0 : sparse_grid(t, a.T, a.R, a.cache.kv_heads);
+  SparsePlan plan = sparse_plan(a.T, a.R, a.G, hkv, a.cache.head_dim, a.cache.page_size, p.top_k);
+  SparseTiles& t = plan.t;
+  t.o = static_cast<float*>(workspace);
+  t.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
+  const int64_t grid = a.R == 0 ? 0 : plan.tiles * hkv * t.splits;
   a.work_groups = (uint32_t)grid;
+  const size_t lds = (size_t)t.tokens * p.top_k * 10;
   with_head_dim(a.cache.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     const dim3 blocks((unsigned)(grid + fill));
-    if (a.G <= 16)
-      hipLaunchKernelGGL((kv_sparse_kernel<D, 1, 4>), blocks, dim3(256), 0, stream, p, t);
+    if (t.bm == 16)
+      hipLaunchKernelGGL((kv_sparse_kernel<D, 1, 4>), blocks, dim3(256), lds, stream, p, t);
     else
-      hipLaunchKernelGGL((kv_sparse_kernel<D, 2, 4>), blocks, dim3(256), 0, stream, p, t);
+      hipLaunchKernelGGL((kv_sparse_kernel<D, 2, 4>), blocks, dim3(256), lds, stream, p, t);
+    if (t.splits > 1 && grid > 0)
+      hipLaunchKernelGGL(kv_sparse_join_kernel<D>, dim3((unsigned)(plan.tiles * hkv), t.bm / 4), dim3(256), 0, stream,
+                         p, t);
   });
   return launch_status();
 }

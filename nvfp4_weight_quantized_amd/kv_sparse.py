@@ -146,15 +146,23 @@ def kv_select(index: NvFp4KvIndex, q: torch.Tensor, query_offsets: torch.Tensor,
     return selected
 
 
+def kv_sparse_attention_workspace_size(T: int, R: int, heads: int, kv_heads: int, head_dim: int, page_size: int,
+                                       top_k: int) -> int:
+    """Workspace bytes of ``kv_sparse_attention`` for T query rows of R requests."""
+    return int(L.lib().moe_nvfp4_kv_sparse_attention_workspace_size(T, R, heads, kv_heads, head_dim, page_size, top_k))
+
+
 def kv_sparse_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: torch.Tensor, seq_lens: torch.Tensor,
                         block_table: torch.Tensor, selected: torch.Tensor, scale: Optional[float] = None,
-                        return_lse: bool = False, out: Optional[torch.Tensor] = None):
+                        return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
     """``kv_attention`` (without a window) over the pages in ``selected`` only -> bf16 [T, heads, head_dim].
 
     ``selected`` int32 [T, kv_heads, top_k]: the columns of the block table that each token's rows of a kv head read, in
     ascending order, negative ones behind them (as ``kv_select`` returns them).  A page listed twice counts once; of the
     row's own page the positions up to its own are seen, pages behind it not at all.  A row that sees nothing gets zeros
-    and an ``lse`` of -inf.  Everything else is as for ``kv_attention``; there is no workspace.
+    and an ``lse`` of -inf.  Everything else is as for ``kv_attention``, ``workspace`` included
+    (``kv_sparse_attention_workspace_size`` bytes; none is needed for steps of many rows).
     """
     c, dev = cache._struct, cache._dev
     dim, kv_heads = c.head_dim, c.kv_heads
@@ -183,10 +191,18 @@ def kv_sparse_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: tor
         _same_device(cache._pages, ("out", out))
         if return_lse:
             lse = torch.full((t, heads), -math.inf, dtype=torch.float32, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+        _same_device(cache._pages, ("workspace", workspace))
+    else:
+        need = lib.moe_nvfp4_kv_sparse_attention_workspace_size(t, r, heads, kv_heads, dim, c.page_size, top_k)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     with _on(dev.index):
         st = attend(c, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(), seq_lens.data_ptr(), r,
                     block_table.data_ptr(), width, selected.data_ptr(), top_k, scale, out.data_ptr(),
-                    lse.data_ptr() if return_lse else None, _raw_stream(dev.index))
+                    lse.data_ptr() if return_lse else None, workspace.data_ptr() if workspace is not None else None,
+                    workspace.numel() if workspace is not None else 0, _raw_stream(dev.index))
     if st:
         L.check("moe_nvfp4_kv_sparse_attention", st)
     return (out, lse) if return_lse else out

@@ -78,10 +78,10 @@ def _select(index, q=0x2000, stride=512, t=3, heads=4, off=0x3000, lens=0x3100, 
 
 
 def _attend(cache, q=0x2000, stride=512, t=3, heads=4, off=0x3000, lens=0x3100, r=2, table=0x3200, width=4,
-            selected=0x5000, top_k=3, scale=0.1, out=0x4000, lse=None, fill=False):
+            selected=0x5000, top_k=3, scale=0.1, out=0x4000, lse=None, fill=False, ws=0x100000, ws_bytes=1 << 40):
     f = L.lib().moe_nvfp4_kv_sparse_attention_fill if fill else L.lib().moe_nvfp4_kv_sparse_attention
     return f(ctypes.byref(cache) if cache else None, q, stride, t, heads, off, lens, r, table, width, selected, top_k,
-             scale, out, lse, None)
+             scale, out, lse, ws, ws_bytes, None)
 
 
 STEP = [dict(off=None), dict(off=0x3002), dict(lens=None), dict(lens=0x3101), dict(r=-1), dict(r=4097), dict(table=None),
@@ -134,6 +134,22 @@ def test_no_ops():
     assert _attend(_cache(), r=0, fill=True, out=None) == INV
     for bad in (dict(d=96), dict(page=40), dict(k=0.0), dict(pages=None)):
         assert _attend(_cache(**bad)) == INV
+
+
+def test_workspace_sizes():
+    size = L.lib().moe_nvfp4_kv_sparse_attention_workspace_size
+    for bad in ((-1, 1, 4, 2, 128, 64, 3), (1, -1, 4, 2, 128, 64, 3), (1, 4097, 4, 2, 128, 64, 3), (1, 1, 5, 2, 128, 64, 3),
+                (1, 1, 130, 2, 128, 64, 3), (1, 1, 4, 2, 96, 64, 3), (1, 1, 4, 2, 128, 40, 3), (1, 1, 4, 2, 128, 64, 0),
+                (1, 1, 4, 2, 128, 64, 1025), (1 << 30, 1, 4, 2, 128, 64, 3)):
+        assert size(*bad) == 0
+    assert size(0, 1, 4, 2, 128, 64, 300) == size(1, 0, 4, 2, 128, 64, 300) == 0
+    long = dict(t=1, top_k=300)
+    need = size(1, 2, 4, 2, 128, 64, 300)
+    assert need > 0
+    for fill in (False, True):
+        assert _attend(_cache(), ws=None, fill=fill, **long) == _attend(_cache(), ws_bytes=need - 1, fill=fill,
+                                                                        **long) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+        assert _attend(_cache(), ws=0x100008, fill=fill, **long) == INV
 
 
 def test_wrappers_refuse_cpu_tensors():
