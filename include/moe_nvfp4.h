@@ -597,7 +597,7 @@ moe_status_t moe_nvfp4_kv_index_update(const moe_nvfp4_kv_cache_t* cache /* host
  * entry is outside [0, num_pages) are not chosen by score; those of the last `last` that lie behind the table are listed
  * (the attention makes such rows NaN).  Rows of no request, and rows at negative positions, get -1 only.
  * q as for moe_nvfp4_kv_attention.
- * Limits: 1 <= first + last <= top_k <= 1024, first >= 0, last >= 1; table_width <= 32768; T * kv_heads <= 2^21. */
+ * Limits: 1 <= first + last <= top_k <= 1024, first >= 0, last >= 1; table_width <= 16384; T * kv_heads <= 2^21. */
 moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index /* host */, const uint16_t* q, int64_t q_stride,
                                  int32_t T, int32_t Hq, const int32_t* query_offsets, const int32_t* seq_lens, int32_t R,
                                  const int32_t* block_table, int32_t table_width, int32_t top_k, int32_t first,

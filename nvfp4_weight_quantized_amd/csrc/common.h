@@ -54,6 +54,11 @@ __device__ __forceinline__ void direct_load16_nt(const void* base, uint32_t offs
   asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(offset), "s"(base), "{m0}"(lds_addr) : "memory");
 }
 
+// direct_load16 from an address of the lane's own.
+__device__ __forceinline__ void direct_load16_from(const void* src, uint32_t lds_addr) {
+  asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(lds_addr) : "memory");
+}
+
 // 4 bytes per lane from global memory straight to LDS (global_load_lds_dword): lane i's dword lands
 // at lds_addr + 4*i; otherwise as direct_load16.
 __device__ __forceinline__ void direct_load4(const void* base, uint32_t offset, uint32_t lds_addr) {

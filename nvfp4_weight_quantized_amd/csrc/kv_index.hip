@@ -25,47 +25,69 @@ __device__ __forceinline__ int touched_pages(const KvStep& s, const StepRequest&
   return max(min((q.len - 1) / s.page_size, s.width - 1) - first_page(s, q) + 1, 0);
 }
 
-// Sum over the 16 lanes of a row, in all of them.
-__device__ __forceinline__ int row_sum(int v) {
-  v += dpp_i<kDppQuad1032>(v, v);
-  v += dpp_i<kDppQuad2301>(v, v);
-  v += dpp_i<kDppRowHalfMirror>(v, v);
-  v += dpp_i<kDppRowMirror>(v, v);
-  return v;
+// Sums over the 16 lanes of a row, 16 numbers at once: number i meets in lane i of the row.  Each step pairs lanes and
+// halves the numbers each holds, so that all of it takes 15 exchanges where 16 sums would take 64.
+template <int CTRL, int BIT, int N>
+__device__ __forceinline__ void meet_halves(int (&v)[16]) {
+  const bool upper = (threadIdx.x >> BIT) & 1;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const int keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
+    v[i] = keep + dpp_i<CTRL>(give, give);
+  }
+}
+__device__ __forceinline__ int row_sums(int (&v)[16]) {
+  meet_halves<kDppRowMirror, 3, 16>(v);
+  meet_halves<kDppRowHalfMirror, 2, 8>(v);
+  meet_halves<kDppQuad2301, 1, 4>(v);
+  meet_halves<kDppQuad1032, 0, 2>(v);
+  return v[0];
 }
 
-// A workgroup per touched page and head, its four waves every fourth unit each.  A lane holds one position (of 16) and
-// the elements [8u, 8u + 8) of every 32, as the unit's 16-byte pieces give them; 16 units are summed in 32 bits (|S| of
-// 512 positions is below 2^31), what lies beyond in 64.
-template <int D>
-__global__ __launch_bounds__(256) void kv_index_kernel(moe_nvfp4_kv_cache_t c, int8_t* __restrict__ codes,
-                                                       float* __restrict__ scales, KvStep s) {
+// W waves per touched page and head take every W-th unit.  A lane holds one position (of 16) and the elements
+// [8u, 8u + 8) of every 32, as the unit's 16-byte pieces give them.  Sums go from fp32 (three units: six positions of a
+// lane, below 2^24 in units of 2^-10, so exact) to 32-bit integers over the 16 lanes (96 positions: below 2^29) and to
+// 64 bits beyond.
+template <int D, int W>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvfp4_kv_cache_t c,
+                                                                         int8_t* __restrict__ codes,
+                                                                         float* __restrict__ scales, KvStep s,
+                                                                         int items) {
   using U = KvUnit<D>;
-  constexpr int NS = D / 32, NL = NS / 2, kFlush = 16;
-  __shared__ long long sums[D], tops[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, u4 = lane >> 4, n16 = lane & 15, h = blockIdx.y;
+  constexpr int NS = D / 32, NL = NS / 2, kUnits = 3;
+  const int tid = threadIdx.x, lane = tid & 63, u4 = lane >> 4, n16 = lane & 15, hkv = c.kv_heads;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), me = W == 1 ? 0 : wave;
+  // heads of a page in neighbouring waves
+  const int at = W == 1 ? 4 * blockIdx.x + wave : blockIdx.x, h = at % hkv;
   StepRequest q;
   int within;
-  if (!step_find(s, blockIdx.x, [&](const StepRequest& x) { return touched_pages(s, x); }, &q, &within)) return;
+  if (at >= items * hkv ||
+      !step_find(s, at / hkv, [&](const StepRequest& x) { return touched_pages(s, x); }, &q, &within))
+    return;
   const int b = first_page(s, q) + within, page = s.table[(size_t)q.r * s.width + b];
   if (page < 0 || page >= c.num_pages) return;
   const int held = min(c.page_size, q.len - b * c.page_size), units = (held + kKvUnit - 1) / kKvUnit;
-  if (tid < D) sums[tid] = 0;
-  __syncthreads();
   const uint8_t* first = c.pages + kv_unit_offset<D>(c, page * c.page_size, h);
-  for (int u0 = wave; u0 < units; u0 += 4 * kFlush) {
-    int acc[NS][8];
+  // sum[j]: element 32*k + 8*u4 + i, number 16*j + n16 = 8*k + i
+  long long sum[NS / 2];
+#pragma unroll
+  for (int j = 0; j < NS / 2; ++j) sum[j] = 0;
+  for (int u0 = me; u0 < units; u0 += kUnits * W) {
+    float acc[NS][8];
 #pragma unroll
     for (int k = 0; k < NS; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[k][e] = 0;
-    for (int u = u0; u < min(units, u0 + 4 * kFlush); u += 4) {
+      for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kUnits; ++x) {
+      const int u = u0 + x * W;
+      if (u >= units) continue;
       const uint8_t* unit = first + (size_t)u * U::kBytes;
       uint32_t w[2 * NS], sc[NS / 2];
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(unit + 1024 * j + 16 * lane);
-        w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+        const uint4 y = *reinterpret_cast<const uint4*>(unit + 1024 * j + 16 * lane);
+        w[4 * j] = y.x, w[4 * j + 1] = y.y, w[4 * j + 2] = y.z, w[4 * j + 3] = y.w;
       }
 #pragma unroll
       for (int j = 0; j < NS / 2; ++j)
@@ -77,40 +99,51 @@ __global__ __launch_bounds__(256) void kv_index_kernel(moe_nvfp4_kv_cache_t c, i
         for (int k = 0; k < NS; ++k) {
           const int word = half * NS + k, byte = word & 3;
           const int bits = (int)sc[word >> 2];
-          const float f = 1024.f * (byte == 0   ? __builtin_amdgcn_cvt_f32_fp8(bits, 0)
-                                    : byte == 1 ? __builtin_amdgcn_cvt_f32_fp8(bits, 1)
-                                    : byte == 2 ? __builtin_amdgcn_cvt_f32_fp8(bits, 2)
-                                                : __builtin_amdgcn_cvt_f32_fp8(bits, 3));
+          const float f8 = byte == 0   ? __builtin_amdgcn_cvt_f32_fp8(bits, 0)
+                           : byte == 1 ? __builtin_amdgcn_cvt_f32_fp8(bits, 1)
+                           : byte == 2 ? __builtin_amdgcn_cvt_f32_fp8(bits, 2)
+                                       : __builtin_amdgcn_cvt_f32_fp8(bits, 3);
+          const float f = seen ? 1024.f * f8 : 0.f;
           const f32x2 e[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 0),
                               __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 1),
                               __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 2),
                               __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 3)};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[k][i] += seen ? (int)(e[i >> 1][i & 1] * f) : 0;      // exact
+          for (int i = 0; i < 8; ++i) acc[k][i] = __fmaf_rn(e[i >> 1][i & 1], f, acc[k][i]);
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < NS; ++k)
+    for (int j = 0; j < NS / 2; ++j) {
+      int v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int v = row_sum(acc[k][i]);
-        if (n16 == 0)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&sums[32 * k + 8 * u4 + i]), (unsigned long long)(long long)v);
-      }
+      for (int i = 0; i < 16; ++i) v[i] = (int)acc[2 * j + (i >> 3)][i & 7];
+      sum[j] += row_sums(v);
+    }
   }
-  __syncthreads();
-  const long long sum = tid < D ? sums[tid] : 0;
-  long long top = sum < 0 ? -sum : sum;
+  if (W > 1) {
+    __shared__ long long sums[W][NS / 2][64];
+#pragma unroll
+    for (int j = 0; j < NS / 2; ++j) sums[wave][j][lane] = sum[j];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int j = 0; j < NS / 2; ++j)
+      for (int w = 1; w < W; ++w) sum[j] += sums[w][j][lane];
+  }
+  long long top = 0;
+#pragma unroll
+  for (int j = 0; j < NS / 2; ++j) top = max(top, sum[j] < 0 ? -sum[j] : sum[j]);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = max(top, (long long)__shfl_xor(top, off));
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
-  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-  const size_t at = (size_t)page * c.kv_heads + h;
+  const size_t out = (size_t)page * hkv + h;
   // in 64 bits: a quotient half way between two whole numbers is exact, others are further from it than their rounding
-  if (tid < D) codes[at * D + tid] = top > 0 ? (int8_t)(int)rint(127.0 * (double)sum / (double)top) : (int8_t)0;
-  if (tid == 0) scales[at] = (float)((double)top / (130048.0 * held));
+#pragma unroll
+  for (int j = 0; j < NS / 2; ++j) {
+    const int d = 32 * (2 * j + (n16 >> 3)) + 8 * u4 + (n16 & 7);
+    codes[out * D + d] = top > 0 ? (int8_t)(int)rint(127.0 * (double)sum[j] / (double)top) : (int8_t)0;
+  }
+  if (lane == 0) scales[out] = (float)((double)top / (130048.0 * held));
 }
 
 // ------------------------------------------------------------------------------------ choice
@@ -135,6 +168,8 @@ struct SelectShape {
 
 constexpr int kOne = 0;
 constexpr int group_tokens(int HS) { return HS == kOne ? 1 : 16 / HS; }
+// Chunks of 16 pages in a wave's ring.
+constexpr int select_ring(int D, bool wide) { return D == 256 && wide ? 1 : 2; }
 
 // The rows of the workgroup's tokens in 8 bits: operand bytes codes[block][step][lane][16] and tops[block][row].
 template <int D, int HS>
@@ -193,215 +228,313 @@ __device__ __forceinline__ void select_rows(const KvSelectProblem& p, const Step
   }
 }
 
+// Bits that stand for no scale (a NaN that no computation gives).
+constexpr uint32_t kBadPage = 0xFFFFDEADu;
+
+// Largest value of the lanes 16 and 32 apart.
+__device__ __forceinline__ float quarters_max(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// 16 pages' codes in LDS, a line of D bytes each.  Piece x (16 bytes) of page n lies at piece x ^ fold(n): the lanes that
+// read the same piece of 16 pages then find it in 16 different sets of four banks.
+template <int D>
+__device__ __forceinline__ int page_piece(int n, int x) {
+  return n * D + 16 * (x ^ ((n / (256 / D)) & (D / 16 - 1)));
+}
+
 // Keys of the pages [0, pages) for the workgroup's tokens: keys[token * stride + page], 0 for a page that is not in the
-// cache.  A wave takes 64 pages at a time, whose codes are all asked for before the first product.
-template <int D, int HS, int NW>
+// cache.  A wave takes 64 pages at a time, a lane's page of the table and its scale first, then the codes 16 pages at a
+// time straight to LDS, through a ring of its own (`ring` of RING chunks): neighbouring lanes ask for pieces of one
+// page, where as operands they would each touch another page's line, and the address unit looks up one line a cycle
+// (one row on 2048 pages: 11 us of products in that form).
+template <int D, int HS, int NW, int RING>
 __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const int32_t* __restrict__ table, int h,
                                               int pages, const SelectShape& sh, const int8_t* codes, const float* tops,
-                                              uint32_t* keys) {
+                                              uint32_t* keys, uint8_t* ring) {
   constexpr int KS = D / 64, TPL = HS == kOne ? 1 : 4 / HS;      // tokens of a lane
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q4 = lane >> 4, n16 = lane & 15, hkv = p.index.kv_heads;
-  for (int j0 = 64 * wave; j0 < pages; j0 += 64 * NW) {
-    i32x4 b[4][KS];
-    float scale[4];
-    bool good[4];
+  constexpr int LPP = D / 16, PPL = 64 / LPP, LOADS = 16 / PPL;  // lanes per page, pages per load, loads per chunk
+  using lds_bytes = __attribute__((address_space(3))) uint8_t*;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q4 = lane >> 4, n16 = lane & 15, hkv = p.index.kv_heads;
+  const lds_bytes mine = (lds_bytes)ring + wave * RING * 16 * D;
+  struct Batch {
+    int page;         // of this lane; 0 where it is not in the cache
+    uint32_t scale;   // its bits, kBadPage there
+  };
+  auto load_batch = [&](int j0) {
+    Batch x{0, kBadPage};
+    if (j0 + lane < pages) {
+      const int page = table[j0 + lane];
+      if (page >= 0 && page < p.index.num_pages)
+        x = Batch{page, __float_as_uint(p.index.scales[(size_t)page * hkv + h])};
+    }
+    return x;
+  };
+  const uint8_t* from[LOADS];      // of page 0
+#pragma unroll
+  for (int t = 0; t < LOADS; ++t) {
+    const int n = t * PPL + lane / LPP;
+    from[t] = reinterpret_cast<const uint8_t*>(p.index.codes) + (size_t)h * D +
+              16 * ((lane % LPP) ^ ((n / (256 / D)) & (LPP - 1)));
+  }
+  const uint32_t page_bytes = hkv * D;
+  // chunk x of a batch into ring slot `slot`
+  auto issue = [&](const Batch& b, int x, int slot) {
+    const uint32_t dst = (uint32_t)(uintptr_t)mine + slot * 16 * D;
+#pragma unroll
+    for (int t = 0; t < LOADS; ++t)
+      direct_load16_from(from[t] + (uint64_t)(uint32_t)__shfl(b.page, 16 * x + t * PPL + lane / LPP) * page_bytes,
+                         dst + 1024 * t);
+  };
+  // 1 .. 0xFFFFFFFE
+  auto key_of = [&](float best, uint32_t scale) {
+    return scale != kBadPage ? min(max(order_key(best * __uint_as_float(scale)), 1u), 0xFFFFFFFEu) : 0u;
+  };
+  const int first = 64 * wave, step = 64 * NW;
+  if (first >= pages) return;
+  Batch now = load_batch(first), next = now;
+#pragma unroll
+  for (int i = 0; i < RING; ++i) issue(now, i, i);
+  for (int j0 = first; j0 < pages; j0 += step, now = next) {
+    const bool more = j0 + step < pages;
+    if (more) next = load_batch(j0 + step);
+    float score = 0.f;      // one token: of page j0 + lane
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int j = j0 + 16 * x + n16, page = j < pages ? table[j] : -1;
-      good[x] = page >= 0 && page < p.index.num_pages;
-      const size_t at = good[x] ? (size_t)page * hkv + h : 0;
-      scale[x] = p.index.scales[at];
+      constexpr int kLater = (RING - 1) * LOADS;
+      if (x + RING - 1 < 4 || more) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLater) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+      const int slot = x % RING;
+      i32x4 b[KS];
 #pragma unroll
       for (int k = 0; k < KS; ++k)
-        b[x][k] = *reinterpret_cast<const i32x4*>(p.index.codes + at * D + 64 * k + 16 * q4);
-    }
-    for (int grp = 0; grp < sh.groups; ++grp) {
-      float best[4][TPL];
+        b[k] = *reinterpret_cast<const __attribute__((address_space(3))) i32x4*>(
+            mine + slot * 16 * D + page_piece<D>(n16, 4 * k + q4));
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");      // the slot has been read
+      if (x + RING < 4) issue(now, x + RING, slot);
+      else if (more) issue(next, x + RING - 4, slot);
+      const int j = j0 + 16 * x + n16;
+      const uint32_t scale = HS == kOne ? 0u : __shfl(now.scale, 16 * x + n16);
+      for (int grp = 0; grp < sh.groups; ++grp) {
+        float best[TPL];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < TPL; ++y) best[x][y] = -INFINITY;
-      for (int blk = 0; blk < sh.blocks; ++blk) {
-        const int8_t* a = codes + (size_t)(grp * sh.blocks + blk) * KS * 1024 + 16 * lane;
-        i32x4 rows[KS];
-#pragma unroll
-        for (int k = 0; k < KS; ++k) rows[k] = *reinterpret_cast<const i32x4*>(a + 1024 * k);
-        const float4 top = *reinterpret_cast<const float4*>(tops + 16 * (grp * sh.blocks + blk) + 4 * q4);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int y = 0; y < TPL; ++y) best[y] = -INFINITY;
+        for (int blk = 0; blk < sh.blocks; ++blk) {
+          const int8_t* a = codes + (size_t)(grp * sh.blocks + blk) * KS * 1024 + 16 * lane;
+          const float4 top = *reinterpret_cast<const float4*>(tops + 16 * (grp * sh.blocks + blk) + 4 * q4);
           i32x4 dot = {0, 0, 0, 0};
 #pragma unroll
-          for (int k = 0; k < KS; ++k) dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(rows[k], b[x][k], dot, 0, 0, 0);
-          const float s[4] = {(float)dot[0] * top.x, (float)dot[1] * top.y, (float)dot[2] * top.z,
-                              (float)dot[3] * top.w};
+          for (int k = 0; k < KS; ++k)
+            dot = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4*>(a + 1024 * k), b[k], dot, 0, 0, 0);
+          const float s[4] = {(float)dot[0] * top.x, (float)dot[1] * top.y, (float)dot[2] * top.z, (float)dot[3] * top.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) best[x][i * TPL / 4] = fmaxf(best[x][i * TPL / 4], s[i]);
+          for (int e = 0; e < 4; ++e) best[e * TPL / 4] = fmaxf(best[e * TPL / 4], s[e]);
         }
-      }
+        if (HS == kOne) {
+          const float v = quarters_max(best[0]);
+          score = q4 == x ? v : score;
+        } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-#pragma unroll
-        for (int y = 0; y < TPL; ++y) {
-          float v = best[x][y];
-          if (HS == kOne) {
-            v = fmaxf(v, __shfl_xor(v, 16));
-            v = fmaxf(v, __shfl_xor(v, 32));
+          for (int y = 0; y < TPL; ++y) {
+            const int t = grp * (16 / (HS == kOne ? 1 : HS)) + q4 * TPL + y;
+            if (j < sh.stride) keys[(size_t)t * sh.stride + j] = key_of(best[y], scale);
           }
-          // 1 .. 0xFFFFFFFE
-          const uint32_t key = good[x] ? min(max(order_key(v * scale[x]), 1u), 0xFFFFFFFEu) : 0u;
-          const int t = HS == kOne ? 0 : grp * (16 / HS) + q4 * TPL + y, j = j0 + 16 * x + n16;
-          if ((HS != kOne || q4 == 0) && j < sh.stride) keys[(size_t)t * sh.stride + j] = key;
         }
       }
     }
+    if (HS == kOne && j0 + lane < sh.stride) keys[j0 + lane] = key_of(score, now.scale);
   }
 }
 
-// The top_k largest of a token's keys, by W waves (1 or all of the workgroup's; `me` of them), 64 * W * 32 keys at most:
-// the threshold by halving the interval of keys that holds it, from the smallest of the lanes' largest keys (which 64
-// keys reach) to the largest; most often some key splits off exactly what is wanted long before the interval is empty.
+// The threshold of the `want` largest of some keys, count(lo) >= want > 0 keys from lo on and none from hi on: afterwards
+// count(lo) >= want > count(lo + 1), or *above == want and exactly `want` lie from lo on, which most often happens long
+// before the interval has been halved 32 times.
+template <typename Count>
+__device__ __forceinline__ void halve(uint32_t* lo, uint32_t hi, int want, int* above, Count&& at_least) {
+  *above = 0;
+  while (hi - *lo > 1) {
+    const uint32_t mid = *lo + (hi - *lo) / 2;
+    const int n = at_least(mid);
+    if (n >= want) *lo = mid;
+    else hi = mid;
+    if (n <= want) *above = n;
+    if (n == want) return;
+  }
+}
+
+// The pages of one token: those listed always, and the `room` largest keys of the others.  W waves (1, or all of the
+// workgroup; `me` of them) hold the keys in registers, each a run of pages.  The room-th largest of a wave's 64 largest
+// keys of a lane bounds the threshold from below and leaves little more than `room` candidates, found by halving over
+// one key per lane; of several waves' bounds the largest holds.  The candidates go to a list in order of pages, where
+// one wave finds the threshold itself.  Where that is too long (many equal keys, more than 64 wanted) or there are few
+// pages the registers are searched instead, by all waves together.
+constexpr int kSelectWaves = 16, kManyWaves = 8;      // of a workgroup: one token or many pages, several tokens
+
 template <int W>
-__device__ __forceinline__ void select_take(const KvSelectProblem& p, const uint32_t* keys, int own, int me, int* meet,
-                                            int& turn, int32_t* out) {
-  constexpr int VPL = 32, STEP = 8;
+__device__ __forceinline__ void select_take(const KvSelectProblem& p, uint32_t* keys, int stride, int own, int me,
+                                            int* meet, int& turn, int32_t* out) {
+  constexpr int VPL = W == 1 ? 32 : 16, STEP = 4, LIST = W == 1 ? 4 : 16;      // registers; LIST for the list
   const int lane = threadIdx.x & 63, width = p.step.width, count = min(own + 1, width);
-  const int tail = max(own + 1 - p.last, 0), head = min(p.first, count);      // listed always: below head, from tail on
-  const int beyond = max(own + 1 - max(width, tail), 0);                       // of them behind the table
-  const int room = p.top_k - beyond - head - max(count - max(tail, head), 0);
+  const uint64_t below = lane == 0 ? 0 : ~0ull >> (64 - lane);
+  const int head = min(p.first, count), tail = min(max(own + 1 - p.last, head), count);      // [head, tail) by score
+  const int beyond = max(own + 1 - max(width, max(own + 1 - p.last, 0)), 0);      // listed always, behind the table
+  const int room = p.top_k - beyond - head - (count - tail), base = W == 1 ? 0 : 64 * VPL * me;
   uint32_t v[VPL];
 #pragma unroll
   for (int s = 0; s < VPL / STEP; ++s) {
-    if (64 * W * STEP * s < count) {
+    if (base + 64 * STEP * s < count) {
 #pragma unroll
       for (int i = STEP * s; i < STEP * (s + 1); ++i) {
-        const int j = 64 * (W * i + me) + lane;
-        v[i] = j >= head && j < tail && j < count ? keys[j] : 0u;
+        const int j = base + 64 * i + lane;
+        v[i] = j >= head && j < tail ? keys[j] : 0u;
       }
     } else {
 #pragma unroll
       for (int i = STEP * s; i < STEP * (s + 1); ++i) v[i] = 0u;
     }
   }
-  // over the waves: sums, smallest and largest values
-  auto all_waves = [&](int x, auto&& join) {
-    if (W == 1) return x;
+  // sum and largest of the waves' values, and the sum of those before this wave
+  auto join = [&](int x, int* before, uint32_t* most) {
+    if (W == 1) {
+      if (before) *before = 0;
+      if (most) *most = (uint32_t)x;
+      return x;
+    }
     int* at = meet + (turn ^= W);      // two sets of W in turn, so that one barrier is enough
     if (lane == 0) at[me] = x;
     __syncthreads();
-    int y = at[0];
+    int sum = 0, low = 0;
+    uint32_t top = 0;
 #pragma unroll
-    for (int w = 1; w < W; ++w) y = join(y, at[w]);
-    return y;
+    for (int w = 0; w < W; ++w) {
+      const int y = __builtin_amdgcn_readfirstlane(at[w]);
+      low += w < me ? y : 0;
+      sum += y;
+      top = max(top, (uint32_t)y);
+    }
+    if (before) *before = low;
+    if (most) *most = top;
+    return sum;
   };
-  auto at_least = [&](uint32_t x) {
+  auto own_at_least = [&](uint32_t x) {
     int n = 0;
 #pragma unroll
     for (int s = 0; s < VPL / STEP; ++s)
-      if (64 * W * STEP * s < count) {
+      if (base + 64 * STEP * s < count) {
 #pragma unroll
         for (int i = STEP * s; i < STEP * (s + 1); ++i) n += __popcll(__ballot(v[i] >= x));
       }
-    return all_waves(n, [](int a, int b) { return a + b; });
+    return n;
   };
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) most = max(most, v[i]);
-  uint32_t lo = wave_min_u32(most), hi = wave_max_u32(most);
-  lo = (uint32_t)all_waves((int)lo, [](int a, int b) { return (int)min((uint32_t)a, (uint32_t)b); });
-  hi = (uint32_t)all_waves((int)hi, [](int a, int b) { return (int)max((uint32_t)a, (uint32_t)b); }) + 1;
-  // count(lo) >= want > count(hi)
-  int at_lo = 64 * W, above = 0;
-  const bool short_list = lo == 0 || room > 64 * W;
-  if (short_list) {
-    lo = 1;
-    at_lo = at_least(1);
+  uint32_t lo = 1, hi = wave_max_u32(most) + 1;
+  int above = 0;
+  if (room > 0 && room <= 64) {
+    auto lanes = [&](uint32_t x) { return (int)__popcll(__ballot(most >= x)); };
+    if (lanes(1) >= room) halve(&lo, hi, room, &above, lanes);
   }
-  const int want = min(room, at_lo);
-  if (want <= 0) {
-    lo = hi;
-  } else if (!short_list || at_lo != want) {
-    while (hi - lo > 1) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      const int n = at_least(mid);
-      if (n >= want) lo = mid;
-      else hi = mid, above = n;
-      if (n == want) {
-        above = want;
-        break;
-      }
-    }
-  } else {
-    above = want;
+  if (W > 1) {
+    join((int)lo, nullptr, &lo);
+    join((int)hi, nullptr, &hi);
   }
-  // chosen: keys from lo + 1 on and the first of those equal to lo, or all from lo on
-  const uint32_t sure = above == want ? lo : lo + 1;
-  int ties = want - above, filled = 0;
-  const uint64_t below = lane == 0 ? 0 : ~0ull >> (64 - lane);
-  const int total = want + head + max(count - max(tail, head), 0);
-  auto take = [&](uint32_t key, int j, int tied_before) {
-    const bool tie = key != 0 && key < sure && key >= lo && want > 0;
-    const uint64_t tied = __ballot(tie);
-    (void)tied;
-    return (j < count && (j < head || j >= tail)) || (key != 0 && key >= sure && want > 0) ||
-           (tie && tied_before + __popcll(tied & below) < ties);
-  };
-  if (W == 1) {
+  int start;      // candidates of the waves before
+  const int found = join(own_at_least(lo), &start, nullptr);
+  const int want = max(min(room, found), 0);      // found >= room, or lo = 1 and these are all
+  const bool listed = count > 256 && found <= min(64 * LIST, stride / 2) && want > 0;
+  if (listed) {
+    // candidates in order of pages: key and page
+    uint32_t* list = keys;
+    int* pages = reinterpret_cast<int*>(keys) + stride / 2;
 #pragma unroll
-    for (int s = 0; s < VPL / STEP; ++s) {
-      if (64 * STEP * s < count) {
+    for (int s = 0; s < VPL / STEP; ++s)
+      if (base + 64 * STEP * s < count) {
 #pragma unroll
         for (int i = STEP * s; i < STEP * (s + 1); ++i) {
-          const int j = 64 * i + lane;
-          const uint64_t tied = __ballot(v[i] != 0 && v[i] < sure && v[i] >= lo);
-          const bool chosen = take(v[i], j, 0);
-          const uint64_t taken = __ballot(chosen);
-          if (chosen) out[filled + __popcll(taken & below)] = j;
-          filled += __popcll(taken);
-          ties -= min(ties, (int)__popcll(tied));
+          const bool in = v[i] >= lo;
+          const uint64_t all = __ballot(in);
+          const int at = start + __popcll(all & below);
+          if (in) list[at] = v[i], pages[at] = base + 64 * i + lane;
+          start += __popcll(all);
         }
+      }
+    if (W > 1) {
+      __syncthreads();
+      if (me != 0) return;
+    }
+    uint32_t u[LIST];
+#pragma unroll
+    for (int i = 0; i < LIST; ++i) u[i] = 64 * i + lane < found ? list[64 * i + lane] : 0u;
+    above = found;
+    if (found > want)
+      halve(&lo, hi, want, &above, [&](uint32_t x) {
+        int n = 0;
+#pragma unroll
+        for (int s = 0; s < LIST; s += 2)
+          if (64 * s < found) n += __popcll(__ballot(u[s] >= x)) + __popcll(__ballot(u[s + 1] >= x));
+        return n;
+      });
+    int ties = want - above, filled = head;      // of the keys equal to lo, the first
+    const uint32_t sure = ties > 0 ? lo + 1 : lo;
+#pragma unroll
+    for (int i = 0; i < LIST; ++i) {
+      if (64 * i < found) {
+        const bool tie = u[i] == lo && ties > 0;
+        const uint64_t tied = __ballot(tie);
+        const bool chosen = (u[i] != 0 && u[i] >= sure) || (tie && __popcll(tied & below) < ties);
+        const uint64_t taken = __ballot(chosen);
+        if (chosen) out[filled + __popcll(taken & below)] = pages[64 * i + lane];
+        filled += __popcll(taken);
+        ties -= min(ties, (int)__popcll(tied));
       }
     }
   } else {
-    // 64 * W keys a round, in order of pages: the waves' counts meet before each writes
-    for (int i = 0; i < VPL; ++i) {
-      if (64 * W * i >= count) break;
-      uint32_t key = 0;
-#pragma unroll
-      for (int k = 0; k < VPL; ++k) key = k == i ? v[k] : key;
-      const int j = 64 * (W * i + me) + lane;
-      const int mine = __popcll(__ballot(key != 0 && key < sure && key >= lo));
-      int* at = meet + (turn ^= W);
-      if (lane == 0) at[me] = mine;
-      __syncthreads();
-      int before = 0, all_ties = 0;
-      for (int w = 0; w < W; ++w) {
-        before += w < me ? at[w] : 0;
-        all_ties += at[w];
-      }
-      const bool chosen = take(key, j, before);
-      const uint64_t taken = __ballot(chosen);
-      at = meet + (turn ^= W);
-      if (lane == 0) at[me] = __popcll(taken);
-      __syncthreads();
-      int start = filled;
-      for (int w = 0; w < W; ++w) {
-        start += w < me ? at[w] : 0;
-        filled += at[w];
-      }
-      if (chosen) out[start + __popcll(taken & below)] = j;
-      ties -= min(ties, all_ties);
+    above = found;
+    if (want > 0 && found > want)
+      halve(&lo, hi, want, &above, [&](uint32_t x) { return join(own_at_least(x), nullptr, nullptr); });
+    const int ties = want - above;
+    const uint32_t sure = ties > 0 ? lo + 1 : lo;
+    int tied_before, filled, left = 0;      // left: ties that this wave takes
+    if (W > 1 || ties > 0) {
+      const int mine = ties > 0 ? own_at_least(lo) - own_at_least(lo + 1) : 0;
+      join(mine, &tied_before, nullptr);
+      left = max(min(ties - tied_before, mine), 0);
     }
+    join((want > 0 ? own_at_least(sure) : 0) + left, &filled, nullptr);
+    filled += head;
+#pragma unroll
+    for (int s = 0; s < VPL / STEP; ++s)
+      if (want > 0 && base + 64 * STEP * s < count) {
+#pragma unroll
+        for (int i = STEP * s; i < STEP * (s + 1); ++i) {
+          const bool tie = v[i] == lo && left > 0;
+          const uint64_t tied = __ballot(tie);
+          const bool chosen = (v[i] != 0 && v[i] >= sure) || (tie && __popcll(tied & below) < left);
+          const uint64_t taken = __ballot(chosen);
+          if (chosen) out[filled + __popcll(taken & below)] = base + 64 * i + lane;
+          filled += __popcll(taken);
+          left -= min(left, (int)__popcll(tied));
+        }
+      }
+    if (me != 0) return;
   }
-  // own pages behind the table are listed all the same: the attention makes such rows NaN
-  for (int i = total + 64 * me + lane; i < p.top_k; i += 64 * W)
-    out[i] = i - total < beyond ? own + 1 - beyond + (i - total) : -1;
+  // one wave: the pages listed always, own pages behind the table among them (the attention makes such rows NaN)
+  for (int i = lane; i < head; i += 64) out[i] = i;
+  const int end = head + want + count - tail;
+  for (int i = head + want + lane; i < p.top_k; i += 64)
+    out[i] = i < end ? tail + (i - head - want) : i - end < beyond ? own + 1 - beyond + (i - end) : -1;
 }
 
 template <int D, int HS, bool WIDE>
-__global__ __launch_bounds__(WIDE || HS == kOne ? 1024 : 512) void kv_select_kernel(KvSelectProblem p, SelectShape sh) {
-  constexpr int NW = WIDE || HS == kOne ? 16 : 8;
+__global__ __launch_bounds__(64 * (WIDE || HS == kOne ? kSelectWaves : kManyWaves)) void kv_select_kernel(KvSelectProblem p, SelectShape sh) {
+  constexpr int NW = WIDE || HS == kOne ? kSelectWaves : kManyWaves, RING = select_ring(D, WIDE);
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ int meet[2 * NW];
+  __shared__ int meet[2 * kSelectWaves];
   const KvStep& s = p.step;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), hkv = p.index.kv_heads;
   if (blockIdx.x >= sh.work_groups) {      // rows of no request
@@ -425,7 +558,8 @@ __global__ __launch_bounds__(WIDE || HS == kOne ? 1024 : 512) void kv_select_ker
   if (pages > 0) {
     select_rows<D, HS>(p, q, h, tok0, sh, codes, tops);
     __syncthreads();
-    select_scores<D, HS, NW>(p, s.table + (size_t)q.r * s.width, h, pages, sh, codes, tops, keys);
+    select_scores<D, HS, NW, RING>(p, s.table + (size_t)q.r * s.width, h, pages, sh, codes, tops, keys,
+                                   reinterpret_cast<uint8_t*>(codes + (size_t)16 * sh.blocks * sh.groups * D));
     __syncthreads();
   }
   int turn = 0;
@@ -435,7 +569,7 @@ __global__ __launch_bounds__(WIDE || HS == kOne ? 1024 : 512) void kv_select_ker
     if (pos < 0) {
       for (int i = WIDE ? tid : tid & 63; i < p.top_k; i += WIDE ? 64 * NW : 64) out[i] = -1;
     } else {
-      select_take<WIDE ? NW : 1>(p, keys + (size_t)t * sh.stride, pos / s.page_size, WIDE ? wave : 0, meet, turn, out);
+      select_take<WIDE ? NW : 1>(p, keys + (size_t)t * sh.stride, sh.stride, pos / s.page_size, WIDE ? wave : 0, meet, turn, out);
     }
   }
 }
@@ -443,9 +577,13 @@ __global__ __launch_bounds__(WIDE || HS == kOne ? 1024 : 512) void kv_select_ker
 // LDS of a workgroup, and what fits: a compute unit holds 160 KB, two workgroups of several tokens are wanted on it.
 constexpr int kSelectLds = 150 << 10, kSelectHalf = 76 << 10;
 
-size_t select_lds(const SelectShape& s, int32_t D) {
-  return (size_t)s.tokens * s.stride * 4 + (size_t)16 * s.blocks * s.groups * (4 + D);
+size_t select_lds(const SelectShape& s, int32_t D, int waves, bool wide) {
+  return (size_t)s.tokens * s.stride * 4 + (size_t)16 * s.blocks * s.groups * (4 + D) +
+         (size_t)waves * select_ring(D, wide) * 16 * D;
 }
+
+// Pages from which a token's keys are held by all waves of the workgroup.
+bool select_wide(int32_t width) { return width > 2048; }
 
 // One token per workgroup where the step may be of single tokens (T <= R); otherwise as many groups of tokens as leave
 // 512 workgroups and fit, since all of them share what a workgroup reads of the index.
@@ -459,7 +597,8 @@ int select_heads(const KvSelectProblem& p, SelectShape* s) {
     for (int groups = 4; groups >= 1; groups /= 2) {
       s->groups = groups;
       s->tokens = groups * group_tokens(HS);
-      const bool fits = select_lds(*s, D) <= (groups > 1 ? kSelectHalf : kSelectLds);
+      const bool wide = select_wide(p.step.width);
+      const bool fits = select_lds(*s, D, wide ? kSelectWaves : kManyWaves, wide) <= (groups > 1 ? kSelectHalf : kSelectLds);
       if (fits && (groups == 1 || T / s->tokens * hkv >= 512)) return HS;
     }
   }
@@ -475,12 +614,18 @@ int64_t kv_index_items(int32_t T, int32_t R, int32_t page_size) {
   return std::min((int64_t)T, T / page_size + 2 * requests);      // n rows lie in at most (n - 2) / page_size + 2 pages
 }
 
+// A wave per page and head where it has at most three units, else four.
 moe_status_t launch_kv_index_update(const moe_nvfp4_kv_cache_t& c, const moe_nvfp4_kv_index_t& index, const KvStep& s,
                                     hipStream_t stream) {
+  const int64_t items = kv_index_items(s.T, s.R, s.page_size);
   with_head_dim(c.head_dim, [&](auto tag) {
-    hipLaunchKernelGGL(kv_index_kernel<decltype(tag)::value>,
-                       dim3((unsigned)kv_index_items(s.T, s.R, s.page_size), c.kv_heads), dim3(256), 0, stream, c,
-                       index.codes, index.scales, s);
+    constexpr int D = decltype(tag)::value;
+    if (c.page_size <= 3 * kKvUnit)
+      hipLaunchKernelGGL((kv_index_kernel<D, 1>), dim3((unsigned)((items * c.kv_heads + 3) / 4)), dim3(256), 0, stream, c,
+                         index.codes, index.scales, s, (int)items);
+    else
+      hipLaunchKernelGGL((kv_index_kernel<D, 4>), dim3((unsigned)(items * c.kv_heads)), dim3(256), 0, stream, c,
+                         index.codes, index.scales, s, (int)items);
   });
   return launch_status();
 }
@@ -492,8 +637,8 @@ moe_status_t launch_kv_select(const KvSelectProblem& p, hipStream_t stream) {
   const int64_t items = R == 0 ? 0 : std::min(T, T / s.tokens + std::min(T, R)) * p.index.kv_heads;
   s.work_groups = (uint32_t)items;
   const dim3 grid((unsigned)(items + fill));
-  const size_t bytes = select_lds(s, p.index.head_dim);
-  const bool wide = p.step.width > 2048;
+  const bool wide = select_wide(p.step.width);
+  const size_t bytes = select_lds(s, p.index.head_dim, wide || HS == kOne ? kSelectWaves : kManyWaves, wide);
   with_head_dim(p.index.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     auto launch = [&](auto heads) {
@@ -501,7 +646,7 @@ moe_status_t launch_kv_select(const KvSelectProblem& p, hipStream_t stream) {
       if (wide)
         hipLaunchKernelGGL((kv_select_kernel<D, H, true>), grid, dim3(1024), bytes, stream, p, s);
       else
-        hipLaunchKernelGGL((kv_select_kernel<D, H, false>), grid, dim3(H == kOne ? 1024 : 512), bytes, stream, p, s);
+        hipLaunchKernelGGL((kv_select_kernel<D, H, false>), grid, dim3(64 * (H == kOne ? kSelectWaves : kManyWaves)), bytes, stream, p, s);
     };
     if (HS == kOne) launch(DimC<kOne>{});
     else if (HS == 1) launch(DimC<1>{});

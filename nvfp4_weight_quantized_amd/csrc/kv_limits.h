@@ -4,7 +4,7 @@
 namespace moe {
 
 constexpr int kKvMaxRequests = 4096;
-constexpr int kKvMaxSelectPages = 32768;   // pages of a row of the block table that a choice looks at
+constexpr int kKvMaxSelectPages = 16384;   // pages of a row of the block table that a choice looks at
 constexpr int kKvMaxSelected = 1024;       // pages chosen for a row
 constexpr int kKvUnit = 32;   // positions per unit of a page (36 * head_dim bytes)
 

@@ -21,6 +21,7 @@ struct SparseTiles {
   int tokens;      // per tile
   int parts;       // tiles per token (tokens == 1)
   int splits;      // of a tile's units
+  uint32_t page_units;      // 2^32 / units of a page, rounded up (0: one unit)
   int bm;          // rows of a tile
   float* o;        // partial sums [tile][split][bm][D], unnormalised
   float* ml;       // [tile][split][2][bm]: reference maximum, sum
@@ -42,7 +43,7 @@ __device__ __forceinline__ bool sparse_find(const KvAttentionProblem& a, const S
 }
 
 template <int D, int MI, int NW>
-__global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void kv_sparse_kernel(KvSparseProblem p,
+__global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_sparse_kernel(KvSparseProblem p,
                                                                                                SparseTiles tiles) {
   using U = KvUnit<D>;
   constexpr int NS = D / 32, BM = 16 * MI, NL = NS / 2;
@@ -137,9 +138,11 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
   const int mine = units > wave ? (units - wave + NW - 1) / NW : 0;
   const lds_bytes ring = (lds_bytes)lds + wave * kRing * U::kBytes;
 
+  // unit u of the union is in entry u / upp, exactly for u < 2^32 / upp
+  auto entry_of = [&](int u) { return tiles.page_units ? (int)__umulhi((uint32_t)u, tiles.page_units) : u; };
   // the wave's unit i is unit u0 + wave + NW * i of the union
   auto issue = [&](int i, int slot) {
-    const int u = u0 + wave + NW * i, e = u / upp, page = __builtin_amdgcn_readfirstlane(entry_phys[e]);
+    const int u = u0 + wave + NW * i, e = entry_of(u), page = __builtin_amdgcn_readfirstlane(entry_phys[e]);
     const uint8_t* base = a.cache.pages;
     if (page >= 0) base += (((uint64_t)page * hkv + h) * upp + (u - e * upp)) * (uint64_t)U::kBytes;
     const uint32_t dst = (uint32_t)(uintptr_t)ring + slot * U::kBytes;
@@ -194,10 +197,8 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
 #pragma unroll
     for (int r = 0; r < NS; ++r) o[mi][r][0] = o[mi][r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  const int full = (1 << toks) - 1;
-
   auto compute = [&](int i, int slot) {
-    const int u = u0 + wave + NW * i, e = u / upp;
+    const int u = u0 + wave + NW * i, e = entry_of(u);
     const int key0 = __builtin_amdgcn_readfirstlane(entry_page[e]) * ps + (u - e * upp) * kKvUnit;
     if (key0 > pos_last) return;
     const int mask = __builtin_amdgcn_readfirstlane((int)entry_mask[e]);
@@ -227,17 +228,21 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
           sc[mi][kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mi][k], sc[mi][kb], 0, 0, 0);
       }
     }
-    // units that some row does not see whole: masks, and nothing from positions past the length
-    if (mask != full || key0 + kKvUnit - 1 > pos0 || bad) {
+    // a unit that every listed token sees whole: the other tokens' rows are hidden by their reference; else by positions,
+    // and nothing from positions past the length
+    const bool inside = key0 + kKvUnit - 1 <= pos0 && !bad;
+    bool hidden[MI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) hidden[mi] = ((mask >> bit[mi]) & 1) == 0;
+    if (!inside) {
       const int quarter = 4 * (lane_now() >> 4);
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi) {
-        const int reach = (mask >> bit[mi]) & 1 ? pos[mi] : -1;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const bool seen = key0 + 16 * kb + quarter + k <= reach;
+            const bool seen = key0 + 16 * kb + quarter + k <= pos[mi] && !hidden[mi];
             sc[mi][kb][k] = !seen ? -INFINITY : bad ? NAN : sc[mi][kb][k];
           }
       }
@@ -259,13 +264,13 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
     for (int mi = 0; mi < MI; ++mi) {
       float t[8];
       auto exponents = [&]() {
-        const float ref = m[mi] - kPExp;
+        const float ref = hidden[mi] ? INFINITY : m[mi] - kPExp;
 #pragma unroll
         for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(sc[mi][k >> 2][k & 3], c[mi], -ref);
         if (__builtin_expect(any_far, 0)) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            t[k] = far[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
+            t[k] = far[mi] && !hidden[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
         }
       };
       exponents();
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(64 * NW, (NW > 4 ? NW / 4 : D == 256 ? 1 : 2)) void
         float mx = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sc[mi][k >> 2][k & 3]);
-        const float f = kv_move(quarter_max(mx), c[mi], m[mi], far[mi]);
+        const float f = kv_move(hidden[mi] ? -INFINITY : quarter_max(mx), c[mi], m[mi], far[mi]);
         any_far |= __any(far[mi]);
         l[mi] *= f;
 #pragma unroll
@@ -462,6 +467,7 @@ __global__ __launch_bounds__(256) void kv_sparse_join_kernel(KvSparseProblem p, 
 }
 
 constexpr int kPlaces = 512;      // workgroups of four waves that splits aim at
+constexpr int64_t kWideRows = 16384;
 
 // Tiles of a call.  A token per tile while that leaves the card unfilled, else as many as the rows hold.
 struct SparsePlan {
@@ -472,9 +478,11 @@ struct SparsePlan {
 
 SparsePlan sparse_plan(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
   SparsePlan p{};
-  p.t.bm = G > 16 ? 32 : 16;
+  const bool many = (int64_t)T * hkv * ((G + 31) / 32) > kPlaces;
+  p.t.bm = G > 16 || (many && D != 256 && (int64_t)T * hkv * G >= kWideRows) ? 32 : 16;
   p.t.parts = (G + p.t.bm - 1) / p.t.bm;
-  p.t.tokens = (int64_t)T * hkv * p.t.parts <= kPlaces ? 1 : std::max(1, std::min(p.t.bm / G, kEntries / top_k));
+  p.t.tokens = many ? std::max(1, std::min(p.t.bm / G, kEntries / top_k)) : 1;
+  p.t.page_units = (uint32_t)((((uint64_t)1 << 32) + page_size / kKvUnit - 1) / (page_size / kKvUnit));
   p.tiles = std::min((int64_t)T, (int64_t)T / p.t.tokens + std::min(T, R)) * p.t.parts;
   const int64_t most = (int64_t)p.t.tokens * top_k * (page_size / kKvUnit), grid = std::max(p.tiles * hkv, (int64_t)1);
   p.t.splits = 1;
@@ -512,7 +520,9 @@ moe_status_t launch_kv_sparse_attention(const KvSparseProblem& problem, void* wo
   with_head_dim(a.cache.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     const dim3 blocks((unsigned)(grid + fill));
-    if (t.bm == 16)
+    if (t.bm == 16 && D != 256 && grid <= kPlaces)
+      hipLaunchKernelGGL((kv_sparse_kernel<D, 1, D == 256 ? 4 : 8>), blocks, dim3(512), lds, stream, p, t);
+    else if (t.bm == 16)
       hipLaunchKernelGGL((kv_sparse_kernel<D, 1, 4>), blocks, dim3(256), lds, stream, p, t);
     else
       hipLaunchKernelGGL((kv_sparse_kernel<D, 2, 4>), blocks, dim3(256), lds, stream, p, t);

@@ -67,13 +67,16 @@ __device__ __forceinline__ void load_rotated_group(const moe_rotary_t& r, const 
   }
 }
 
+// Blocks of the queries move memory, those of the keys and values keep the vector unit busy: a compute unit should hold
+// both, so they take turns, `run` blocks of the queries after each of the others for as long as both last.
 struct AppendRotaryBlocks {
   int q_tokens, k_tokens;      // per block
-  unsigned q, k;               // blocks of the queries, of the keys; the others quantize values
+  unsigned q, k, v;            // blocks of the queries, of the keys, of the values
+  unsigned run, turns;
 };
 
-// Three kinds of workgroups in one launch: tokens of the keys, of the queries (count and order chosen by the host), and
-// windows of the values as kv_append takes them.
+// Three kinds of workgroups in one launch: tokens of the queries, of the keys, and windows of the values as kv_append
+// takes them.
 template <int D, int W>
 __global__ __launch_bounds__(256) void kv_append_rotary_kernel(moe_nvfp4_kv_cache_t c, RotaryProblem q,
                                                                const uint16_t* __restrict__ k,
@@ -82,7 +85,17 @@ __global__ __launch_bounds__(256) void kv_append_rotary_kernel(moe_nvfp4_kv_cach
                                                                AppendRotaryBlocks blocks) {
   constexpr int NG = D / 16;
   __shared__ float2 table[kRotaryEntries];
+  // block: first the keys', then the values', from there on the queries'
   unsigned block = blockIdx.x;
+  const unsigned period = blocks.run + 1, mixed = blocks.turns * period, others = blocks.k + blocks.v;
+  if (block < mixed) {
+    const unsigned turn = block / period, place = block - turn * period;
+    block = place == 0 ? turn : others + turn * blocks.run + place - 1;
+  } else if (blocks.turns == others) {
+    block = others + (block - mixed) + blocks.turns * blocks.run;
+  } else {      // every query is taken
+    block = blocks.turns + (block - mixed);
+  }
   if (block < blocks.k) {
     const int t0 = block * blocks.k_tokens, count = min(blocks.k_tokens, q.T - t0);
     rotary_table(q.r, q.positions, q.position_stride, t0, count, table);
@@ -96,16 +109,14 @@ __global__ __launch_bounds__(256) void kv_append_rotary_kernel(moe_nvfp4_kv_cach
     }
     return;
   }
-  block -= blocks.k;
-  if (block < blocks.q) {
-    const int t0 = block * blocks.q_tokens, count = min(blocks.q_tokens, q.T - t0);
+  if (block >= others) {
+    const int t0 = (block - others) * blocks.q_tokens, count = min(blocks.q_tokens, q.T - t0);
     rotary_table(q.r, q.positions, q.position_stride, t0, count, table);
     __syncthreads();
     rotate_rows(q, t0, count, table);
     return;
   }
-  block -= blocks.q;
-  const long long i = (long long)block * 256 + threadIdx.x;
+  const long long i = (long long)(block - blocks.k) * 256 + threadIdx.x;
   const int per = c.kv_heads * NG;
   const long long wl = i / per;
   if (wl * W >= q.T) return;
@@ -142,8 +153,11 @@ moe_status_t launch_kv_append_rotary(const moe_nvfp4_kv_cache_t& c, const Rotary
   b.k_tokens = tokens_per_block(T, q.r.pairs, per, 512);
   b.q = blocks_for(T, b.q_tokens);
   b.k = blocks_for(T, b.k_tokens);
-  const int64_t values = ((quads ? (T + 3) / 4 : T) * per + 255) / 256;
-  const dim3 grid((unsigned)(b.q + b.k + values));
+  b.v = (unsigned)(((quads ? (T + 3) / 4 : T) * per + 255) / 256);
+  const unsigned others = b.k + b.v;
+  b.run = std::max(1u, b.q / others);
+  b.turns = std::min(others, b.q / b.run);
+  const dim3 grid(b.q + others);
   with_head_dim(c.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     if (quads)

@@ -21,7 +21,7 @@ from .kv import _BF16, _I32, _I32_END, _UNIT, HEAD_DIMS, NvFp4KvCache, _ints, _o
 from .ops import _need, _same_device, _shape
 
 MAX_SELECTED = 1024          # pages chosen for a row
-MAX_SELECT_WIDTH = 32768     # columns of a block table that a choice looks at
+MAX_SELECT_WIDTH = 16384     # columns of a block table that a choice looks at
 
 
 class NvFp4KvIndex:

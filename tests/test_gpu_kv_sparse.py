@@ -140,6 +140,12 @@ class Choice:
     (9, 128, 2, 6, 32, [(1, 70 * i) for i in range(9)], 0, 1, 0, 1),
     (10, 64, 1, 1, 32, [(17, 2000)], 0, 100, 0, 1),              # more than there are
     (11, 64, 1, 1, 32, [(2, 32 * 5000)], 0, 1024, 1, 1),
+    (12, 64, 1, 4, 32, [(9, 32 * 3000), (1, 40)], 0, 48, 1, 1),      # keys over all waves, several tokens
+    (13, 128, 1, 2, 32, [(10, 32 * 2100)], 0, 1000, 2, 2),
+    (14, 256, 1, 1, 64, [(3, 64 * 2500)], 0, 5, 1, 1),
+    (15, 256, 1, 48, 32, [(1, 32 * 1900)], 0, 200, 1, 1),
+    (16, 128, 2, 4, 32, [(20, 32 * 1000)], 0, 24, 1, 1),             # a list of candidates
+    (17, 128, 2, 1, 32, [(1, 32 * 2040), (1, 32 * 700)], 0, 63, 0, 1),
 ])
 def test_choice_matches_the_oracle(seed, dim, kv_heads, group, page, reqs, pad, top_k, first, last):
     Choice(seed, dim, kv_heads, group, page, reqs, pad=pad).check(top_k, first, last)
@@ -155,6 +161,14 @@ def test_choice_of_equal_scores_takes_the_lowest_pages():
     c.check(60)
     c.codes[:] = 0
     c.check(33, 2, 2)
+    for width in (1500, 5000):                                        # many equal keys, one wave and all of them
+        c = Choice(25, 64, 1, 4, 32, [(5, 32 * width)])
+        c.codes[:] = c.codes[0]
+        c.scales[:] = np.where(np.arange(len(c.scales)) % 7 == 0, 2.0, 1.0)[:, None].astype(np.float32)
+        c.check(100, 1, 3)
+        c.check(1000)
+        c.scales[:] = np.float32(0.25)
+        c.check(70)
 
 
 def test_choice_of_rows_without_a_usable_value():
@@ -358,7 +372,7 @@ def test_strided_queries_other_stream_and_refusals():
         with pytest.raises(ValueError):
             moe.kv_select(index, q, *args, **kw)
     with pytest.raises(ValueError):
-        moe.kv_select(index, q, args[0], args[1], torch.zeros(1, 32769, dtype=torch.int32, device=DEV), 4)
+        moe.kv_select(index, q, args[0], args[1], torch.zeros(1, 16385, dtype=torch.int32, device=DEV), 4)
     other = moe.NvFp4KvIndex(index.codes, index.scales, 64)
     with pytest.raises(ValueError):
         moe.kv_index_update(cache, other, *args, 9)

@@ -109,7 +109,7 @@ def test_index_update_needs_a_cache_of_its_sizes():
 
 
 @pytest.mark.parametrize("bad", STEP + [dict(q=None), dict(q=0x2008), dict(stride=511), dict(stride=504), dict(heads=0),
-                                        dict(heads=3), dict(heads=130), dict(width=32769), dict(top_k=0), dict(top_k=1),
+                                        dict(heads=3), dict(heads=130), dict(width=16385), dict(top_k=0), dict(top_k=1),
                                         dict(top_k=1025), dict(first=-1), dict(last=0), dict(first=3), dict(last=3),
                                         dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(out=None), dict(out=0x4002),
                                         dict(t=1 << 23)])
