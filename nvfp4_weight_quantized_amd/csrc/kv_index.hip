@@ -251,10 +251,11 @@ __device__ __forceinline__ int page_piece(int n, int x) {
 // time straight to LDS, through a ring of its own (`ring` of RING chunks): neighbouring lanes ask for pieces of one
 // page, where as operands they would each touch another page's line, and the address unit looks up one line a cycle
 // (one row on 2048 pages: 11 us of products in that form).
-template <int D, int HS, int NW, int RING>
+// rows() makes the operands of the rows while the first pages are on their way.
+template <int D, int HS, int NW, int RING, typename Rows>
 __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const int32_t* __restrict__ table, int h,
                                               int pages, const SelectShape& sh, const int8_t* codes, const float* tops,
-                                              uint32_t* keys, uint8_t* ring) {
+                                              uint32_t* keys, uint8_t* ring, Rows&& rows) {
   constexpr int KS = D / 64, TPL = HS == kOne ? 1 : 4 / HS;      // tokens of a lane
   constexpr int LPP = D / 16, PPL = 64 / LPP, LOADS = 16 / PPL;  // lanes per page, pages per load, loads per chunk
   using lds_bytes = __attribute__((address_space(3))) uint8_t*;
@@ -295,10 +296,13 @@ __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const in
     return scale != kBadPage ? min(max(order_key(best * __uint_as_float(scale)), 1u), 0xFFFFFFFEu) : 0u;
   };
   const int first = 64 * wave, step = 64 * NW;
-  if (first >= pages) return;
   Batch now = load_batch(first), next = now;
+  if (first < pages) {
 #pragma unroll
-  for (int i = 0; i < RING; ++i) issue(now, i, i);
+    for (int i = 0; i < RING; ++i) issue(now, i, i);
+  }
+  rows();
+  __syncthreads();
   for (int j0 = first; j0 < pages; j0 += step, now = next) {
     const bool more = j0 + step < pages;
     if (more) next = load_batch(j0 + step);
@@ -556,10 +560,9 @@ __global__ __launch_bounds__(64 * (WIDE || HS == kOne ? kSelectWaves : kManyWave
   float* tops = reinterpret_cast<float*>(keys + (size_t)sh.tokens * sh.stride);
   int8_t* codes = reinterpret_cast<int8_t*>(tops + 16 * sh.blocks * sh.groups);
   if (pages > 0) {
-    select_rows<D, HS>(p, q, h, tok0, sh, codes, tops);
-    __syncthreads();
     select_scores<D, HS, NW, RING>(p, s.table + (size_t)q.r * s.width, h, pages, sh, codes, tops, keys,
-                                   reinterpret_cast<uint8_t*>(codes + (size_t)16 * sh.blocks * sh.groups * D));
+                                   reinterpret_cast<uint8_t*>(codes + (size_t)16 * sh.blocks * sh.groups * D),
+                                   [&]() { select_rows<D, HS>(p, q, h, tok0, sh, codes, tops); });
     __syncthreads();
   }
   int turn = 0;
