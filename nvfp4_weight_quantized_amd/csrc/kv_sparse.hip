@@ -74,6 +74,21 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
   const int rows = tiles.parts > 1 ? min(BM, a.G - g0) : toks * a.G;
   const int pos0 = rq.len - rq.n + tok0, pos_last = pos0 + toks - 1;      // positions of the first and last token
 
+  // the query rows, asked for first: row n16 of block mi, elements [32s + 8*q4, +8)
+  u32x4 raw[MI][NS];
+  int pos[MI], bit[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int row = 16 * mi + n16;
+    const bool valid = row < rows;
+    const int t = valid && tiles.parts == 1 ? row / a.G : 0, g = valid ? g0 + row - t * a.G : 0;
+    pos[mi] = valid ? pos0 + t : -1;
+    bit[mi] = t;
+    const uint16_t* src = a.q + (int64_t)(rq.row0 + tok0 + t) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * q4;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) raw[mi][k] = *reinterpret_cast<const u32x4*>(src + 32 * k);
+  }
+
   // ---- the union of the lists
   int entries = 0;
   {
@@ -86,49 +101,60 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
     }
     __syncthreads();
     const int32_t* table = a.table + (size_t)rq.r * a.width;
-    // entry i of the lists opens an entry of the union where no earlier token lists its page
-    auto look = [&](int i, uint32_t* mask) {
-      const int t = i / K, k = i - t * K;
-      const uint32_t b = lists[i];
-      *mask = 1u << t;
-      if ((int)b < 0 || (long long)b * ps > pos0 + t || (k > 0 && lists[i - 1] == b)) return false;
-      bool first = true;
-      for (int o = 0; o < toks; ++o) {
-        if (o == t) continue;
-        int lo = 0, hi = K;      // the first element of list o not below b
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (lists[o * K + mid] < b) lo = mid + 1;
-          else hi = mid;
+    // a lane per entry of the lists: whether it opens one of the union, which no earlier token's list does, and the tokens
+    // whose lists hold the page
+    constexpr int kChunks = kEntries / 64 / NW;
+    int page_of[kChunks], phys_of[kChunks];
+    uint32_t mask_of[kChunks];
+    uint64_t opens[kChunks];
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int c = wave + NW * x, i = 64 * c + lane;
+      opens[x] = 0;
+      if (64 * c >= all) break;
+      bool open = false;
+      if (i < all) {
+        const int t = i / K, k = i - t * K;
+        const uint32_t b = lists[i];
+        uint32_t mask = 1u << t;
+        open = (int)b >= 0 && (long long)b * ps <= pos0 + t && (k == 0 || lists[i - 1] != b);
+        const int page = open && (int)b < a.width ? table[b] : -1;
+        for (int o = 0; o < toks; ++o) {
+          if (o == t) continue;
+          int lo = 0, hi = K;      // the first element of list o not below b
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (lists[o * K + mid] < b) lo = mid + 1;
+            else hi = mid;
+          }
+          // a token that lists a page ahead of its own position does not see it
+          if (lo < K && lists[o * K + lo] == b && (long long)b * ps <= pos0 + o) {
+            mask |= 1u << o;
+            open &= o > t;
+          }
         }
-        // an earlier token that lists a page ahead of its own position does not see it
-        if (lo < K && lists[o * K + lo] == b && (long long)b * ps <= pos0 + o) {
-          *mask |= 1u << o;
-          first &= o > t;
-        }
+        page_of[x] = (int)b;
+        phys_of[x] = page >= 0 && page < a.cache.num_pages ? page : -1;
+        mask_of[x] = mask;
       }
-      return first;
-    };
-    for (int c = wave; c < (all + 63) / 64; c += NW) {
-      uint32_t mask;
-      const uint64_t opens = __ballot(64 * c + lane < all && look(64 * c + lane, &mask));
-      if (lane == 0) chunk_count[c] = __popcll(opens);
+      opens[x] = __ballot(open);
+      if (lane == 0) chunk_count[c] = __popcll(opens[x]);
     }
     __syncthreads();
-    for (int c = 0; c < (all + 63) / 64; ++c) {
-      if (c % NW == wave) {
-        uint32_t mask = 0;
-        const bool open = 64 * c + lane < all && look(64 * c + lane, &mask);
-        const uint64_t opens = __ballot(open), below = lane == 0 ? 0 : ~0ull >> (64 - lane);
-        if (open) {
-          const int at = entries + __popcll(opens & below), b = (int)lists[64 * c + lane];
-          const int page = b < a.width ? table[b] : -1;
-          entry_page[at] = b;
-          entry_phys[at] = page >= 0 && page < a.cache.num_pages ? page : -1;
-          entry_mask[at] = (uint16_t)mask;
-        }
+    const int chunks = (all + 63) / 64;
+    const int mine = lane < chunks ? chunk_count[lane] : 0, before = wave_inclusive_scan(mine) - mine;      // chunks <= 16
+    entries = __builtin_amdgcn_readlane(before + mine, 63);
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int c = wave + NW * x;
+      if (64 * c >= all) break;
+      if ((opens[x] >> lane) & 1) {
+        const uint64_t below = lane == 0 ? 0 : ~0ull >> (64 - lane);
+        const int at = __builtin_amdgcn_readlane(before, c) + __popcll(opens[x] & below);
+        entry_page[at] = page_of[x];
+        entry_phys[at] = phys_of[x];
+        entry_mask[at] = (uint16_t)mask_of[x];
       }
-      entries += chunk_count[c];
     }
     __syncthreads();      // the lists have been read
   }
@@ -147,32 +173,29 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
     if (page >= 0) base += (((uint64_t)page * hkv + h) * upp + (u - e * upp)) * (uint64_t)U::kBytes;
     const uint32_t dst = (uint32_t)(uintptr_t)ring + slot * U::kBytes;
 #pragma unroll
-    for (int j = 0; j < kFull; ++j) direct_load16(base + 1024 * j, 16 * lane, dst + 1024 * j);
+    for (int j = 0; j < kFull; ++j) {
+      if (NW > 4) direct_load16_nt(base + 1024 * j, 16 * lane, dst + 1024 * j);
+      else direct_load16(base + 1024 * j, 16 * lane, dst + 1024 * j);
+    }
 #pragma unroll
-    for (int j = 0; j < kTail; ++j) direct_load4(base + 1024 * kFull + 256 * j, 4 * lane, dst + 1024 * kFull + 256 * j);
+    for (int j = 0; j < kTail; ++j) {
+      if (NW > 4) direct_load4_nt(base + 1024 * kFull + 256 * j, 4 * lane, dst + 1024 * kFull + 256 * j);
+      else direct_load4(base + 1024 * kFull + 256 * j, 4 * lane, dst + 1024 * kFull + 256 * j);
+    }
   };
   for (int i = 0; i < min(mine, kRing); ++i) issue(i, i);
 
-  // query operands: row n16 of block mi, elements [32s + 8*q4, +8)
+  // query operands
   f16x8 qf[MI][NS];
   float c[MI];
-  int pos[MI], bit[MI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
-    const int row = 16 * mi + n16;
-    const bool valid = row < rows;
-    const int t = valid && tiles.parts == 1 ? row / a.G : 0, g = valid ? g0 + row - t * a.G : 0;
-    pos[mi] = valid ? pos0 + t : -1;
-    bit[mi] = t;
-    const uint16_t* src = a.q + (int64_t)(rq.row0 + tok0 + t) * a.q_stride + (size_t)(h * a.G + g) * D + 8 * q4;
-    u32x4 w[NS];
+    const auto& w = raw[mi];
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < NS; ++k) {
-      w[k] = *reinterpret_cast<const u32x4*>(src + 32 * k);
+    for (int k = 0; k < NS; ++k)
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, max(w[k][j] & 0x7FFFu, (w[k][j] >> 16) & 0x7FFFu));
-    }
     int e = (int)(top >> 7);    // the row's largest exponent field
     e = max(e, __shfl_xor(e, 16));
     e = max(e, __shfl_xor(e, 32));
@@ -473,6 +496,7 @@ constexpr int64_t kWideRows = 16384;
 struct SparsePlan {
   SparseTiles t;
   int64_t tiles;      // bound on their number, over requests, tokens and parts
+  int waves;          // of a workgroup
   size_t o_bytes, bytes;
 };
 
@@ -485,8 +509,10 @@ SparsePlan sparse_plan(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, 
   p.t.page_units = (uint32_t)((((uint64_t)1 << 32) + page_size / kKvUnit - 1) / (page_size / kKvUnit));
   p.tiles = std::min((int64_t)T, (int64_t)T / p.t.tokens + std::min(T, R)) * p.t.parts;
   const int64_t most = (int64_t)p.t.tokens * top_k * (page_size / kKvUnit), grid = std::max(p.tiles * hkv, (int64_t)1);
+  p.waves = p.t.bm == 16 && D != 256 && grid <= kPlaces ? 8 : 4;
   p.t.splits = 1;
-  if (most > 64 && grid * 2 <= kPlaces) p.t.splits = (int)std::min(kPlaces / grid, (most + 3) / 4);
+  if (most > 64 && grid * 2 * p.waves <= 4 * kPlaces)
+    p.t.splits = (int)std::min(4 * kPlaces / p.waves / grid, (most + p.waves - 1) / p.waves);
   if (p.t.splits > 1) {
     p.o_bytes = (size_t)grid * p.t.splits * p.t.bm * D * 4;
     p.bytes = p.o_bytes + (size_t)grid * p.t.splits * 2 * p.t.bm * 4;
@@ -498,7 +524,7 @@ SparsePlan sparse_plan(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, 
 
 bool kv_sparse_launchable(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
   const SparsePlan p = sparse_plan(T, R, G, hkv, D, page_size, top_k);
-  return (p.tiles * hkv * p.t.splits + 256) * 256 < (int64_t)1 << 32;
+  return (p.tiles * hkv * p.t.splits + 256) * 64 * p.waves < (int64_t)1 << 32;
 }
 
 size_t kv_sparse_workspace(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
@@ -520,7 +546,7 @@ moe_status_t launch_kv_sparse_attention(const KvSparseProblem& problem, void* wo
   with_head_dim(a.cache.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     const dim3 blocks((unsigned)(grid + fill));
-    if (t.bm == 16 && D != 256 && grid <= kPlaces)
+    if (plan.waves == 8)
       hipLaunchKernelGGL((kv_sparse_kernel<D, 1, D == 256 ? 4 : 8>), blocks, dim3(512), lds, stream, p, t);
     else if (t.bm == 16)
       hipLaunchKernelGGL((kv_sparse_kernel<D, 1, 4>), blocks, dim3(256), lds, stream, p, t);
