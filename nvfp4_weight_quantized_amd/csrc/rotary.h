@@ -14,6 +14,22 @@ namespace {
 
 constexpr int kRotaryEntries = 1024;      // cosines and sines that a block holds in LDS, 8 KB
 
+// Entries are read four to a load by lanes that are 8 (or 4) entries apart; 16-byte pieces 256 bytes apart lie in the same
+// banks, so those of each next 256 bytes are exchanged among four.
+struct RotaryTable {
+  float4 pieces[kRotaryEntries / 2];
+  __device__ static int place(int piece) { return piece ^ ((piece >> 4) & 3); }
+  __device__ float4 pair(int entry) const { return pieces[place(entry >> 1)]; }      // entry even: two entries
+  __device__ float2& at(int entry) { return reinterpret_cast<float2*>(&pieces[place(entry >> 1)])[entry & 1]; }
+};
+
+// Division by a number that the host knows: of i with i * divisor < 2^32.
+struct Divider {
+  uint32_t divisor, magic;      // 2^32 / divisor, rounded up; 0: 1
+  static Divider of(uint32_t d) { return Divider{d, (uint32_t)((((uint64_t)1 << 32) + d - 1) / d)}; }
+  __device__ uint32_t operator()(uint32_t i) const { return magic ? __umulhi(i, magic) : i; }
+};
+
 // (cos a, sin a) * scale.  a = k pi/2 + r with |r| <= pi/4, pi/2 in two parts (|a| < 2^40: the parts reach 2^-106, so
 // r is off by less than 2^-52), then the Taylor series: the first terms left out are r^17 / 17! < 2^-54 and
 // r^18 / 18! < 2^-58.
@@ -43,14 +59,14 @@ __device__ __forceinline__ float2 rotary_turn(double a, float scale) {
   return float2{(float)(cs * scale), (float)(sn * scale)};
 }
 
-// The entries of the tokens [t0, t0 + count): table[n * i + pair].
+// The entries of the tokens [t0, t0 + count): pairs * i + pair.
 __device__ __forceinline__ void rotary_table(const moe_rotary_t& r, const int32_t* __restrict__ positions,
-                                             int64_t position_stride, int t0, int count, float2* table) {
+                                             int64_t position_stride, int t0, int count, RotaryTable& table) {
   for (int i = threadIdx.x; i < count * r.pairs; i += blockDim.x) {
     const int t = i / r.pairs, pair = i - t * r.pairs;
     const int axis = r.axis ? min(max(r.axis[pair], 0), r.axes - 1) : 0;
     const double angle = (double)positions[axis * position_stride + t0 + t] * r.inv_freq[pair];
-    table[i] = rotary_turn(angle, r.scale);
+    table.at(i) = rotary_turn(angle, r.scale);
   }
 }
 
@@ -58,8 +74,7 @@ struct Chunk {      // eight elements
   float v[8];
 };
 
-__device__ __forceinline__ Chunk load_chunk(const uint16_t* src) {
-  const uint4 w = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ Chunk chunk_of(const uint4& w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   Chunk x;
 #pragma unroll
@@ -70,34 +85,35 @@ __device__ __forceinline__ Chunk load_chunk(const uint16_t* src) {
   return x;
 }
 
-__device__ __forceinline__ void store_chunk(uint16_t* dst, const Chunk& x) {
-  *reinterpret_cast<uint4*>(dst) = uint4{f32x2_to_bf16x2(x.v[0], x.v[1]), f32x2_to_bf16x2(x.v[2], x.v[3]),
-                                         f32x2_to_bf16x2(x.v[4], x.v[5]), f32x2_to_bf16x2(x.v[6], x.v[7])};
+__device__ __forceinline__ uint4 bits_of(const Chunk& x) {
+  return uint4{f32x2_to_bf16x2(x.v[0], x.v[1]), f32x2_to_bf16x2(x.v[2], x.v[3]), f32x2_to_bf16x2(x.v[4], x.v[5]),
+               f32x2_to_bf16x2(x.v[6], x.v[7])};
 }
 
-// a, b: the first and the second elements of eight pairs.
-__device__ __forceinline__ void rotate_halves(const float2* turn, Chunk& a, Chunk& b) {
+__device__ __forceinline__ void rotate_pair(float c, float s, float& x, float& y) {
 #pragma clang fp contract(off)
+  const float xc = x * c, ys = y * s, yc = y * c, xs = x * s;
+  x = xc - ys;
+  y = yc + xs;
+}
+
+// a, b: the first and the second elements of eight pairs, whose entries begin at `entry`.
+__device__ __forceinline__ void rotate_halves(const RotaryTable& table, int entry, Chunk& a, Chunk& b) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 t = turn[i];
-    const float x = a.v[i], y = b.v[i];
-    const float xc = x * t.x, ys = y * t.y, yc = y * t.x, xs = x * t.y;
-    a.v[i] = xc - ys;
-    b.v[i] = yc + xs;
+  for (int i = 0; i < 4; ++i) {
+    const float4 t = table.pair(entry + 2 * i);
+    rotate_pair(t.x, t.y, a.v[2 * i], b.v[2 * i]);
+    rotate_pair(t.z, t.w, a.v[2 * i + 1], b.v[2 * i + 1]);
   }
 }
 
 // Four pairs of neighbours.
-__device__ __forceinline__ void rotate_neighbours(const float2* turn, Chunk& a) {
-#pragma clang fp contract(off)
+__device__ __forceinline__ void rotate_neighbours(const RotaryTable& table, int entry, Chunk& a) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = turn[i];
-    const float x = a.v[2 * i], y = a.v[2 * i + 1];
-    const float xc = x * t.x, ys = y * t.y, yc = y * t.x, xs = x * t.y;
-    a.v[2 * i] = xc - ys;
-    a.v[2 * i + 1] = yc + xs;
+  for (int i = 0; i < 2; ++i) {
+    const float4 t = table.pair(entry + 2 * i);
+    rotate_pair(t.x, t.y, a.v[4 * i], a.v[4 * i + 1]);
+    rotate_pair(t.z, t.w, a.v[4 * i + 2], a.v[4 * i + 3]);
   }
 }
 
