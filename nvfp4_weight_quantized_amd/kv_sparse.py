@@ -11,6 +11,7 @@ Every call only enqueues kernels on the current stream of its tensors' device an
 
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
@@ -136,7 +137,7 @@ def kv_select(index: NvFp4KvIndex, q: torch.Tensor, query_offsets: torch.Tensor,
     if not (first >= 0 and last >= 1 and first + last <= top_k <= MAX_SELECTED):
         raise ValueError(f"top_k {top_k}, first {first}, last {last}: expected first >= 0, last >= 1 and first + last <= "
                          f"top_k <= {MAX_SELECTED}")
-    selected = torch.empty((t, kv_heads, top_k), dtype=_I32, device=dev)
+    selected = torch.empty(t, kv_heads, top_k, dtype=_I32, device=dev)
     with _on(dev.index):
         st = L.lib().moe_nvfp4_kv_select(x, q.data_ptr(), stride, t, heads, query_offsets.data_ptr(),
                                          seq_lens.data_ptr(), r, block_table.data_ptr(), width, top_k, first, last,
@@ -146,6 +147,7 @@ def kv_select(index: NvFp4KvIndex, q: torch.Tensor, query_offsets: torch.Tensor,
     return selected
 
 
+@functools.lru_cache(maxsize=1024)      # a call's sizes come again every step
 def kv_sparse_attention_workspace_size(T: int, R: int, heads: int, kv_heads: int, head_dim: int, page_size: int,
                                        top_k: int) -> int:
     """Workspace bytes of ``kv_sparse_attention`` for T query rows of R requests."""
@@ -181,9 +183,9 @@ def kv_sparse_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: tor
     lib, lse = L.lib(), None
     if out is None:
         attend = lib.moe_nvfp4_kv_sparse_attention_fill
-        out = torch.empty((t, heads, dim), dtype=_BF16, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(t, heads, dim, dtype=_BF16, device=dev)
         if return_lse:
-            lse = torch.empty((t, heads), dtype=torch.float32, device=dev)
+            lse = torch.empty(t, heads, dtype=torch.float32, device=dev)
     else:
         attend = lib.moe_nvfp4_kv_sparse_attention
         _need(out, "out", _BF16, 3)
@@ -195,7 +197,7 @@ def kv_sparse_attention(cache: NvFp4KvCache, q: torch.Tensor, query_offsets: tor
         _need(workspace, "workspace", torch.uint8)
         _same_device(cache._pages, ("workspace", workspace))
     else:
-        need = lib.moe_nvfp4_kv_sparse_attention_workspace_size(t, r, heads, kv_heads, dim, c.page_size, top_k)
+        need = kv_sparse_attention_workspace_size(t, r, heads, kv_heads, dim, c.page_size, top_k)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     with _on(dev.index):

@@ -130,7 +130,8 @@ def _out(out: Optional[torch.Tensor], x: torch.Tensor, name: str, shape, dim: in
     """A new tensor, or a given one that is checked: (tensor, token stride)."""
     tokens, heads = shape
     if out is None:
-        return torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev), heads * dim
+        return (torch.empty_like(x) if x.is_contiguous() else
+                torch.empty(tokens, heads, dim, dtype=torch.bfloat16, device=dev)), heads * dim
     t, h, stride = _rows(out, "out", dim, dev)
     if t != tokens or h != heads:
         raise ValueError(f"out: expected {(tokens, heads, dim)}, got {tuple(out.shape)}")
