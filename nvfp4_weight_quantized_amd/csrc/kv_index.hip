@@ -78,36 +78,41 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvf
     for (int k = 0; k < NS; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+    // all units' loads first
+    uint32_t w[kUnits][2 * NS], sc[kUnits][NS / 2];
 #pragma unroll
     for (int x = 0; x < kUnits; ++x) {
-      const int u = u0 + x * W;
-      if (u >= units) continue;
-      const uint8_t* unit = first + (size_t)u * U::kBytes;
-      uint32_t w[2 * NS], sc[NS / 2];
+      if (u0 + x * W >= units) break;
+      const uint8_t* unit = first + (size_t)(u0 + x * W) * U::kBytes;
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
         const uint4 y = *reinterpret_cast<const uint4*>(unit + 1024 * j + 16 * lane);
-        w[4 * j] = y.x, w[4 * j + 1] = y.y, w[4 * j + 2] = y.z, w[4 * j + 3] = y.w;
+        w[x][4 * j] = y.x, w[x][4 * j + 1] = y.y, w[x][4 * j + 2] = y.z, w[x][4 * j + 3] = y.w;
       }
 #pragma unroll
       for (int j = 0; j < NS / 2; ++j)
-        sc[j] = *reinterpret_cast<const uint32_t*>(unit + U::kKScales + (16 * (u4 >> 1) + n16) * 2 * NS + 4 * j);
+        sc[x][j] = *reinterpret_cast<const uint32_t*>(unit + U::kKScales + (16 * (u4 >> 1) + n16) * 2 * NS + 4 * j);
+    }
+#pragma unroll
+    for (int x = 0; x < kUnits; ++x) {
+      const int u = u0 + x * W;
+      if (u >= units) break;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const bool seen = kKvUnit * u + 16 * half + n16 < held;
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
           const int word = half * NS + k, byte = word & 3;
-          const int bits = (int)sc[word >> 2];
+          const int bits = (int)sc[x][word >> 2];
           const float f8 = byte == 0   ? __builtin_amdgcn_cvt_f32_fp8(bits, 0)
                            : byte == 1 ? __builtin_amdgcn_cvt_f32_fp8(bits, 1)
                            : byte == 2 ? __builtin_amdgcn_cvt_f32_fp8(bits, 2)
                                        : __builtin_amdgcn_cvt_f32_fp8(bits, 3);
           const float f = seen ? 1024.f * f8 : 0.f;
-          const f32x2 e[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 0),
-                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 1),
-                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 2),
-                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[word], 1.0f, 3)};
+          const f32x2 e[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[x][word], 1.0f, 0),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[x][word], 1.0f, 1),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[x][word], 1.0f, 2),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[x][word], 1.0f, 3)};
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[k][i] = __fmaf_rn(e[i >> 1][i & 1], f, acc[k][i]);
         }
