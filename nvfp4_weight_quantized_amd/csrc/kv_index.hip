@@ -173,8 +173,6 @@ struct SelectShape {
 
 constexpr int kOne = 0;
 constexpr int group_tokens(int HS) { return HS == kOne ? 1 : 16 / HS; }
-// Chunks of 16 pages in a wave's ring.
-constexpr int select_ring(int D, bool wide) { return D == 256 && wide ? 1 : 2; }
 
 // The rows of the workgroup's tokens in 8 bits: operand bytes codes[block][step][lane][16] and tops[block][row].
 template <int D, int HS>
@@ -253,20 +251,20 @@ __device__ __forceinline__ int page_piece(int n, int x) {
 
 // Keys of the pages [0, pages) for the workgroup's tokens: keys[token * stride + page], 0 for a page that is not in the
 // cache.  A wave takes 64 pages at a time, a lane's page of the table and its scale first, then the codes 16 pages at a
-// time straight to LDS, through a ring of its own (`ring` of RING chunks): neighbouring lanes ask for pieces of one
+// time straight to LDS, into a place of its own in `stage`: neighbouring lanes ask for pieces of one
 // page, where as operands they would each touch another page's line, and the address unit looks up one line a cycle
 // (one row on 2048 pages: 11 us of products in that form).
 // rows() makes the operands of the rows while the first pages are on their way.
-template <int D, int HS, int NW, int RING, typename Rows>
+template <int D, int HS, int NW, typename Rows>
 __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const int32_t* __restrict__ table, int h,
                                               int pages, const SelectShape& sh, const int8_t* codes, const float* tops,
-                                              uint32_t* keys, uint8_t* ring, Rows&& rows) {
+                                              uint32_t* keys, uint8_t* stage, Rows&& rows) {
   constexpr int KS = D / 64, TPL = HS == kOne ? 1 : 4 / HS;      // tokens of a lane
   constexpr int LPP = D / 16, PPL = 64 / LPP, LOADS = 16 / PPL;  // lanes per page, pages per load, loads per chunk
   using lds_bytes = __attribute__((address_space(3))) uint8_t*;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q4 = lane >> 4, n16 = lane & 15, hkv = p.index.kv_heads;
-  const lds_bytes mine = (lds_bytes)ring + wave * RING * 16 * D;
+  const lds_bytes mine = (lds_bytes)stage + wave * 16 * D;
   struct Batch {
     int page;         // of this lane; 0 where it is not in the cache
     uint32_t scale;   // its bits, kBadPage there
@@ -288,9 +286,9 @@ __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const in
               16 * ((lane % LPP) ^ ((n / (256 / D)) & (LPP - 1)));
   }
   const uint32_t page_bytes = hkv * D;
-  // chunk x of a batch into ring slot `slot`
-  auto issue = [&](const Batch& b, int x, int slot) {
-    const uint32_t dst = (uint32_t)(uintptr_t)mine + slot * 16 * D;
+  // chunk x of a batch
+  auto issue = [&](const Batch& b, int x) {
+    const uint32_t dst = (uint32_t)(uintptr_t)mine;
 #pragma unroll
     for (int t = 0; t < LOADS; ++t)
       direct_load16_from(from[t] + (uint64_t)(uint32_t)__shfl(b.page, 16 * x + t * PPL + lane / LPP) * page_bytes,
@@ -302,10 +300,7 @@ __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const in
   };
   const int first = 64 * wave, step = 64 * NW;
   Batch now = load_batch(first), next = now;
-  if (first < pages) {
-#pragma unroll
-    for (int i = 0; i < RING; ++i) issue(now, i, i);
-  }
+  if (first < pages) issue(now, 0);
   rows();
   __syncthreads();
   for (int j0 = first; j0 < pages; j0 += step, now = next) {
@@ -314,18 +309,14 @@ __device__ __forceinline__ void select_scores(const KvSelectProblem& p, const in
     float score = 0.f;      // one token: of page j0 + lane
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      constexpr int kLater = (RING - 1) * LOADS;
-      if (x + RING - 1 < 4 || more) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kLater) : "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-      const int slot = x % RING;
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
       i32x4 b[KS];
 #pragma unroll
       for (int k = 0; k < KS; ++k)
-        b[k] = *reinterpret_cast<const __attribute__((address_space(3))) i32x4*>(
-            mine + slot * 16 * D + page_piece<D>(n16, 4 * k + q4));
-      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");      // the slot has been read
-      if (x + RING < 4) issue(now, x + RING, slot);
-      else if (more) issue(next, x + RING - 4, slot);
+        b[k] = *reinterpret_cast<const __attribute__((address_space(3))) i32x4*>(mine + page_piece<D>(n16, 4 * k + q4));
+      asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");      // the chunk has been read
+      if (x < 3) issue(now, x + 1);
+      else if (more) issue(next, 0);
       const int j = j0 + 16 * x + n16;
       const uint32_t scale = HS == kOne ? 0u : __shfl(now.scale, 16 * x + n16);
       for (int grp = 0; grp < sh.groups; ++grp) {
@@ -375,175 +366,164 @@ __device__ __forceinline__ void halve(uint32_t* lo, uint32_t hi, int want, int* 
   }
 }
 
-// The pages of one token: those listed always, and the `room` largest keys of the others.  W waves (1, or all of the
-// workgroup; `me` of them) hold the keys in registers, each a run of pages.  The room-th largest of a wave's 64 largest
-// keys of a lane bounds the threshold from below and leaves little more than `room` candidates, found by halving over
-// one key per lane; of several waves' bounds the largest holds.  The candidates go to a list in order of pages, where
-// one wave finds the threshold itself.  Where that is too long (many equal keys, more than 64 wanted) or there are few
-// pages the registers are searched instead, by all waves together.
-constexpr int kSelectWaves = 16, kManyWaves = 8;      // of a workgroup: one token or many pages, several tokens
+// The pages of one token, chosen by one wave: those listed always, and the `room` largest keys of the others.
+// The keys are dealt into 64 sets, one per lane (256 of many pages or for room > 64, 1024 of many for more), whose room-th
+// largest maximum bounds the threshold from below: it leaves little more than `room` candidates (44 for 32 of many, 177 for
+// 128), found by halving over 1, 4 or 16 maxima per lane.  Their pages go to a list of `cap` places, in order, over which the threshold itself is found; where they are
+// more (many equal keys, most of the pages wanted), and where there are few pages, over all keys.  HELD: up to so many pages
+// the keys stay in registers (0: each pass reads them).  One token: 2048 (2048 pages, a row of 32/4 heads, top 64: 12.8
+// against 14.9 us); several: 1024, since 2048 cost a compute unit the third workgroup (chunks
+// of 1024 and 301 rows on 60000 and 20000 positions, 32/8 heads, top 32: 39.7 against 48.2 us).
+constexpr int kSelectWaves = 16, kManyWaves = 8;      // of a workgroup: one token, several tokens
+constexpr int held_pages(int HS) { return HS == kOne ? 2048 : 1024; }
 
-template <int W>
-__device__ __forceinline__ void select_take(const KvSelectProblem& p, uint32_t* keys, int stride, int own, int me,
-                                            int* meet, int& turn, int32_t* out) {
-  constexpr int VPL = W == 1 ? 32 : 16, STEP = 4, LIST = W == 1 ? 4 : 16;      // registers; LIST for the list
+template <int HELD>
+__device__ __forceinline__ void select_take(const KvSelectProblem& p, const uint32_t* keys, int own, uint16_t* list,
+                                            int cap, int32_t* out) {
+  constexpr bool REGS = HELD > 0;
+  constexpr int VPL = REGS ? HELD / 64 : 8, STEP = 4, SETS = REGS ? 4 : 16, FEW = 4;
   const int lane = threadIdx.x & 63, width = p.step.width, count = min(own + 1, width);
   const uint64_t below = lane == 0 ? 0 : ~0ull >> (64 - lane);
   const int head = min(p.first, count), tail = min(max(own + 1 - p.last, head), count);      // [head, tail) by score
   const int beyond = max(own + 1 - max(width, max(own + 1 - p.last, 0)), 0);      // listed always, behind the table
-  const int room = p.top_k - beyond - head - (count - tail), base = W == 1 ? 0 : 64 * VPL * me;
+  const int room = p.top_k - beyond - head - (count - tail);
+  auto key_at = [&](int j) { return j >= head && j < tail ? keys[j] : 0u; };
   uint32_t v[VPL];
+  auto load = [&](int j0) {
 #pragma unroll
-  for (int s = 0; s < VPL / STEP; ++s) {
-    if (base + 64 * STEP * s < count) {
+    for (int s = 0; s < VPL; s += STEP) {
+      if (j0 + 64 * s < count) {
 #pragma unroll
-      for (int i = STEP * s; i < STEP * (s + 1); ++i) {
-        const int j = base + 64 * i + lane;
-        v[i] = j >= head && j < tail ? keys[j] : 0u;
+        for (int i = s; i < s + STEP; ++i) v[i] = key_at(j0 + 64 * i + lane);
+      } else {
+#pragma unroll
+        for (int i = s; i < s + STEP; ++i) v[i] = 0u;
       }
-    } else {
-#pragma unroll
-      for (int i = STEP * s; i < STEP * (s + 1); ++i) v[i] = 0u;
     }
-  }
-  // sum and largest of the waves' values, and the sum of those before this wave
-  auto join = [&](int x, int* before, uint32_t* most) {
-    if (W == 1) {
-      if (before) *before = 0;
-      if (most) *most = (uint32_t)x;
-      return x;
-    }
-    int* at = meet + (turn ^= W);      // two sets of W in turn, so that one barrier is enough
-    if (lane == 0) at[me] = x;
-    __syncthreads();
-    int sum = 0, low = 0;
-    uint32_t top = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const int y = __builtin_amdgcn_readfirstlane(at[w]);
-      low += w < me ? y : 0;
-      sum += y;
-      top = max(top, (uint32_t)y);
-    }
-    if (before) *before = low;
-    if (most) *most = top;
-    return sum;
   };
-  auto own_at_least = [&](uint32_t x) {
+  // f(number of the key in its lane, key, page) for every key
+  auto each = [&](auto&& f) {
+    for (int j0 = 0; j0 < (REGS ? 1 : count); j0 += 64 * VPL) {
+      if (!REGS) load(j0);
+#pragma unroll
+      for (int s = 0; s < VPL; s += STEP)
+        if (j0 + 64 * s < count) {
+#pragma unroll
+          for (int i = s; i < s + STEP; ++i) f(i, v[i], j0 + 64 * i + lane);
+        }
+    }
+  };
+  auto at_least = [&](uint32_t x) {
     int n = 0;
-#pragma unroll
-    for (int s = 0; s < VPL / STEP; ++s)
-      if (base + 64 * STEP * s < count) {
-#pragma unroll
-        for (int i = STEP * s; i < STEP * (s + 1); ++i) n += __popcll(__ballot(v[i] >= x));
-      }
+    each([&](int, uint32_t key, int) { n += __popcll(__ballot(key >= x)); });
     return n;
   };
-  uint32_t most = 0;
+  if (REGS) load(0);
+  uint32_t most[SETS], top = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) most = max(most, v[i]);
-  uint32_t lo = 1, hi = wave_max_u32(most) + 1;
+  for (int i = 0; i < SETS; ++i) most[i] = 0;
+  if (REGS) {
+    each([&](int i, uint32_t key, int) { most[i % SETS] = max(most[i % SETS], key); });
+  } else {
+    for (int j0 = 0; j0 < count; j0 += 64 * SETS)
+#pragma unroll
+      for (int i = 0; i < SETS; ++i) most[i] = max(most[i], key_at(j0 + 64 * i + lane));
+  }
+  const bool few = room <= 32 * FEW;
+  if (few) {
+#pragma unroll
+    for (int i = FEW; i < SETS; ++i) most[i % FEW] = max(most[i % FEW], most[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < SETS; ++i) top = max(top, most[i]);
+  uint32_t lo = 1;
+  const uint32_t hi = wave_max_u32(top) + 1;
   int above = 0;
-  if (room > 0 && room <= 64) {
-    auto lanes = [&](uint32_t x) { return (int)__popcll(__ballot(most >= x)); };
-    if (lanes(1) >= room) halve(&lo, hi, room, &above, lanes);
-  }
-  if (W > 1) {
-    join((int)lo, nullptr, &lo);
-    join((int)hi, nullptr, &hi);
-  }
-  int start;      // candidates of the waves before
-  const int found = join(own_at_least(lo), &start, nullptr);
-  const int want = max(min(room, found), 0);      // found >= room, or lo = 1 and these are all
-  const bool listed = count > 256 && found <= min(64 * LIST, stride / 2) && want > 0;
-  if (listed) {
-    // candidates in order of pages: key and page
-    uint32_t* list = keys;
-    int* pages = reinterpret_cast<int*>(keys) + stride / 2;
+  auto sets = [&](uint32_t x) {
+    if (REGS && room <= 64) return (int)__popcll(__ballot(top >= x));
+    int n = 0;
 #pragma unroll
-    for (int s = 0; s < VPL / STEP; ++s)
-      if (base + 64 * STEP * s < count) {
+    for (int i = 0; i < FEW; ++i) n += __popcll(__ballot(most[i] >= x));
+    if (!few) {
 #pragma unroll
-        for (int i = STEP * s; i < STEP * (s + 1); ++i) {
-          const bool in = v[i] >= lo;
-          const uint64_t all = __ballot(in);
-          const int at = start + __popcll(all & below);
-          if (in) list[at] = v[i], pages[at] = base + 64 * i + lane;
-          start += __popcll(all);
-        }
-      }
-    if (W > 1) {
-      __syncthreads();
-      if (me != 0) return;
+      for (int i = FEW; i < SETS; ++i) n += __popcll(__ballot(most[i] >= x));
     }
-    uint32_t u[LIST];
+    return n;
+  };
+  const bool bounded = room > 0 && (few || !REGS) && sets(1) >= room, list_them = bounded && count > 256;
+  if (bounded) halve(&lo, hi, room, &above, sets);
+  int found = 0;      // candidates; all keys where there is no bound
+  if (list_them) {
+    each([&](int, uint32_t key, int j) {
+      const bool in = key >= lo;
+      const uint64_t all = __ballot(in);
+      const int at = found + __popcll(all & below);
+      if (in && at < cap) list[at] = (uint16_t)j;
+      found += __popcll(all);
+    });
+  } else {
+    found = at_least(lo);
+  }
+  const int want = max(min(room, found), 0);      // found >= room, or lo = 1 and these are all
+  const bool listed = list_them && found <= min(cap, 256);
+  uint32_t u[4];
+  int page[4];
+  above = found;
+  if (listed) {
 #pragma unroll
-    for (int i = 0; i < LIST; ++i) u[i] = 64 * i + lane < found ? list[64 * i + lane] : 0u;
-    above = found;
+    for (int i = 0; i < 4; ++i) {
+      const bool in = 64 * i + lane < found;
+      page[i] = in ? list[64 * i + lane] : 0;
+      u[i] = in ? keys[page[i]] : 0u;
+    }
     if (found > want)
       halve(&lo, hi, want, &above, [&](uint32_t x) {
         int n = 0;
 #pragma unroll
-        for (int s = 0; s < LIST; s += 2)
-          if (64 * s < found) n += __popcll(__ballot(u[s] >= x)) + __popcll(__ballot(u[s + 1] >= x));
+        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(u[i] >= x));
         return n;
       });
-    int ties = want - above, filled = head;      // of the keys equal to lo, the first
-    const uint32_t sure = ties > 0 ? lo + 1 : lo;
-#pragma unroll
-    for (int i = 0; i < LIST; ++i) {
-      if (64 * i < found) {
-        const bool tie = u[i] == lo && ties > 0;
-        const uint64_t tied = __ballot(tie);
-        const bool chosen = (u[i] != 0 && u[i] >= sure) || (tie && __popcll(tied & below) < ties);
-        const uint64_t taken = __ballot(chosen);
-        if (chosen) out[filled + __popcll(taken & below)] = pages[64 * i + lane];
-        filled += __popcll(taken);
-        ties -= min(ties, (int)__popcll(tied));
-      }
-    }
-  } else {
-    above = found;
-    if (want > 0 && found > want)
-      halve(&lo, hi, want, &above, [&](uint32_t x) { return join(own_at_least(x), nullptr, nullptr); });
-    const int ties = want - above;
-    const uint32_t sure = ties > 0 ? lo + 1 : lo;
-    int tied_before, filled, left = 0;      // left: ties that this wave takes
-    if (W > 1 || ties > 0) {
-      const int mine = ties > 0 ? own_at_least(lo) - own_at_least(lo + 1) : 0;
-      join(mine, &tied_before, nullptr);
-      left = max(min(ties - tied_before, mine), 0);
-    }
-    join((want > 0 ? own_at_least(sure) : 0) + left, &filled, nullptr);
-    filled += head;
-#pragma unroll
-    for (int s = 0; s < VPL / STEP; ++s)
-      if (want > 0 && base + 64 * STEP * s < count) {
-#pragma unroll
-        for (int i = STEP * s; i < STEP * (s + 1); ++i) {
-          const bool tie = v[i] == lo && left > 0;
-          const uint64_t tied = __ballot(tie);
-          const bool chosen = (v[i] != 0 && v[i] >= sure) || (tie && __popcll(tied & below) < left);
-          const uint64_t taken = __ballot(chosen);
-          if (chosen) out[filled + __popcll(taken & below)] = base + 64 * i + lane;
-          filled += __popcll(taken);
-          left -= min(left, (int)__popcll(tied));
-        }
-      }
-    if (me != 0) return;
+  } else if (list_them && !REGS && found <= cap) {
+    if (found > want)
+      halve(&lo, hi, want, &above, [&](uint32_t x) {
+        int n = 0;
+        for (int i = lane; i - lane < found; i += 64) n += __popcll(__ballot(i < found && keys[list[min(i, found - 1)]] >= x));
+        return n;
+      });
+  } else if (want > 0 && found > want) {
+    halve(&lo, hi, want, &above, at_least);
   }
-  // one wave: the pages listed always, own pages behind the table among them (the attention makes such rows NaN)
+  // chosen: keys from `sure` on, and the first `ties` of those equal to lo
+  int ties = want - above, filled = head;
+  const uint32_t sure = ties > 0 ? lo + 1 : lo;
+  auto write = [&](uint32_t key, int j) {
+    const bool tie = key == lo && ties > 0;
+    const uint64_t tied = __ballot(tie);
+    const bool chosen = (key != 0 && key >= sure) || (tie && __popcll(tied & below) < ties);
+    const uint64_t taken = __ballot(chosen);
+    if (chosen) out[filled + __popcll(taken & below)] = j;
+    filled += __popcll(taken);
+    ties -= min(ties, (int)__popcll(tied));
+  };
+  if (listed) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (64 * i < found) write(u[i], page[i]);
+  } else if (want > 0) {
+    each([&](int, uint32_t key, int j) { write(key, j); });
+  }
+  // own pages behind the table are listed all the same: the attention makes such rows NaN
   for (int i = lane; i < head; i += 64) out[i] = i;
   const int end = head + want + count - tail;
   for (int i = head + want + lane; i < p.top_k; i += 64)
     out[i] = i < end ? tail + (i - head - want) : i - end < beyond ? own + 1 - beyond + (i - end) : -1;
 }
 
-template <int D, int HS, bool WIDE>
-__global__ __launch_bounds__(64 * (WIDE || HS == kOne ? kSelectWaves : kManyWaves)) void kv_select_kernel(KvSelectProblem p, SelectShape sh) {
-  constexpr int NW = WIDE || HS == kOne ? kSelectWaves : kManyWaves, RING = select_ring(D, WIDE);
+template <int D, int HS, bool REGS>
+__global__ __launch_bounds__(64 * (HS == kOne ? kSelectWaves : kManyWaves)) void kv_select_kernel(KvSelectProblem p,
+                                                                                                  SelectShape sh) {
+  constexpr int NW = HS == kOne ? kSelectWaves : kManyWaves;
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ int meet[2 * kSelectWaves];
   const KvStep& s = p.step;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), hkv = p.index.kv_heads;
   if (blockIdx.x >= sh.work_groups) {      // rows of no request
@@ -564,34 +544,34 @@ __global__ __launch_bounds__(64 * (WIDE || HS == kOne ? kSelectWaves : kManyWave
   uint32_t* keys = reinterpret_cast<uint32_t*>(lds);
   float* tops = reinterpret_cast<float*>(keys + (size_t)sh.tokens * sh.stride);
   int8_t* codes = reinterpret_cast<int8_t*>(tops + 16 * sh.blocks * sh.groups);
+  uint8_t* stage = reinterpret_cast<uint8_t*>(codes + (size_t)16 * sh.blocks * sh.groups * D);
   if (pages > 0) {
-    select_scores<D, HS, NW, RING>(p, s.table + (size_t)q.r * s.width, h, pages, sh, codes, tops, keys,
-                                   reinterpret_cast<uint8_t*>(codes + (size_t)16 * sh.blocks * sh.groups * D),
-                                   [&]() { select_rows<D, HS>(p, q, h, tok0, sh, codes, tops); });
+    select_scores<D, HS, NW>(p, s.table + (size_t)q.r * s.width, h, pages, sh, codes, tops, keys, stage,
+                             [&]() { select_rows<D, HS>(p, q, h, tok0, sh, codes, tops); });
     __syncthreads();
   }
-  int turn = 0;
-  for (int t = WIDE ? 0 : wave; t < toks; t += WIDE ? 1 : NW) {
+  // the lists lie where the pages' codes came in: a wave's own place, or all of them for one token
+  uint16_t* list = reinterpret_cast<uint16_t*>(stage + wave * 16 * D);
+  for (int t = wave; t < toks; t += NW) {
     const int pos = pos0 + t;
     int32_t* out = p.selected + ((size_t)(q.row0 + tok0 + t) * hkv + h) * p.top_k;
     if (pos < 0) {
-      for (int i = WIDE ? tid : tid & 63; i < p.top_k; i += WIDE ? 64 * NW : 64) out[i] = -1;
+      for (int i = tid & 63; i < p.top_k; i += 64) out[i] = -1;
     } else {
-      select_take<WIDE ? NW : 1>(p, keys + (size_t)t * sh.stride, sh.stride, pos / s.page_size, WIDE ? wave : 0, meet, turn, out);
+      select_take<REGS ? held_pages(HS) : 0>(p, keys + (size_t)t * sh.stride, pos / s.page_size, list, HS == kOne ? NW * 8 * D : 8 * D, out);
     }
   }
 }
 
-// LDS of a workgroup, and what fits: a compute unit holds 160 KB, two workgroups of several tokens are wanted on it.
-constexpr int kSelectLds = 150 << 10, kSelectHalf = 76 << 10;
+// LDS of a workgroup, and what fits: a compute unit holds 160 KB, three workgroups of several groups of tokens are wanted
+// on it (chunks of 1024 and 301 rows on 60000 and 20000 positions, 32/8 heads of 128, top 32: 39.2 us; two workgroups, with
+// another 16 pages per wave on their way, 47.6).
+constexpr int kSelectLds = 150 << 10, kSelectThird = 52 << 10;
 
-size_t select_lds(const SelectShape& s, int32_t D, int waves, bool wide) {
+size_t select_lds(const SelectShape& s, int32_t D, int waves) {
   return (size_t)s.tokens * s.stride * 4 + (size_t)16 * s.blocks * s.groups * (4 + D) +
-         (size_t)waves * select_ring(D, wide) * 16 * D;
+         (size_t)waves * 16 * D;
 }
-
-// Pages from which a token's keys are held by all waves of the workgroup.
-bool select_wide(int32_t width) { return width > 2048; }
 
 // One token per workgroup where the step may be of single tokens (T <= R); otherwise as many groups of tokens as leave
 // 512 workgroups and fit, since all of them share what a workgroup reads of the index.
@@ -605,8 +585,7 @@ int select_heads(const KvSelectProblem& p, SelectShape* s) {
     for (int groups = 4; groups >= 1; groups /= 2) {
       s->groups = groups;
       s->tokens = groups * group_tokens(HS);
-      const bool wide = select_wide(p.step.width);
-      const bool fits = select_lds(*s, D, wide ? kSelectWaves : kManyWaves, wide) <= (groups > 1 ? kSelectHalf : kSelectLds);
+      const bool fits = select_lds(*s, D, kManyWaves) <= (groups > 1 ? kSelectThird : kSelectLds);
       if (fits && (groups == 1 || T / s->tokens * hkv >= 512)) return HS;
     }
   }
@@ -645,16 +624,14 @@ moe_status_t launch_kv_select(const KvSelectProblem& p, hipStream_t stream) {
   const int64_t items = R == 0 ? 0 : std::min(T, T / s.tokens + std::min(T, R)) * p.index.kv_heads;
   s.work_groups = (uint32_t)items;
   const dim3 grid((unsigned)(items + fill));
-  const bool wide = select_wide(p.step.width);
-  const size_t bytes = select_lds(s, p.index.head_dim, wide || HS == kOne ? kSelectWaves : kManyWaves, wide);
+  const size_t bytes = select_lds(s, p.index.head_dim, HS == kOne ? kSelectWaves : kManyWaves);
   with_head_dim(p.index.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
     auto launch = [&](auto heads) {
       constexpr int H = decltype(heads)::value;
-      if (wide)
-        hipLaunchKernelGGL((kv_select_kernel<D, H, true>), grid, dim3(1024), bytes, stream, p, s);
-      else
-        hipLaunchKernelGGL((kv_select_kernel<D, H, false>), grid, dim3(64 * (H == kOne ? kSelectWaves : kManyWaves)), bytes, stream, p, s);
+      const dim3 block(64 * (H == kOne ? kSelectWaves : kManyWaves));
+      if (p.step.width <= held_pages(H)) hipLaunchKernelGGL((kv_select_kernel<D, H, true>), grid, block, bytes, stream, p, s);
+      else hipLaunchKernelGGL((kv_select_kernel<D, H, false>), grid, block, bytes, stream, p, s);
     };
     if (HS == kOne) launch(DimC<kOne>{});
     else if (HS == 1) launch(DimC<1>{});
