@@ -27,6 +27,11 @@ struct SparseTiles {
   float* ml;       // [tile][split][2][bm]: reference maximum, sum
 };
 
+// Bound by memory where each page is read by one tile: 64 requests on up to 16000 positions, 64/8 heads of dimension 128, 48
+// pages of 64 each (210 MB) 42.3 us, 5.0 TB/s, the rate of a copy, with loads that pass the caches by.  Bound by the
+// vector unit where tokens have lists of their own: 1325 rows, 32/8 heads, 24 pages each, 200 us, the vector unit 64% busy
+// with about 300 instructions per unit (172 of them turn codes into operands) beside 32 matrix instructions.
+
 constexpr int kEntries = kKvMaxSelected;      // of a tile's lists
 
 // The tile `index` (over requests, tokens and parts) of the step: its request, first token and part.
@@ -489,10 +494,21 @@ __global__ __launch_bounds__(256) void kv_sparse_join_kernel(KvSparseProblem p, 
   if (a.lse && lane == 0) a.lse[dst] = any ? kLn2 * (top + (__builtin_amdgcn_logf(sum) - kPExp)) : -INFINITY;
 }
 
-constexpr int kPlaces = 512;      // workgroups of four waves that splits aim at
-constexpr int64_t kWideRows = 16384;
+// The launch of a call, from its sizes.  Measured on random lists of which neighbouring tokens share about half, 32/8 heads
+// of dimension 128, pages of 64, top 24, contexts of 30000 unless said; other side in brackets.
+//   Tokens per tile: one while that makes at most kPlaces tiles, which then end sooner (64 tokens 23.3 [28.3] us; 17 requests
+//   of 2 to 5 tokens, 18/3 heads of 64, 10.1 [11.9]), else as many as the rows hold.
+//   Rows per tile: 32 with kWideRows rows over all heads, for groups of 4 heads or more (2048 tokens 228 [239] us, 1325 tokens
+//   of two requests 200 [208]; 512 tokens 70.0 [76.7], 512 of 64/4 heads 65.3 [72.2] with 16; 512 of 16/16 heads of 64
+//   48.9 [101], where every token looks into 31 other lists).
+//   Splits: few tiles with 48 units of dimension 128 or more (one token, top 32, 32/4 heads, 11.4 [17.4] us; top 64 13.4
+//   [27.6]; 8 tokens, top 32, 15.6 [18.2]; dimension 256, 16/2 heads, top 32, 15.2 [28.6]; but top 16 12.3 whole, and two
+//   launches).
+//   Waves: eight where the tiles alone leave places free and are not short (64 requests of 64/8 heads, top 48, 42.4 [47.7]
+//   us, 48 of them 43.9 [47.1]; the drafts 10.1 [11.0]; but 64 requests, top 16, 20.7 with four [23.1]).
+constexpr int kPlaces = 512;      // workgroups of four waves
+constexpr int64_t kWideRows = 40000;
 
-// Tiles of a call.  A token per tile while that leaves the card unfilled, else as many as the rows hold.
 struct SparsePlan {
   SparseTiles t;
   int64_t tiles;      // bound on their number, over requests, tokens and parts
@@ -503,16 +519,16 @@ struct SparsePlan {
 SparsePlan sparse_plan(int32_t T, int32_t R, int32_t G, int32_t hkv, int32_t D, int32_t page_size, int32_t top_k) {
   SparsePlan p{};
   const bool many = (int64_t)T * hkv * ((G + 31) / 32) > kPlaces;
-  p.t.bm = G > 16 || (many && D != 256 && (int64_t)T * hkv * G >= kWideRows) ? 32 : 16;
+  p.t.bm = G > 16 || (many && D != 256 && G >= 4 && (int64_t)T * hkv * G >= kWideRows) ? 32 : 16;
   p.t.parts = (G + p.t.bm - 1) / p.t.bm;
   p.t.tokens = many ? std::max(1, std::min(p.t.bm / G, kEntries / top_k)) : 1;
   p.t.page_units = (uint32_t)((((uint64_t)1 << 32) + page_size / kKvUnit - 1) / (page_size / kKvUnit));
   p.tiles = std::min((int64_t)T, (int64_t)T / p.t.tokens + std::min(T, R)) * p.t.parts;
   const int64_t most = (int64_t)p.t.tokens * top_k * (page_size / kKvUnit), grid = std::max(p.tiles * hkv, (int64_t)1);
-  p.waves = p.t.bm == 16 && D != 256 && grid <= kPlaces ? 8 : 4;
   p.t.splits = 1;
-  if (most > 64 && grid * 2 * p.waves <= 4 * kPlaces)
-    p.t.splits = (int)std::min(4 * kPlaces / p.waves / grid, (most + p.waves - 1) / p.waves);
+  if (most * D >= 48 * 128 && 4 * grid <= kPlaces) p.t.splits = (int)std::min(kPlaces / grid, (most + 3) / 4);
+  const bool eight = p.t.splits == 1 && p.t.bm == 16 && D != 256;
+  p.waves = eight && (2 * grid <= kPlaces || (grid <= kPlaces && most >= 64)) ? 8 : 4;
   if (p.t.splits > 1) {
     p.o_bytes = (size_t)grid * p.t.splits * p.t.bm * D * 4;
     p.bytes = p.o_bytes + (size_t)grid * p.t.splits * 2 * p.t.bm * 4;
