@@ -253,7 +253,7 @@ def check_sparse(c, lists, **kw):
     assert np.array_equal(np.isneginf(got_lse[sel]), empty) and np.all(got[sel][empty] == 0)
     over = np.abs(got[sel] - ref[sel]) / tol
     assert np.all(over <= 1), f"out: {np.nanmax(over)} times the bound"
-    over = np.abs(got_lse[sel] - ref_lse[sel])[~empty] / tol_lse[~empty]
+    over = np.abs(got_lse[sel][~empty] - ref_lse[sel][~empty]) / tol_lse[~empty]
     assert np.all(over <= 1), f"lse: {over.max()} times the bound"
     return out, lse
 
