@@ -47,7 +47,8 @@ __device__ __forceinline__ int row_sums(int (&v)[16]) {
 // W waves per touched page and head take every W-th unit.  A lane holds one position (of 16) and the elements
 // [8u, 8u + 8) of every 32, as the unit's 16-byte pieces give them.  Sums go from fp32 (three units: six positions of a
 // lane, below 2^24 in units of 2^-10, so exact) to 32-bit integers over the 16 lanes (96 positions: below 2^29) and to
-// 64 bits beyond.
+// 64 bits beyond.  Bound by latency, one round of waves: 46 MB of keys (3 prompts of up to 30011 positions, 8 heads of 128,
+// pages of 96) in 14.3 us, 3.2 TB/s; the last pages of 64 requests in 4.3 us.
 template <int D, int W>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvfp4_kv_cache_t c,
                                                                          int8_t* __restrict__ codes,
@@ -155,7 +156,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvf
 // A workgroup takes some tokens of a request and one kv head: their rows in 8 bits into LDS as matrix operands, the
 // products of all of them with 16 pages at a time on the matrix unit (the rows are the first operand, so a lane holds one
 // page's products with four rows), a key per token and page (its score as an ordered integer) into LDS, and then a wave
-// per token, or with many pages the whole workgroup, takes the top_k largest keys.
+// per token takes the top_k largest keys.  Bound by the vector and scalar unit of the choice and by the chain of loads
+// before it: 1325 rows, 32/8 heads of 128, on 20000 and 60000 positions of pages of 64, top 32, 40 us; one row of 32/4
+// heads on 131072 positions, top 64, 12.4 us, of which the products of its 2048 pages are 4 and the choice 3.
 //
 // Rows of a 16-row block, so that the heads of a token meet in one lane, without exchange:
 //   several tokens: lane quarter q4 holds the rows 4*q4 + i; with HS = 4 these are heads 4*block + i of token q4 of the
@@ -601,7 +604,7 @@ int64_t kv_index_items(int32_t T, int32_t R, int32_t page_size) {
   return std::min((int64_t)T, T / page_size + 2 * requests);      // n rows lie in at most (n - 2) / page_size + 2 pages
 }
 
-// A wave per page and head where it has at most three units, else four.
+// A wave per page and head where it has at most three units, which it sums in one go, else four.
 moe_status_t launch_kv_index_update(const moe_nvfp4_kv_cache_t& c, const moe_nvfp4_kv_index_t& index, const KvStep& s,
                                     hipStream_t stream) {
   const int64_t items = kv_index_items(s.T, s.R, s.page_size);
