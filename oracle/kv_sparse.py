@@ -100,6 +100,14 @@ def attention(q, pages, page_size, k_gscale, v_gscale, offsets, lens, table, sel
     terms, plain, mag = np.zeros(q.shape), np.zeros(q.shape), np.zeros((tokens, heads))
     for r in range(len(lens)):
         a, n, length = _span(offsets, lens, r, tokens)
+        # the request's keys and values by position; pages that are not in the cache are never looked at
+        slots = np.zeros(length, np.int64)
+        for b in range(min(-(-length // page_size), table.shape[1])):
+            if 0 <= table[r, b] < pages.shape[0]:
+                at = np.arange(b * page_size, min((b + 1) * page_size, length))
+                slots[at] = int(table[r, b]) * page_size + at % page_size
+        keys = okv.decode(pages, page_size, slots, k_gscale, False)
+        values = okv.decode(pages, page_size, slots, v_gscale, True)
         for t in range(a, a + n):
             pos = length - n + t - a
             for kh in range(kv_heads):
@@ -109,10 +117,8 @@ def attention(q, pages, page_size, k_gscale, v_gscale, offsets, lens, table, sel
                     continue
                 if any(b >= table.shape[1] or not 0 <= table[r, b] < pages.shape[0] for b in seen):
                     continue
-                slots = np.concatenate([int(table[r, b]) * page_size + np.arange(min(page_size, pos + 1 - b * page_size))
-                                        for b in seen])
-                k = okv.decode(pages, page_size, slots, k_gscale, False)[:, kh]
-                v = okv.decode(pages, page_size, slots, v_gscale, True)[:, kh]
+                at = np.concatenate([np.arange(b * page_size, min((b + 1) * page_size, pos + 1)) for b in seen])
+                k, v = keys[at, kh], values[at, kh]
                 for h in range(kh * g, (kh + 1) * g):
                     s = scale * (k @ q[t, h])
                     m = s.max()
