@@ -193,6 +193,7 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
   // query operands
   f16x8 qf[MI][NS];
   float c[MI];
+  bool rare = false;      // a row of the wave has a far reference, or a query with an infinity or NaN
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const auto& w = raw[mi];
@@ -204,6 +205,7 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
     int e = (int)(top >> 7);    // the row's largest exponent field
     e = max(e, __shfl_xor(e, 16));
     e = max(e, __shfl_xor(e, 32));
+    rare |= __any(e == 255);
     const int shift = row_shift(e, a.scale * kLog2e);
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
 
   f32x4 o[MI][NS][2];
   float m[MI], l[MI];
-  bool far[MI], any_far = false;
+  bool far[MI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     far[mi] = false;
@@ -256,8 +258,8 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
           sc[mi][kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mi][k], sc[mi][kb], 0, 0, 0);
       }
     }
-    // a unit that every listed token sees whole: the other tokens' rows are hidden by their reference; else by positions,
-    // and nothing from positions past the length
+    // a unit that every listed token sees whole: the other tokens' rows are hidden by a reference of +inf, which leaves a
+    // NaN score a NaN (rare); else by positions, and nothing from positions past the length
     const bool inside = key0 + kKvUnit - 1 <= pos0 && !bad;
     bool hidden[MI];
 #pragma unroll
@@ -295,10 +297,10 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
         const float ref = hidden[mi] ? INFINITY : m[mi] - kPExp;
 #pragma unroll
         for (int k = 0; k < 8; ++k) t[k] = __fmaf_rn(sc[mi][k >> 2][k & 3], c[mi], -ref);
-        if (__builtin_expect(any_far, 0)) {
+        if (__builtin_expect(rare, 0)) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            t[k] = far[mi] && !hidden[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
+            t[k] = hidden[mi] ? -INFINITY : far[mi] ? __fmaf_rn(sc[mi][k >> 2][k & 3] - m[mi], c[mi], kPExp) : t[k];
         }
       };
       exponents();
@@ -309,7 +311,7 @@ __global__ __launch_bounds__(64 * NW, (D == 256 && MI == 2 ? 1 : 2)) void kv_spa
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx = fmaxf(mx, sc[mi][k >> 2][k & 3]);
         const float f = kv_move(hidden[mi] ? -INFINITY : quarter_max(mx), c[mi], m[mi], far[mi]);
-        any_far |= __any(far[mi]);
+        rare |= __any(far[mi]);
         l[mi] *= f;
 #pragma unroll
         for (int r = 0; r < NS; ++r)
