@@ -319,6 +319,8 @@ struct RotaryProblem {
   uint16_t* out;            // [T][heads][head_dim], out_stride elements per token; may be x
   int64_t out_stride;
 };
+bool rotary_launchable(const RotaryProblem& p);
+bool kv_append_rotary_launchable(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q);
 moe_status_t launch_rotary(const RotaryProblem& p, hipStream_t stream);
 moe_status_t launch_kv_append_rotary(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q, const uint16_t* k,
                                      const uint16_t* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,

@@ -55,8 +55,7 @@ bool valid_rotary(const moe_rotary_t* r) {
 // Rows [T][heads][dim] and the token stride that reaches them.
 bool valid_stride(int32_t T, int64_t stride, int64_t row) { return T <= 1 || (stride >= row && stride % 8 == 0); }
 
-// A launch of the rotary kernels holds fewer than 2^32 work-items: the rows one per 8 elements and up to 255 more per
-// token, of which there are at least 16 (32 and 2^35 for the append's three kinds together).
+// Elements of the rows; that a launch holds fewer than 2^32 work-items is seen from the launch itself.
 constexpr int64_t kMaxRotary = (int64_t)1 << 36, kMaxAppendRotary = (int64_t)1 << 35;
 
 bool valid_rotary_rows(const moe_rotary_t& r, int64_t x_stride, int32_t T, int32_t heads, int64_t position_stride,
@@ -215,8 +214,9 @@ moe_status_t moe_rotary(const moe_rotary_t* rotary, const uint16_t* x, int64_t x
   if (T == 0) return MOE_OK;
   if (!x || !positions || !out || !al16(x) || !al16(out) || !al4(positions)) return MOE_ERR_INVALID_ARGUMENT;
   if (x == out && T > 1 && x_stride != out_stride) return MOE_ERR_INVALID_ARGUMENT;
-  if (moe_status_t st = check_arch(nullptr)) return st;
   const moe::RotaryProblem p{*rotary, x, x_stride, T, heads, positions, position_stride, out, out_stride};
+  if (!moe::rotary_launchable(p)) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
   return moe::launch_rotary(p, static_cast<hipStream_t>(stream));
 }
 
@@ -237,8 +237,9 @@ moe_status_t moe_nvfp4_kv_append_rotary(const moe_nvfp4_kv_cache_t* cache, const
   if (!al16(q) || !al16(k) || !al16(v) || !al16(q_out) || !al4(positions) || !al4(slots))
     return MOE_ERR_INVALID_ARGUMENT;
   if (q == q_out && T > 1 && q_stride != q_out_stride) return MOE_ERR_INVALID_ARGUMENT;
-  if (moe_status_t st = check_arch(nullptr)) return st;
   const moe::RotaryProblem p{*rotary, q, q_stride, T, Hq, positions, position_stride, q_out, q_out_stride};
+  if (!moe::kv_append_rotary_launchable(*cache, p)) return MOE_ERR_INVALID_ARGUMENT;
+  if (moe_status_t st = check_arch(nullptr)) return st;
   return moe::launch_kv_append_rotary(*cache, p, k, v, k_stride, v_stride, slots, static_cast<hipStream_t>(stream));
 }
 

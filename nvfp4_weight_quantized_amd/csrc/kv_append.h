@@ -7,8 +7,6 @@
 namespace moe {
 namespace {
 
-constexpr long long kAppendQuadThreads = 1 << 19;      // rows * groups from which quads are taken (kv_cache.hip)
-
 __device__ __forceinline__ void load_group16(const uint16_t* __restrict__ row, float (&x)[16]) {
   const uint4* src = reinterpret_cast<const uint4*>(row);
 #pragma unroll

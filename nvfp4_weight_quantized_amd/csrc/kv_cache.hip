@@ -238,7 +238,7 @@ moe_status_t launch_kv_plan(const int32_t* kv_lens, const int32_t* new_lens, int
 moe_status_t launch_kv_append(const moe_nvfp4_kv_cache_t& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                               int64_t v_stride, const int32_t* slots, int32_t T, hipStream_t stream) {
   const long long per = 2LL * c.kv_heads * (c.head_dim / 16);
-  const bool quads = T * per >= kAppendQuadThreads;
+  const bool quads = T * per >= kKvAppendQuadThreads;
   const long long total = (quads ? (T + 3LL) / 4 : T) * per, blocks = (total + 255) / 256;
   with_head_dim(c.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;

@@ -8,11 +8,10 @@
 #pragma once
 
 #include "common.h"
+#include "rotary_launch.h"
 
 namespace moe {
 namespace {
-
-constexpr int kRotaryEntries = 1024;      // cosines and sines that a block holds in LDS, 8 KB
 
 // Entries are read four to a load by lanes that are 8 (or 4) entries apart; 16-byte pieces 256 bytes apart lie in the same
 // banks, so those of each next 256 bytes are exchanged among four.

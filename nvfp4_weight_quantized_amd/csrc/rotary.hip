@@ -5,12 +5,6 @@
 namespace moe {
 namespace {
 
-// Pieces of a head that one thread takes: a pair of chunks of eight elements (halves), or one chunk (neighbours, and
-// what lies behind the rotated elements).
-inline int rotary_pieces(const moe_rotary_t& r) {
-  return (r.interleaved ? r.pairs / 4 : r.pairs / 8) + (r.head_dim - 2 * r.pairs) / 8;
-}
-
 struct RotaryShape {
   int per_block;            // tokens
   Divider pieces, heads;
@@ -237,51 +231,46 @@ __global__ __launch_bounds__(256) void kv_append_rotary_kernel(moe_nvfp4_kv_cach
                       true, h, g, (int)wl * W, slots, q.T);
 }
 
-// Tokens per block: about `items` pieces of `per` a token, within what LDS holds of angles.
-int tokens_per_block(int64_t T, int pairs, int64_t per, int64_t items) {
-  const int64_t most = std::min((int64_t)kRotaryEntries / pairs, std::max((int64_t)1, items / per));
-  // small steps: a block per token until the card is full
-  return (int)std::max((int64_t)1, std::min(most, T / 1024));
+RotaryLaunch plan(const RotaryProblem& p) {
+  return plan_rotary(p.T, p.heads, p.r.head_dim, p.r.pairs, p.r.interleaved);
 }
 
-RotaryShape rotary_shape(const RotaryProblem& p) {
-  const int pieces = rotary_pieces(p.r);
-  return RotaryShape{tokens_per_block(p.T, p.r.pairs, (int64_t)p.heads * pieces, 2048), Divider::of(pieces),
-                     Divider::of(p.heads)};
+AppendRotaryLaunch plan(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q) {
+  return plan_append_rotary(q.T, q.heads, c.kv_heads, c.head_dim, q.r.pairs, q.r.interleaved);
 }
 
-unsigned blocks_for(int64_t T, int per_block) { return (unsigned)((T + per_block - 1) / per_block); }
+RotaryShape shape_of(const RotaryLaunch& x, int heads) {
+  return RotaryShape{x.per_block, Divider::of(x.pieces), Divider::of(heads)};
+}
 
 }  // namespace
 
+bool rotary_launchable(const RotaryProblem& p) { return rotary_fits(plan(p).blocks); }
+
+bool kv_append_rotary_launchable(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q) {
+  return rotary_fits(plan(c, q).blocks);
+}
+
 moe_status_t launch_rotary(const RotaryProblem& p, hipStream_t stream) {
-  const RotaryShape sh = rotary_shape(p);
-  hipLaunchKernelGGL(rotary_kernel, dim3(blocks_for(p.T, sh.per_block)), dim3(256), 0, stream, p, sh);
+  const RotaryLaunch x = plan(p);
+  hipLaunchKernelGGL(rotary_kernel, dim3((unsigned)x.blocks), dim3(kRotaryThreads), 0, stream, p, shape_of(x, p.heads));
   return launch_status();
 }
 
 moe_status_t launch_kv_append_rotary(const moe_nvfp4_kv_cache_t& c, const RotaryProblem& q, const uint16_t* k,
                                      const uint16_t* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
                                      hipStream_t stream) {
-  const int64_t per = (int64_t)c.kv_heads * (c.head_dim / 16), T = q.T;
-  const bool quads = 2 * T * per >= kAppendQuadThreads;
-  AppendRotaryBlocks b;
-  b.rows = rotary_shape(q);
-  const int64_t k_per = quads ? 2 * c.kv_heads : per;
-  b.k_per = Divider::of((uint32_t)k_per);
-  b.k_tokens = tokens_per_block(T, q.r.pairs, k_per, quads ? 256 : 512);
-  b.q = blocks_for(T, b.rows.per_block);
-  b.k = blocks_for(T, b.k_tokens);
-  b.v = (unsigned)(((quads ? (T + 3) / 4 : T) * per + 255) / 256);
-  for (unsigned* x : {&b.q, &b.k, &b.v}) *x = (*x + 7) / 8;
-  const dim3 grid(8 * (b.q + b.k + b.v));
+  const AppendRotaryLaunch x = plan(c, q);
+  const AppendRotaryBlocks b{shape_of(x.rows, q.heads), x.k_tokens,    Divider::of((uint32_t)x.k_per),
+                             (unsigned)x.q,             (unsigned)x.k, (unsigned)x.v};
+  const dim3 grid((unsigned)x.blocks), block(kRotaryThreads);
   with_head_dim(c.head_dim, [&](auto tag) {
     constexpr int D = decltype(tag)::value;
-    if (quads)
-      hipLaunchKernelGGL((kv_append_rotary_kernel<D, 4>), grid, dim3(256), 0, stream, c, q, k, v, k_stride, v_stride,
+    if (x.quads)
+      hipLaunchKernelGGL((kv_append_rotary_kernel<D, 4>), grid, block, 0, stream, c, q, k, v, k_stride, v_stride,
                          slots, b);
     else
-      hipLaunchKernelGGL((kv_append_rotary_kernel<D, 1>), grid, dim3(256), 0, stream, c, q, k, v, k_stride, v_stride,
+      hipLaunchKernelGGL((kv_append_rotary_kernel<D, 1>), grid, block, 0, stream, c, q, k, v, k_stride, v_stride,
                          slots, b);
   });
   return launch_status();

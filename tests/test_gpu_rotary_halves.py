@@ -24,5 +24,5 @@ pytestmark = pytest.mark.gpu
     (32, 1025, 1, 64, 64, 32, 1, False, 32, "run"),               # more half rows of a token than threads
 ])
 def test_long_steps_are_their_parts(seed, tokens, heads, kv_heads, dim, pairs, axes, interleaved, page, order):
-    assert 2 * tokens * kv_heads * (dim // 16) >= 1 << 19          # by the rule of csrc/rotary.hip
+    assert 2 * tokens * kv_heads * (dim // 16) >= 1 << 19          # by the rule of csrc/rotary_launch.h
     base.test_append_rotary_is_its_parts(seed, tokens, heads, kv_heads, dim, pairs, axes, interleaved, page, order)
