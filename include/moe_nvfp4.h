@@ -595,7 +595,8 @@ moe_status_t moe_nvfp4_kv_index_update(const moe_nvfp4_kv_cache_t* cache /* host
  *   score = max over the heads of fp32(fp32((x8 . codes) * a)) * scale, in fp32;
  * a row of a head with a value that is not finite or above 2^100, or with a < 2^-100, counts as zeros.  Pages whose table
  * entry is outside [0, num_pages) are not chosen by score; those of the last `last` that lie behind the table are listed
- * (the attention makes such rows NaN).  Rows of no request, and rows at negative positions, get -1 only.
+ * (the attention makes such rows NaN).  Rows of no request, and rows at negative positions, get -1 only.  The launch makes
+ * room for every column of the table, so a table no wider than the requests need is the fast one.
  * q as for moe_nvfp4_kv_attention.
  * Limits: 1 <= first + last <= top_k <= 1024, first >= 0, last >= 1; table_width <= 16384; T * kv_heads <= 2^21. */
 moe_status_t moe_nvfp4_kv_select(const moe_nvfp4_kv_index_t* index /* host */, const uint16_t* q, int64_t q_stride,

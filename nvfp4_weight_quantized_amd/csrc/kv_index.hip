@@ -47,8 +47,9 @@ __device__ __forceinline__ int row_sums(int (&v)[16]) {
 // W waves per touched page and head take every W-th unit.  A lane holds one position (of 16) and the elements
 // [8u, 8u + 8) of every 32, as the unit's 16-byte pieces give them.  Sums go from fp32 (three units: six positions of a
 // lane, below 2^24 in units of 2^-10, so exact) to 32-bit integers over the 16 lanes (96 positions: below 2^29) and to
-// 64 bits beyond.  Bound by latency, one round of waves: 46 MB of keys (3 prompts of up to 30011 positions, 8 heads of 128,
-// pages of 96) in 14.3 us, 3.2 TB/s; the last pages of 64 requests in 4.3 us.
+// 64 bits beyond.  46 MB of keys (3 prompts of up to 30011 positions, 8 heads of 128, pages of 96) in 14.3 us, 3.2 TB/s: a
+// wave looks, loads, sums and stores once, and all of them do so together, so the memory idles while they sum.  The last
+// pages of 64 requests in 4.3 us, a chain of loads.
 template <int D, int W>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvfp4_kv_cache_t c,
                                                                          int8_t* __restrict__ codes,
@@ -156,9 +157,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void kv_index_kernel(moe_nvf
 // A workgroup takes some tokens of a request and one kv head: their rows in 8 bits into LDS as matrix operands, the
 // products of all of them with 16 pages at a time on the matrix unit (the rows are the first operand, so a lane holds one
 // page's products with four rows), a key per token and page (its score as an ordered integer) into LDS, and then a wave
-// per token takes the top_k largest keys.  Bound by the vector and scalar unit of the choice and by the chain of loads
-// before it: 1325 rows, 32/8 heads of 128, on 20000 and 60000 positions of pages of 64, top 32, 40 us; one row of 32/4
-// heads on 131072 positions, top 64, 12.4 us, of which the products of its 2048 pages are 4 and the choice 3.
+// per token takes the top_k largest keys.  Chunks of 1024 and 748 rows, 32/8 heads of 128, on 44726 and 60000 positions of
+// pages of 64, top 32, 40 us, the vector unit 50% busy (the choice), the matrix unit 5%: a wave's choice is one chain of
+// ballots and counts.  One row of 32/4 heads on 131072 positions, top 64, 12.6 us on four compute units, of which the
+// products of its 2048 pages are 4 and the choice 3; 64 rows of requests of their own on up to 16000, 32/8 heads, 12.7 us.
 //
 // Rows of a 16-row block, so that the heads of a token meet in one lane, without exchange:
 //   several tokens: lane quarter q4 holds the rows 4*q4 + i; with HS = 4 these are heads 4*block + i of token q4 of the
@@ -374,9 +376,9 @@ __device__ __forceinline__ void halve(uint32_t* lo, uint32_t hi, int want, int* 
 // largest maximum bounds the threshold from below: it leaves little more than `room` candidates (44 for 32 of many, 177 for
 // 128), found by halving over 1, 4 or 16 maxima per lane.  Their pages go to a list of `cap` places, in order, over which the threshold itself is found; where they are
 // more (many equal keys, most of the pages wanted), and where there are few pages, over all keys.  HELD: up to so many pages
-// the keys stay in registers (0: each pass reads them).  One token: 2048 (2048 pages, a row of 32/4 heads, top 64: 12.8
-// against 14.9 us); several: 1024, since 2048 cost a compute unit the third workgroup (chunks
-// of 1024 and 301 rows on 60000 and 20000 positions, 32/8 heads, top 32: 39.7 against 48.2 us).
+// the keys stay in registers (0: each pass reads them).  One token: 2048 (2048 pages, a row of 32/4 heads, top 64: 12.6
+// against 15.0 us); several: 1024, since 2048 cost a compute unit the third workgroup (chunks of 1024 and 748 rows on
+// 44726 and 60000 positions, 32/8 heads, top 32: 40.2 against 46.9 us).
 constexpr int kSelectWaves = 16, kManyWaves = 8;      // of a workgroup: one token, several tokens
 constexpr int held_pages(int HS) { return HS == kOne ? 2048 : 1024; }
 
@@ -567,8 +569,8 @@ __global__ __launch_bounds__(64 * (HS == kOne ? kSelectWaves : kManyWaves)) void
 }
 
 // LDS of a workgroup, and what fits: a compute unit holds 160 KB, three workgroups of several groups of tokens are wanted
-// on it (chunks of 1024 and 301 rows on 60000 and 20000 positions, 32/8 heads of 128, top 32: 39.2 us; two workgroups, with
-// another 16 pages per wave on their way, 47.6).
+// on it (chunks of 1024 and 748 rows on 44726 and 60000 positions, 32/8 heads of 128, top 32: 40.2 us; with LDS for two
+// 48.1).
 constexpr int kSelectLds = 150 << 10, kSelectThird = 52 << 10;
 
 size_t select_lds(const SelectShape& s, int32_t D, int waves) {
@@ -577,7 +579,11 @@ size_t select_lds(const SelectShape& s, int32_t D, int waves) {
 }
 
 // One token per workgroup where the step may be of single tokens (T <= R); otherwise as many groups of tokens as leave
-// 512 workgroups and fit, since all of them share what a workgroup reads of the index.
+// 512 workgroups and fit, since all of them share what a workgroup reads of the index.  The chunks above take two groups,
+// 40.2 us (one 51.3, a token per workgroup 218); 64 rows on 16000 positions one, 8.5 us (four 14.8, a token each 11.7).
+// The host knows the table's width, not the lengths, and makes room for keys of all its columns: the same chunks take 40
+// us up to 960 columns, 62 from 1025 on (the keys leave the registers, four tokens a workgroup), 144 at 4096 and 8192 (one
+// workgroup per compute unit) and 470 at 16384 (a token per workgroup); 64 single tokens 12.7 us up to 2048, 16.7 at 16384.
 int select_heads(const KvSelectProblem& p, SelectShape* s) {
   const int64_t T = p.step.T, R = p.step.R;
   const int D = p.index.head_dim, hkv = p.index.kv_heads;
@@ -604,7 +610,9 @@ int64_t kv_index_items(int32_t T, int32_t R, int32_t page_size) {
   return std::min((int64_t)T, T / page_size + 2 * requests);      // n rows lie in at most (n - 2) / page_size + 2 pages
 }
 
-// A wave per page and head where it has at most three units, which it sums in one go, else four.
+// A wave per page and head where it has at most three units, which it sums in one go, else four.  Other side in brackets:
+// the prompts of kv_index_kernel with pages of 32 21.5 [39.4] us, of 96 14.3 [20.6], of 128 18.4 [14.2], of 256 14.1 [14.2];
+// the last pages of 64 requests, of 64 4.3 [4.6], of 128 4.7 [5.2], of 256 5.3 [7.1].
 moe_status_t launch_kv_index_update(const moe_nvfp4_kv_cache_t& c, const moe_nvfp4_kv_index_t& index, const KvStep& s,
                                     hipStream_t stream) {
   const int64_t items = kv_index_items(s.T, s.R, s.page_size);

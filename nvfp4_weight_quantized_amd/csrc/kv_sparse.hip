@@ -28,9 +28,10 @@ struct SparseTiles {
 };
 
 // Bound by memory where each page is read by one tile: 64 requests on up to 16000 positions, 64/8 heads of dimension 128, 48
-// pages of 64 each (210 MB) 42.3 us, 5.0 TB/s, the rate of a copy, with loads that pass the caches by.  Bound by the
-// vector unit where tokens have lists of their own: 1325 rows, 32/8 heads, 24 pages each, 200 us, the vector unit 64% busy
-// with about 300 instructions per unit (172 of them turn codes into operands) beside 32 matrix instructions.
+// pages of 64 each (210 MB) 42.3 us, 5.0 TB/s, the rate of a copy, with loads that pass the caches by.  Where tokens have
+// lists of their own no unit is full: chunks of 1024 and 748 rows on 26185 and 30000 positions, 32/8 heads, 24 pages each,
+// 198 us, the vector unit 67% busy with about 360 instructions per unit (172 of them turn codes into operands) beside 32
+// matrix instructions, the matrix unit 23%.
 
 constexpr int kEntries = kKvMaxSelected;      // of a tile's lists
 
@@ -498,16 +499,21 @@ __global__ __launch_bounds__(256) void kv_sparse_join_kernel(KvSparseProblem p, 
 
 // The launch of a call, from its sizes.  Measured on random lists of which neighbouring tokens share about half, 32/8 heads
 // of dimension 128, pages of 64, top 24, contexts of 30000 unless said; other side in brackets.
-//   Tokens per tile: one while that makes at most kPlaces tiles, which then end sooner (64 tokens 23.3 [28.3] us; 17 requests
-//   of 2 to 5 tokens, 18/3 heads of 64, 10.1 [11.9]), else as many as the rows hold.
-//   Rows per tile: 32 with kWideRows rows over all heads, for groups of 4 heads or more (2048 tokens 228 [239] us, 1325 tokens
-//   of two requests 200 [208]; 512 tokens 70.0 [76.7], 512 of 64/4 heads 65.3 [72.2] with 16; 512 of 16/16 heads of 64
-//   48.9 [101], where every token looks into 31 other lists).
-//   Splits: few tiles with 48 units of dimension 128 or more (one token, top 32, 32/4 heads, 11.4 [17.4] us; top 64 13.4
-//   [27.6]; 8 tokens, top 32, 15.6 [18.2]; dimension 256, 16/2 heads, top 32, 15.2 [28.6]; but top 16 12.3 whole, and two
-//   launches).
-//   Waves: eight where the tiles alone leave places free and are not short (64 requests of 64/8 heads, top 48, 42.4 [47.7]
-//   us, 48 of them 43.9 [47.1]; the drafts 10.1 [11.0]; but 64 requests, top 16, 20.7 with four [23.1]).
+//   Tokens per tile: one while that makes at most kPlaces tiles, which then end sooner (64 tokens 24.1 [28.8] us; 17 requests
+//   of 5 tokens on 9000, 18/3 heads of 64, pages of 32, top 25, 10.0 [12.0]), else as many as the rows hold (256 tokens 46.8
+//   [64.3]; 2048 226 [460]).
+//   Rows per tile: 32 with kWideRows rows over all heads (2048 tokens 226 [241] us; the chunks of 1024 and 748 199 [210];
+//   512 tokens 70.9 [76.6], 512 of 64/4 heads 66.0 [71.9] with 16).  Either side may be the better one by a round of
+//   workgroups between 32768 and 45056 rows: 32 against 16 rows, 1024 tokens 127.8 / 128.7, 1152 147.9 / 142.8, 1280 151.1 /
+//   156.8, 1408 171.6 / 170.8, and of 64/8 heads 640 115.0 / 114.5, 704 130.5 / 125.6; from 49152 on 32 is no slower: 1536
+//   175.1 / 184.8, of 64/8 heads 768 133.6 / 135.4.  For groups of 4 heads or more: with fewer a token looks into many other
+//   lists (512 tokens of 16/8 heads of 64 46.9 [66.9]; 4096 of 16/8 heads 320 [318]), and a mask holds 16 tokens.
+//   Splits: few tiles with 48 units of dimension 128 or more (one token on 131072, 32/4 heads, top 32, 11.5 [17.4] us; top 64
+//   13.4 [28.6]; 8 tokens, top 32, 13.2 [18.5]; dimension 256, 16/2 heads, top 32, 15.3 [29.0]); top 16 stays whole, 12.0
+//   [10.7], and saves a launch.
+//   Waves: eight where the tiles alone leave places free and are not short (64 requests on up to 16000 of 64/8 heads, top 48,
+//   42.8 [47.3] us, 48 of them 38.8 [41.7]; 17 requests of 2 to 5 tokens, 18/3 heads of 64, 10.1 [10.9]; but 64 requests, top
+//   16, 21.1 with four [23.4]).
 constexpr int kPlaces = 512;      // workgroups of four waves
 constexpr int64_t kWideRows = 40000;
 

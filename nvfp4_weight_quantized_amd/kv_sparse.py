@@ -125,6 +125,9 @@ def kv_select(index: NvFp4KvIndex, q: torch.Tensor, query_offsets: torch.Tensor,
     A row chooses among the pages up to its own position: always the ``first`` first and the ``last`` last of them (its
     own among these), and of the others those with the highest products of the kv head's query rows with the pages' means,
     in 8-bit integers (include/moe_nvfp4.h), equal ones the lowest page first.  Rows of no request get -1 only.
+
+    The launch makes room for every column of ``block_table``, however short the requests: for steps of many rows a table of
+    1024 columns or fewer is the fast one, and one of 16384 takes several times as long.
     """
     x, dev = index._struct, index._dev
     t, heads, stride = _rows(q, "q", x.head_dim, dev)

@@ -1,5 +1,5 @@
-"""Sparse attention with query rows that hold NaN or infinities: such a row is NaN where it sees a position, zeros and
-lse = -inf where it sees none, and the rows beside it in a tile keep their bounds."""
+"""Sparse attention with query rows that hold NaN or infinities and whose scores are NaN: such a row is NaN where it sees a
+position, zeros and lse = -inf where it sees none, and the rows beside it in a tile keep their bounds."""
 
 import numpy as np
 import pytest
