@@ -5,6 +5,8 @@
 namespace moe {
 namespace {
 
+static_assert(kRotaryThreads == 256, "the kernels below");
+
 struct RotaryShape {
   int per_block;            // tokens
   Divider pieces, heads;
